@@ -359,6 +359,205 @@ kvq_status kvq_calibrate_head_scales(const void* x, int64_t num_tokens, int32_t 
                                      int32_t head_dim, int64_t stride, float qmax,
                                      float* scales_out, kvq_stream_t stream);
 
+/*
+ * kvq_plan_step -- one serving step's bookkeeping on the GPU: block tables,
+ * slot mapping, positions and query offsets from the requests' lengths, in one
+ * launch and without a copy to the host.  None of the source pages has a
+ * counterpart: it makes the slot_mapping that kvq_write_cache takes and the
+ * block_table that the decode reads.
+ *
+ * context_lens: device int32 [num_seqs], tokens already cached per request;
+ *   new_lens: device int32 [num_seqs], tokens it adds (0: none).  A length below
+ *   0, or one for which the block table is too narrow, is clamped and sets
+ *   KVQ_DEVERR_CONTEXT_RANGE.
+ * block_table: device int32 [num_seqs, max_blocks_per_seq], read and written:
+ *   entries below ceil(context_len / block_size) are the request's pages;
+ *   those from there up to ceil((context_len + new_len) / block_size) are set
+ *   to free blocks; later entries are left alone.
+ * free_blocks: device int32 [free_capacity], ids of unused blocks; free_range:
+ *   device int32 [2], {first, end}: entries first..end-1 may be taken, in that
+ *   order, request by request.  free_range_out: device int32 [2], {first + blocks
+ *   taken, end}.  When they run out (KVQ_DEVERR_FREE_BLOCKS) the pages left over
+ *   get the entry -1 and their tokens the slot -1; a range outside
+ *   [0, free_capacity] is cut to it and sets the same bit.  An id outside
+ *   [0, num_blocks) sets KVQ_DEVERR_BLOCK_RANGE and gives slot -1 (and the entry
+ *   -1 if it came from the free list).
+ * The new tokens are packed request by request:
+ * cu_new: device int32 [num_seqs + 1], cu_new[s] = new tokens of the requests
+ *   before s; cu_new[num_seqs] = their total (the cu_query of kvq_paged_prefill).
+ * positions: device int32 [max_tokens]; slot_mapping: device int64 [max_tokens]:
+ *   per packed token its position in its request and its slot; position 0 and
+ *   slot -1 (which kvq_write_cache skips) behind the last one.  16-byte aligned.
+ *   More new tokens than max_tokens: the first max_tokens are written and
+ *   KVQ_DEVERR_TOKENS is set.
+ * context_lens_out: device int32 [num_seqs], context_len + new_len.
+ * No output may overlap an input or another output (block_table, in and out,
+ * aside).  The inputs are not consumed: the same call again gives the same
+ * result.  max_blocks_per_seq * block_size <= 2^30, max_tokens < 2^31.
+ * num_seqs == 0 writes the padding, cu_new[0] and free_range_out.
+ */
+kvq_status kvq_plan_step(const int32_t* context_lens, const int32_t* new_lens, int32_t num_seqs,
+                         int32_t* block_table, int32_t max_blocks_per_seq, int32_t block_size,
+                         int32_t num_blocks, const int32_t* free_blocks, int32_t free_capacity,
+                         const int32_t* free_range, int64_t* slot_mapping, int32_t* positions,
+                         int64_t max_tokens, int32_t* context_lens_out, int32_t* cu_new,
+                         int32_t* free_range_out, kvq_stream_t stream);
+
+/* How rotary angles are stretched for contexts longer than trained on.  Pair i
+ * of r/2 turns by theta_i = base^(-2i/r) per position; n = original_len. */
+typedef enum {
+  KVQ_ROPE_NONE = 0,
+  KVQ_ROPE_LINEAR = 1, /* theta_i / factor                                       */
+  KVQ_ROPE_NTK = 2,    /* base * factor^(r/(r-2)) in place of base (r > 2)        */
+  KVQ_ROPE_YARN = 3,   /* theta_i (1 - g_i) + theta_i / factor g_i, g_i = clamp((i - a) /
+                          max(b - a, 0.001), 0, 1), a = max(floor(d(high)), 0),
+                          b = min(ceil(d(low)), r - 1),
+                          d(x) = r ln(n / (2 pi x)) / (2 ln base)                 */
+  KVQ_ROPE_BANDS = 4,  /* theta_i h_i + theta_i / factor (1 - h_i),
+                          h_i = clamp((n theta_i / (2 pi) - low) / (high - low), 0, 1) */
+} kvq_rope_kind;
+
+typedef struct {
+  int32_t kind;        /* kvq_rope_kind */
+  double factor;       /* > 0 (kinds other than NONE) */
+  double original_len; /* > 0 (YARN, BANDS) */
+  double low, high;    /* turns within original_len: 0 < low < high (YARN, BANDS) */
+  double amplitude;    /* multiplies cos and sin (1 for most; YARN's is 0.1 ln(factor) + 1) */
+} kvq_rope_scaling;
+
+/*
+ * kvq_rope_table -- cos and sin of rotary positions: table[p][i] =
+ * amplitude * (cos, sin)(p theta_i), for p in [0, num_positions), i in
+ * [0, rot_dim / 2).
+ * table: device fp32 [num_positions, rot_dim / 2, 2], 16-byte aligned.
+ * rot_dim: even, 2..256.  base > 1.  scaling: NULL for KVQ_ROPE_NONE with
+ * amplitude 1.
+ * The angle is reduced to a part of a turn in 64-bit integers, so entries are
+ * within 3e-7 of amplitude 1 at every position.  num_positions == 0 is a no-op.
+ */
+kvq_status kvq_rope_table(float* table, int64_t num_positions, int32_t rot_dim, double base,
+                          const kvq_rope_scaling* scaling, kvq_stream_t stream);
+
+/* A layer's norm and rotation of queries and keys. */
+typedef struct {
+  int32_t head_dim;     /* 64, 128 or 256 (64 or 128 with a cache) */
+  int32_t rot_dim;      /* first elements of a head that turn: 0 or a multiple of 16 up to head_dim */
+  int32_t interleaved;  /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1) */
+  float eps;            /* of the norms, >= 0 */
+  float weight_offset;  /* added to the norms' weights (0, or 1 for weights kept as w - 1) */
+  const void* q_weight; /* device bf16 [head_dim], 16-byte aligned, or NULL: no norm of the queries */
+  const void* k_weight; /* the same for the keys */
+  const float* table;   /* kvq_rope_table's, 16-byte aligned (unused with rot_dim 0) */
+  int64_t num_positions;
+} kvq_rope_desc;
+
+/*
+ * kvq_norm_rope -- norm of every head's query and key, with the rotation of
+ * their positions in the same pass.  None of the source pages has a counterpart:
+ * it is the step between a layer's projections and the cache write.
+ *   y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)   (over a head)
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)        (its pairs)
+ * in float32, rounded once to bf16.
+ *
+ * query: device bf16 [num_tokens, num_q_heads, head_dim], key: device bf16
+ *   [num_tokens, num_kv_heads, head_dim]; heads and elements contiguous, tokens
+ *   the given strides (elements) apart: each >= its heads * head_dim, a multiple
+ *   of 8.  All 16-byte aligned.  query_out, key_out likewise, with their strides.
+ *   An output may be its own input (same pointer and stride); it may not overlap
+ *   anything else.  num_q_heads or num_kv_heads may be 0 (its pointers unused).
+ * positions: device int32 [num_tokens].  One outside [0, num_positions) sets
+ *   KVQ_DEVERR_POSITION and leaves the token's outputs as they were.
+ */
+kvq_status kvq_norm_rope(const kvq_rope_desc* rope, void* query_out, int64_t query_out_stride,
+                         void* key_out, int64_t key_out_stride, const void* query,
+                         int64_t query_stride, const void* key, int64_t key_stride,
+                         const int32_t* positions, int64_t num_tokens, int32_t num_q_heads,
+                         int32_t num_kv_heads, kvq_stream_t stream);
+
+/*
+ * kvq_norm_rope_write -- kvq_norm_rope of the queries, and of the keys straight
+ * into the paged cache together with the values: the codes and metadata are
+ * those that kvq_norm_rope followed by kvq_write_cache store, without the keys'
+ * round trip through memory.
+ *
+ * cache, k_cache, v_cache, slot_mapping: as in kvq_write_cache (a slot < 0
+ *   leaves the token's key and value out; its query is written all the same).
+ * value: device bf16 [num_tokens, num_kv_heads, head_dim], as key.
+ * Other arguments as in kvq_norm_rope; a position outside the table writes
+ *   nothing of the token.  rope->head_dim must be the cache's.
+ */
+kvq_status kvq_norm_rope_write(const kvq_rope_desc* rope, const kvq_cache_desc* cache, void* k_cache,
+                               void* v_cache, void* query_out, int64_t query_out_stride,
+                               const void* query, int64_t query_stride, const void* key,
+                               int64_t key_stride, const void* value, int64_t value_stride,
+                               const int32_t* positions, const int64_t* slot_mapping,
+                               int64_t num_tokens, int32_t num_q_heads, kvq_stream_t stream);
+
+/*
+ * kvq_decode_window -- kvq_paged_decode_ex (new_key == NULL) or
+ * kvq_decode_append through a sliding window: the query of a sequence of
+ * context_len n, which sits at position n - 1, sees position t when
+ * t >= n - window or t < num_sinks (the first tokens, kept in view).
+ *
+ * window >= 1 (it counts the query's own token), num_sinks >= 0.
+ * Block-table entries of pages without a visible token are never read (pages
+ * behind the window may have been freed); tokens out of view in a page that is
+ * read do not touch the result, whatever their codes are.
+ * Everything else (workspace and its size, num_ctas, out, the new token's
+ * write) is that of kvq_paged_decode_ex / kvq_decode_append.
+ */
+kvq_status kvq_decode_window(const kvq_cache_desc* cache, void* k_cache, void* v_cache,
+                             const void* new_key, const void* new_value, int64_t key_stride,
+                             int64_t value_stride, void* out, const void* query, int32_t num_seqs,
+                             int32_t num_q_heads, const int32_t* block_table,
+                             int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             int32_t max_context_len, float sm_scale, int32_t window,
+                             int32_t num_sinks, int32_t num_ctas, void* workspace,
+                             size_t workspace_bytes, kvq_stream_t stream);
+
+/*
+ * kvq_paged_prefill -- attention of each sequence's new tokens to its paged,
+ * quantized context, which already holds them (issue #4025 'methods' item 3
+ * for the prompt phase; chunked prompts, drafted tokens under check, and single
+ * tokens alike).
+ *
+ * query, out: device bf16 [total_q, num_q_heads, head_dim], contiguous, 16-byte
+ *   aligned: the new tokens of all sequences, packed.
+ * cu_query: device int32 [num_seqs + 1], non-decreasing: sequence s has rows
+ *   cu_query[s] .. cu_query[s+1]-1, its last positions: with q of them and
+ *   context_lens[s] = n, row cu_query[s] + j sits at position p = n - q + j.
+ *   It sees position t when t <= p and (window == 0 or t > p - window or
+ *   t < num_sinks).  A row with p < 0 sees nothing: its output is 0 and
+ *   KVQ_DEVERR_CONTEXT_RANGE is set.  Rows of out outside
+ *   [cu_query[0], cu_query[num_seqs]) are left as they were.  Offsets outside
+ *   [0, total_q], decreasing ones, and a sequence of more than max_query_len
+ *   rows are cut and set KVQ_DEVERR_TOKENS.
+ * block_table, context_lens, max_context_len, sm_scale: as in kvq_paged_decode;
+ *   entries of pages without a token that some row sees are never read.
+ * window >= 0 (0: no limit), num_sinks >= 0.
+ * workspace: device memory of >= kvq_prefill_workspace_size(...) bytes, 16-byte
+ *   aligned (may be NULL when that is 0); its contents on entry do not matter.
+ *   Two calls that overlap on the GPU must not share one.
+ * Arithmetic: 16-bit operands in the tensor cores, float32 sums and softmax.
+ *   int8 and FP8 codes are exact in fp16; asymmetric rows are rounded to fp16
+ *   once dequantized ((code * scale + zero_point) [* sigma], saturated at 65504);
+ *   the query is rounded to fp16 as in kvq_paged_decode (KVQ_DEVERR_QUERY_RANGE);
+ *   probabilities are rounded to fp16.  The 16-bit cache uses bf16 throughout.
+ *   A value (V) that is not finite makes the rows that see it not finite; rows
+ *   that do not see it are unaffected.
+ */
+kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t num_seqs,
+                                      int32_t num_q_heads, int64_t total_q, int32_t max_query_len,
+                                      int32_t max_context_len, size_t* bytes);
+kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, const void* v_cache,
+                             void* out, const void* query, const int32_t* cu_query,
+                             int32_t num_seqs, int64_t total_q, int32_t max_query_len,
+                             int32_t num_q_heads, const int32_t* block_table,
+                             int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             int32_t max_context_len, float sm_scale, int32_t window,
+                             int32_t num_sinks, void* workspace, size_t workspace_bytes,
+                             kvq_stream_t stream);
+
 /* Device error word bits. */
 #define KVQ_DEVERR_SLOT_RANGE 1u  /* a slot id past num_blocks*block_size */
 #define KVQ_DEVERR_BLOCK_RANGE 2u /* a block-table entry outside [0, num_blocks) */
@@ -371,6 +570,11 @@ kvq_status kvq_calibrate_head_scales(const void* x, int64_t num_tokens, int32_t 
                                        fp16's range (65504) for the quantized formats,
                                        or an infinity or NaN; that row's output is not
                                        meaningful */
+#define KVQ_DEVERR_FREE_BLOCKS 128u /* kvq_plan_step: the free blocks ran out, or their
+                                       range lies outside the list */
+#define KVQ_DEVERR_TOKENS 256u      /* more new tokens than a call has room for, or query
+                                       offsets that do not fit it */
+#define KVQ_DEVERR_POSITION 512u    /* a position outside the rotation table */
 
 /*
  * kvq_debug_arm_wait_timeout -- test hook for the decode kernel's bounded

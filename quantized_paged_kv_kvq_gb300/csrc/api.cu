@@ -31,6 +31,44 @@ bool pairing_ok(int kf, int vf, bool kvarn) {
 }
 bool scaled(int f) { return !is_asym(f) && f != KVQ_FMT_BF16; }
 
+// A power of two from 8 to 128: a 16-token tile lies in one block, or in two
+// consecutive entries of the block table (8-token pages).
+bool supported_block_size(int bs) {
+  return bs == 8 || bs == 16 || bs == 32 || bs == 64 || bs == 128;
+}
+
+// A range of bytes; two that overlap (empty ones never do).
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
+}
+
+// Rows of `width` 16-bit elements, `stride` elements apart.
+struct Rows {
+  const void* p;
+  int64_t stride, width;
+};
+bool rows_ok(const Rows& r) {
+  return r.width == 0 || (r.p != nullptr && aligned(r.p, 16) && r.stride >= r.width && r.stride % 8 == 0);
+}
+// Whether two sets of n rows share a byte; exact for equal strides (slices of
+// one packed projection), else whether their address ranges overlap.
+bool rows_meet(const Rows& a, const Rows& b, int64_t n) {
+  if (a.width == 0 || b.width == 0 || n == 0) return false;
+  const Span sa = {a.p, static_cast<size_t>(((n - 1) * a.stride + a.width) * 2)};
+  const Span sb = {b.p, static_cast<size_t>(((n - 1) * b.stride + b.width) * 2)};
+  if (!overlap(sa, sb)) return false;
+  if (a.stride != b.stride || n == 1) return true;
+  const int64_t pitch = 2 * a.stride;
+  int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % pitch;
+  if (d < 0) d += pitch;
+  return d < 2 * a.width || d + 2 * b.width > pitch;
+}
+
 // Checks shared by write and decode on the cache description.
 kvq_status check_cache(const kvq_cache_desc* c) {
   if (c == nullptr) return KVQ_ERR_INVALID_ARGUMENT;
@@ -39,11 +77,7 @@ kvq_status check_cache(const kvq_cache_desc* c) {
     return KVQ_ERR_INVALID_ARGUMENT;
   if (c->flags & ~KVQ_FLAG_VARNORM_ROTATE) return KVQ_ERR_INVALID_ARGUMENT;
   if (c->head_dim != 64 && c->head_dim != 128) return KVQ_ERR_UNSUPPORTED;
-  // a power of two from 8 to 128: a 16-token tile lies in one block, or in two
-  // consecutive entries of the block table (8-token pages)
-  if (c->block_size != 8 && c->block_size != 16 && c->block_size != 32 && c->block_size != 64 &&
-      c->block_size != 128)
-    return KVQ_ERR_UNSUPPORTED;
+  if (!supported_block_size(c->block_size)) return KVQ_ERR_UNSUPPORTED;
   const bool kvarn = (c->flags & KVQ_FLAG_VARNORM_ROTATE) != 0;
   if (!pairing_ok(c->k_fmt, c->v_fmt, kvarn)) return KVQ_ERR_UNSUPPORTED;
   if (scaled(c->k_fmt) && !(c->k_scale > 0.0f && isfinite(c->k_scale)))
@@ -147,6 +181,91 @@ kvq_status decode_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q
                    sms, c->k_fmt == KVQ_FMT_BF16 ? 1 : 2);
   }
   *NC = nc;
+  return KVQ_OK;
+}
+
+// The turns (of 2^64) per position of every pair of a rotation; see
+// kvq_rope_kind for the formulas.
+void rope_turns(int rot_dim, double base, const kvq_rope_scaling& sc, RopeTurns* turns) {
+  const double two_pi = 6.283185307179586476925;
+  if (sc.kind == KVQ_ROPE_NTK) base *= pow(sc.factor, rot_dim / (rot_dim - 2.0));
+  double from = 0.0, to = 0.0;  // YARN's ramp
+  if (sc.kind == KVQ_ROPE_YARN) {
+    auto pair_of = [&](double n) {
+      return rot_dim * log(sc.original_len / (two_pi * n)) / (2.0 * log(base));
+    };
+    from = fmax(floor(pair_of(sc.high)), 0.0);
+    to = fmin(ceil(pair_of(sc.low)), rot_dim - 1.0);
+  }
+  for (int i = 0; i < kMaxRopePairs; ++i) {
+    turns->t[i] = 0;
+    if (i >= rot_dim / 2) continue;
+    double theta = pow(base, -2.0 * i / rot_dim);
+    if (sc.kind == KVQ_ROPE_LINEAR) theta /= sc.factor;
+    if (sc.kind == KVQ_ROPE_YARN) {
+      const double g = fmin(fmax((i - from) / fmax(to - from, 0.001), 0.0), 1.0);
+      theta = theta / sc.factor * g + theta * (1.0 - g);
+    }
+    if (sc.kind == KVQ_ROPE_BANDS) {
+      const double n = sc.original_len * theta / two_pi;
+      const double h = fmin(fmax((n - sc.low) / (sc.high - sc.low), 0.0), 1.0);
+      theta = theta / sc.factor * (1.0 - h) + theta * h;
+    }
+    double part = theta / two_pi;
+    part -= floor(part);  // whole turns change nothing
+    turns->t[i] = static_cast<unsigned long long>(ldexp(part, 64));  // part <= 1 - 2^-53: fits
+  }
+}
+
+// Checks shared by the norm and rotation calls; fills what they share of *a.
+kvq_status check_rope(const kvq_rope_desc* r, const int32_t* positions, int64_t num_tokens,
+                      int32_t num_q_heads, int32_t num_kv_heads, NormRopeArgs* a) {
+  if (r == nullptr || num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (r->head_dim < 1 || r->rot_dim < 0 || r->rot_dim > r->head_dim ||
+      (r->interleaved != 0 && r->interleaved != 1) || !(r->eps >= 0.0f) || !isfinite(r->eps) ||
+      !isfinite(r->weight_offset))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if ((r->head_dim != 64 && r->head_dim != 128 && r->head_dim != 256) || r->rot_dim % 16)
+    return KVQ_ERR_UNSUPPORTED;
+  if (!aligned(r->q_weight, 16) || !aligned(r->k_weight, 16)) return KVQ_ERR_INVALID_ARGUMENT;
+  if (r->rot_dim > 0) {
+    if (r->num_positions < 0) return KVQ_ERR_INVALID_ARGUMENT;
+    if (num_tokens > 0 && (!r->table || !aligned(r->table, 16) || !positions || !aligned(positions, 4)))
+      return KVQ_ERR_INVALID_ARGUMENT;
+  }
+  a->positions = positions;
+  a->table = r->table;
+  a->q_weight = static_cast<const uint16_t*>(r->q_weight);
+  a->k_weight = static_cast<const uint16_t*>(r->k_weight);
+  a->num_positions = r->num_positions;
+  a->num_tokens = num_tokens;
+  a->num_q_heads = num_q_heads;
+  a->num_kv_heads = num_kv_heads;
+  a->rot_dim = r->rot_dim;
+  a->interleaved = r->interleaved;
+  a->eps = r->eps;
+  a->weight_offset = r->weight_offset;
+  return KVQ_OK;
+}
+
+// Row tiles and key splits of a prefill launch.
+struct PrefillShape {
+  int tiles = 0;            // row tiles, of all sequences, that the batch may need
+  int splits = 1;
+  size_t partial_rows = 0;  // rows of partial results in the workspace
+  size_t workspace = 0;
+};
+kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
+                         int64_t total_q, int32_t max_query_len, int32_t max_context_len,
+                         PrefillShape* sh) {
+  kvq_status st = check_cache(c);
+  if (st != KVQ_OK) return st;
+  if (num_seqs < 0 || num_q_heads < 1 || total_q < 0 || max_query_len < 0 || max_context_len < 0)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_q_heads % c->num_kv_heads) return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_q_heads / c->num_kv_heads > 8) return KVQ_ERR_UNSUPPORTED;
+  if (total_q > INT32_MAX || max_context_len > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
   return KVQ_OK;
 }
 
@@ -274,7 +393,8 @@ kvq_status decode_call(const kvq_cache_desc* classes, int32_t num_classes,
                        const int32_t* block_table, int32_t max_blocks_per_seq,
                        const int32_t* context_lens, int32_t max_context_len, float sm_scale,
                        int32_t num_ctas, void* workspace, size_t workspace_bytes,
-                       const AppendRows& app, kvq_stream_t stream) {
+                       const AppendRows& app, kvq_stream_t stream, int32_t window = 0,
+                       int32_t num_sinks = 0) {
   const kvq_cache_desc* cache = classes;  // class 0: formats, heads, scales of every class
   int NC = 0;
   kvq_status st = decode_shape(cache, num_seqs, num_q_heads, max_context_len, num_ctas, &NC);
@@ -338,6 +458,8 @@ kvq_status decode_call(const kvq_cache_desc* classes, int32_t num_classes,
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.max_context_len = max_context_len;
   a.num_ctas = NC;
+  a.window = window;
+  a.sinks = num_sinks;
   a.qk_scale = sm_scale * kLog2e * (scaled(cache->k_fmt) ? cache->k_scale : 1.0f);
   a.v_scale = scaled(cache->v_fmt) ? cache->v_scale : 1.0f;
   a.qk_base = sm_scale * kLog2e;
@@ -465,6 +587,27 @@ kvq_status kvq_decode_mixed(const kvq_cache_desc* classes, int32_t num_classes,
                      stream);
 }
 
+kvq_status kvq_decode_window(const kvq_cache_desc* cache, void* k_cache, void* v_cache,
+                             const void* new_key, const void* new_value, int64_t key_stride,
+                             int64_t value_stride, void* out, const void* query, int32_t num_seqs,
+                             int32_t num_q_heads, const int32_t* block_table,
+                             int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             int32_t max_context_len, float sm_scale, int32_t window,
+                             int32_t num_sinks, int32_t num_ctas, void* workspace,
+                             size_t workspace_bytes, kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (window < 1 || num_sinks < 0) return KVQ_ERR_INVALID_ARGUMENT;
+  AppendRows app;
+  if (new_key != nullptr || new_value != nullptr) {
+    st = append_rows(cache, num_seqs, new_key, new_value, key_stride, value_stride, &app);
+    if (st != KVQ_OK) return st;
+  }
+  return decode_call(cache, 1, &k_cache, &v_cache, nullptr, out, query, num_seqs, num_q_heads,
+                     block_table, max_blocks_per_seq, context_lens, max_context_len, sm_scale,
+                     num_ctas, workspace, workspace_bytes, app, stream, window, num_sinks);
+}
+
 kvq_status kvq_paged_decode(const kvq_cache_desc* cache, const void* k_cache,
                             const void* v_cache, void* out, const void* query, int32_t num_seqs,
                             int32_t num_q_heads, const int32_t* block_table,
@@ -474,6 +617,259 @@ kvq_status kvq_paged_decode(const kvq_cache_desc* cache, const void* k_cache,
   return kvq_paged_decode_ex(cache, k_cache, v_cache, out, query, num_seqs, num_q_heads,
                              block_table, max_blocks_per_seq, context_lens, max_context_len,
                              sm_scale, 0, workspace, workspace_bytes, stream);
+}
+
+kvq_status kvq_plan_step(const int32_t* context_lens, const int32_t* new_lens, int32_t num_seqs,
+                         int32_t* block_table, int32_t max_blocks_per_seq, int32_t block_size,
+                         int32_t num_blocks, const int32_t* free_blocks, int32_t free_capacity,
+                         const int32_t* free_range, int64_t* slot_mapping, int32_t* positions,
+                         int64_t max_tokens, int32_t* context_lens_out, int32_t* cu_new,
+                         int32_t* free_range_out, kvq_stream_t stream) {
+  if (num_seqs < 0 || max_blocks_per_seq < 0 || block_size < 1 || num_blocks < 1 ||
+      free_capacity < 0 || max_tokens < 0)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!supported_block_size(block_size)) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > (1 << 30) || max_tokens > INT32_MAX)
+    return KVQ_ERR_UNSUPPORTED;
+  if (!free_range || !free_range_out || !cu_new) return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_seqs > 0 && (!context_lens || !new_lens || !context_lens_out ||
+                       (max_blocks_per_seq > 0 && !block_table)))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if ((free_capacity > 0 && !free_blocks) || (max_tokens > 0 && (!slot_mapping || !positions)))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  for (const void* p : {static_cast<const void*>(context_lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(block_table), static_cast<const void*>(free_blocks),
+                        static_cast<const void*>(free_range), static_cast<const void*>(context_lens_out),
+                        static_cast<const void*>(cu_new), static_cast<const void*>(free_range_out)})
+    if (!aligned(p, 4)) return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned(slot_mapping, 16) || !aligned(positions, 16)) return KVQ_ERR_INVALID_ARGUMENT;
+  // every CTA reads the inputs while others write: nothing written may be read
+  const size_t n = static_cast<size_t>(num_seqs), t = static_cast<size_t>(max_tokens);
+  const Span out[] = {{slot_mapping, 8 * t},
+                      {positions, 4 * t},
+                      {context_lens_out, 4 * n},
+                      {cu_new, 4 * n + 4},
+                      {free_range_out, 8},
+                      {block_table, 4 * n * static_cast<size_t>(max_blocks_per_seq)}};
+  const Span in[] = {{context_lens, 4 * n},
+                     {new_lens, 4 * n},
+                     {free_blocks, 4 * static_cast<size_t>(free_capacity)},
+                     {free_range, 8}};
+  for (int i = 0; i < 6; ++i) {
+    for (int j = i + 1; j < 6; ++j)
+      if (overlap(out[i], out[j])) return KVQ_ERR_INVALID_ARGUMENT;
+    for (const Span& x : in)
+      if (overlap(out[i], x)) return KVQ_ERR_INVALID_ARGUMENT;
+  }
+  PlanArgs a;
+  a.context_lens = context_lens;
+  a.new_lens = new_lens;
+  a.block_table = block_table;
+  a.free_blocks = free_blocks;
+  a.free_range = free_range;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.context_lens_out = context_lens_out;
+  a.cu_new = cu_new;
+  a.free_range_out = free_range_out;
+  a.max_tokens = max_tokens;
+  a.num_seqs = num_seqs;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.block_shift = __builtin_ctz(static_cast<unsigned>(block_size));
+  a.num_blocks = num_blocks;
+  a.free_capacity = free_capacity;
+  return launch_plan(a, stream) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_rope_table(float* table, int64_t num_positions, int32_t rot_dim, double base,
+                          const kvq_rope_scaling* scaling, kvq_stream_t stream) {
+  if (num_positions < 0 || rot_dim < 2 || rot_dim % 2 || !(base > 1.0) || !isfinite(base))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (rot_dim > 2 * kMaxRopePairs || num_positions > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+  const kvq_rope_scaling none = {KVQ_ROPE_NONE, 1.0, 1.0, 1.0, 2.0, 1.0};
+  const kvq_rope_scaling& sc = scaling ? *scaling : none;
+  if (sc.kind < KVQ_ROPE_NONE || sc.kind > KVQ_ROPE_BANDS || !isfinite(sc.amplitude))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (sc.kind != KVQ_ROPE_NONE && !(sc.factor > 0.0 && isfinite(sc.factor)))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (sc.kind == KVQ_ROPE_NTK && rot_dim == 2) return KVQ_ERR_INVALID_ARGUMENT;
+  if (sc.kind >= KVQ_ROPE_YARN &&
+      !(sc.original_len > 0.0 && isfinite(sc.original_len) && sc.low > 0.0 && sc.high > sc.low &&
+        isfinite(sc.high)))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  RopeTurns turns;
+  rope_turns(rot_dim, base, sc, &turns);
+  if (num_positions == 0) return KVQ_OK;
+  if (!table || !aligned(table, 16)) return KVQ_ERR_INVALID_ARGUMENT;
+  const cudaError_t e = launch_rope_table(table, num_positions, rot_dim / 2,
+                                          static_cast<float>(sc.amplitude), turns, stream);
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_norm_rope(const kvq_rope_desc* rope, void* query_out, int64_t query_out_stride,
+                         void* key_out, int64_t key_out_stride, const void* query,
+                         int64_t query_stride, const void* key, int64_t key_stride,
+                         const int32_t* positions, int64_t num_tokens, int32_t num_q_heads,
+                         int32_t num_kv_heads, kvq_stream_t stream) {
+  NormRopeArgs a = {};
+  kvq_status st = check_rope(rope, positions, num_tokens, num_q_heads, num_kv_heads, &a);
+  if (st != KVQ_OK || num_tokens == 0 || num_q_heads + num_kv_heads == 0) return st;
+  const int d = rope->head_dim;
+  const Rows rows[] = {{query, query_stride, num_q_heads * static_cast<int64_t>(d)},
+                       {key, key_stride, num_kv_heads * static_cast<int64_t>(d)},
+                       {query_out, query_out_stride, num_q_heads * static_cast<int64_t>(d)},
+                       {key_out, key_out_stride, num_kv_heads * static_cast<int64_t>(d)}};
+  for (const Rows& r : rows)
+    if (!rows_ok(r)) return KVQ_ERR_INVALID_ARGUMENT;
+  for (int o = 2; o < 4; ++o)  // outputs against inputs (in place allowed) and each other
+    for (int i = 0; i < o; ++i) {
+      const bool in_place = i == o - 2 && rows[i].p == rows[o].p && rows[i].stride == rows[o].stride;
+      if (!in_place && rows_meet(rows[o], rows[i], num_tokens)) return KVQ_ERR_INVALID_ARGUMENT;
+    }
+  a.query = static_cast<const uint16_t*>(query);
+  a.key = static_cast<const uint16_t*>(key);
+  a.query_out = static_cast<uint16_t*>(query_out);
+  a.key_out = static_cast<uint16_t*>(key_out);
+  a.query_stride = query_stride;
+  a.key_stride = key_stride;
+  a.query_out_stride = query_out_stride;
+  a.key_out_stride = key_out_stride;
+  const cudaError_t e = launch_norm_rope(a, d, stream);
+  if (e == cudaErrorNotSupported) return KVQ_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_norm_rope_write(const kvq_rope_desc* rope, const kvq_cache_desc* cache, void* k_cache,
+                               void* v_cache, void* query_out, int64_t query_out_stride,
+                               const void* query, int64_t query_stride, const void* key,
+                               int64_t key_stride, const void* value, int64_t value_stride,
+                               const int32_t* positions, const int64_t* slot_mapping,
+                               int64_t num_tokens, int32_t num_q_heads, kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  NormRopeArgs a = {};
+  st = check_rope(rope, positions, num_tokens, num_q_heads, cache->num_kv_heads, &a);
+  if (st != KVQ_OK) return st;
+  if (rope->head_dim != cache->head_dim) return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_tokens == 0) return KVQ_OK;
+  const int64_t d = cache->head_dim, row = cache->num_kv_heads * d;
+  if (!k_cache || !v_cache || !slot_mapping || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(slot_mapping, 8))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  const Rows rows[] = {{query, query_stride, num_q_heads * d}, {key, key_stride, row},
+                       {value, value_stride, row}, {query_out, query_out_stride, num_q_heads * d}};
+  for (const Rows& r : rows)
+    if (!rows_ok(r)) return KVQ_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < 3; ++i) {
+    const bool in_place = i == 0 && query == query_out && query_stride == query_out_stride;
+    if (!in_place && rows_meet(rows[3], rows[i], num_tokens)) return KVQ_ERR_INVALID_ARGUMENT;
+  }
+  a.query = static_cast<const uint16_t*>(query);
+  a.key = static_cast<const uint16_t*>(key);
+  a.value = static_cast<const uint16_t*>(value);
+  a.query_out = static_cast<uint16_t*>(query_out);
+  a.query_stride = query_stride;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.query_out_stride = query_out_stride;
+  a.slot_mapping = slot_mapping;
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.k_meta = static_cast<__half*>(cache->k_meta);
+  a.v_meta = static_cast<__half*>(cache->v_meta);
+  a.block_size = cache->block_size;
+  a.block_shift = __builtin_ctz(static_cast<unsigned>(cache->block_size));
+  a.num_blocks = cache->num_blocks;
+  volatile float one = 1.0f;  // 1/scale, one IEEE float32 division, as kvq_write_cache
+  a.k_inv = scaled(cache->k_fmt) ? one / cache->k_scale : 1.0f;
+  a.v_inv = scaled(cache->v_fmt) ? one / cache->v_scale : 1.0f;
+  a.k_head_scale = cache->k_head_scales;
+  a.v_head_scale = cache->v_head_scales;
+  a.signs = cache->signs;
+  a.cR = rotation_scale(cache->head_dim);
+  const cudaError_t e = launch_norm_rope_write(a, cache->head_dim, cache->k_fmt, cache->v_fmt,
+                                               (cache->flags & KVQ_FLAG_VARNORM_ROTATE) != 0, stream);
+  if (e == cudaErrorNotSupported) return KVQ_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t num_seqs,
+                                      int32_t num_q_heads, int64_t total_q, int32_t max_query_len,
+                                      int32_t max_context_len, size_t* bytes) {
+  if (bytes == nullptr) return KVQ_ERR_INVALID_ARGUMENT;
+  PrefillShape sh;
+  kvq_status st = prefill_shape(cache, num_seqs, num_q_heads, total_q, max_query_len,
+                                max_context_len, &sh);
+  if (st != KVQ_OK) return st;
+  *bytes = sh.workspace;
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, const void* v_cache,
+                             void* out, const void* query, const int32_t* cu_query,
+                             int32_t num_seqs, int64_t total_q, int32_t max_query_len,
+                             int32_t num_q_heads, const int32_t* block_table,
+                             int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             int32_t max_context_len, float sm_scale, int32_t window,
+                             int32_t num_sinks, void* workspace, size_t workspace_bytes,
+                             kvq_stream_t stream) {
+  PrefillShape sh;
+  kvq_status st = prefill_shape(cache, num_seqs, num_q_heads, total_q, max_query_len,
+                                max_context_len, &sh);
+  if (st != KVQ_OK) return st;
+  if (window < 0 || num_sinks < 0 || !isfinite(sm_scale)) return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_seqs == 0 || total_q == 0 || max_query_len == 0) return KVQ_OK;
+  if (!k_cache || !v_cache || !out || !query || !cu_query || !block_table || !context_lens)
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(query, 16) ||
+      !aligned(cu_query, 4) || !aligned(block_table, 4) || !aligned(context_lens, 4))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  const size_t rows = static_cast<size_t>(total_q) * num_q_heads * cache->head_dim * 2;
+  if (overlap({out, rows}, {query, rows})) return KVQ_ERR_INVALID_ARGUMENT;
+  if (max_blocks_per_seq < ceil_div(max_context_len, cache->block_size))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (sh.workspace > 0 && (workspace == nullptr || workspace_bytes < sh.workspace))
+    return KVQ_ERR_WORKSPACE;
+  if (sh.workspace > 0 && !aligned(workspace, 16)) return KVQ_ERR_INVALID_ARGUMENT;
+  PrefillArgs a;
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.k_meta = static_cast<const __half*>(cache->k_meta);
+  a.v_meta = static_cast<const __half*>(cache->v_meta);
+  a.k_fmt = cache->k_fmt;
+  a.v_fmt = cache->v_fmt;
+  a.kvarn = (cache->flags & KVQ_FLAG_VARNORM_ROTATE) != 0;
+  a.block_shift = __builtin_ctz(static_cast<unsigned>(cache->block_size));
+  a.num_blocks = cache->num_blocks;
+  a.query = static_cast<const uint16_t*>(query);
+  a.out = static_cast<uint16_t*>(out);
+  a.cu_query = cu_query;
+  a.block_table = block_table;
+  a.context_lens = context_lens;
+  a.signs = cache->signs;
+  a.k_head_scale = cache->k_head_scales;
+  a.v_head_scale = cache->v_head_scales;
+  a.k_scale = scaled(cache->k_fmt) ? cache->k_scale : 1.0f;
+  a.v_scale = scaled(cache->v_fmt) ? cache->v_scale : 1.0f;
+  a.sm_scale_log2 = sm_scale * kLog2e;
+  a.cR = rotation_scale(cache->head_dim);
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.gqa = num_q_heads / cache->num_kv_heads;
+  a.total_q = total_q;
+  a.max_query_len = max_query_len;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.max_context_len = max_context_len;
+  a.window = window;
+  a.sinks = num_sinks;
+  a.tiles = sh.tiles;
+  a.num_splits = sh.splits;
+  a.ws_out = static_cast<float*>(workspace);
+  a.ws_ml = sh.workspace ? a.ws_out + sh.partial_rows * cache->head_dim : nullptr;
+  const cudaError_t e = launch_prefill(a, cache->head_dim, stream);
+  if (e == cudaErrorNotSupported) return KVQ_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 kvq_status kvq_hadamard(void* x, int32_t dtype, int64_t rows, int32_t head_dim,
@@ -534,6 +930,8 @@ kvq_status kvq_get_device_error(kvq_stream_t stream, uint32_t* bits) {
   unsigned v = 0;
 #define KVQ_UNIT_TAKE(U) take_error_bits_##U,
   cudaError_t (*take[])(unsigned*) = {take_error_bits_write, take_error_bits_write_asym,
+                                      take_error_bits_plan, take_error_bits_norm_rope,
+                                      take_error_bits_norm_rope_asym, take_error_bits_prefill,
                                       KVQ_DECODE_UNITS(KVQ_UNIT_TAKE)};
 #undef KVQ_UNIT_TAKE
   for (auto f : take)

@@ -408,6 +408,36 @@ __device__ __forceinline__ uint32_t pack_op2(float lo, float hi) {
 constexpr int kPagesOne = 0;    // one pool, pages of 16 tokens or more
 constexpr int kPages8 = 1;      // one pool of 8-token pages
 constexpr int kPagesMixed = 2;  // a pool per page class, pages of 16 tokens or more
+// kvq_decode_window: one pool, a sliding window behind first tokens kept in view
+constexpr int kPagesWindow = 3;   // pages of 16 tokens or more
+constexpr int kPages8Window = 4;  // 8-token pages
+constexpr bool windowed(int pages) { return pages == kPagesWindow || pages == kPages8Window; }
+
+// The tiles of a sequence of n > 0 tokens that a decode reads, in order: all of
+// them, or with a window the `kept` first ones (tokens below min(sinks, lo)) and
+// then those from the one that holds lo = n - window on, `skip` tiles later.
+struct TileView {
+  int lo;     // first token of the window
+  int kept;   // leading tiles with kept tokens
+  int skip;   // tiles left out behind them
+  int tiles;  // tiles read
+};
+template <int PAGES>
+__device__ __forceinline__ TileView tile_view(const DecodeArgs& a, int n) {
+  TileView v{0, 0, 0, (n + 15) >> 4};
+  if constexpr (windowed(PAGES)) {
+    v.lo = max(n - a.window, 0);
+    v.kept = (min(a.sinks, v.lo) + 15) >> 4;
+    v.skip = max((v.lo >> 4) - v.kept, 0);
+    v.tiles -= v.skip;  // the last tile read is always the sequence's last
+  }
+  return v;
+}
+// First token of the t-th tile read.
+template <int PAGES>
+__device__ __forceinline__ int tile_token(const TileView& v, int t) {
+  return 16 * (windowed(PAGES) && t >= v.kept ? t + v.skip : t);
+}
 
 // The producer's position in the range.
 struct Cursor {
@@ -445,7 +475,8 @@ __device__ __forceinline__ int seq_class_of(const DecodeArgs& a, int s) {
 struct TileHeader {
   int s;       // sequence
   int t;       // 16-token tile index within the sequence
-  int valid;   // valid tokens in the tile (1..16)
+  int valid;   // valid tokens in the tile (1..16); with a window also, in bits 8-15, the
+               // tile's first tokens that are kept and, in bits 16-23, its first in the window
   int flags;   // bit 0: first tile of this CTA's segment of s; bit 1: last tile
   int ps;      // global index of the sequence's first tile
   int tiles;   // tiles of the sequence
@@ -470,9 +501,10 @@ __device__ __forceinline__ unsigned long long ld_relaxed_u64(const unsigned long
   return v;
 }
 
+template <int PAGES>
 __device__ __forceinline__ int seq_tiles(const DecodeArgs& a, int s) {
   const int ctx = a.context_lens[s];
-  return ctx <= 0 ? 0 : (min(ctx, a.max_context_len) + 15) >> 4;
+  return ctx <= 0 ? 0 : tile_view<PAGES>(a, min(ctx, a.max_context_len)).tiles;
 }
 
 // floor(n / d) for n >= 0, d > 0: a 32-bit division whenever both fit (the
@@ -708,11 +740,12 @@ __device__ __forceinline__ void merge_slots(const DecodeArgs& a, int s, const Se
 // to this range alone, so no other CTA reads the new row.  The warps walk the
 // sequences from the range's first one, 32 at a time (a lane per sequence,
 // prefix sum of tile counts, ballot of those that end inside the range).
-// MIXED: the row lands in the pool of the sequence's page class.
-template <int D, int KF, int VF, bool KVARN, bool MIXED>
+// With mixed pages the row lands in the pool of the sequence's page class.
+template <int D, int KF, int VF, bool KVARN, int PAGES>
 __device__ __forceinline__ void append_new_tokens(const DecodeArgs& a, long long R0, long long R1,
                                                int s0, long long ps0, int h, int lane) {
   constexpr int LPR = RowGeom<D>::LPR;
+  constexpr bool MIXED = PAGES == kPagesMixed;
   const int sub = lane % LPR;
   uint32_t sign_bits = 0;
   if constexpr (KVARN) {
@@ -733,7 +766,7 @@ __device__ __forceinline__ void append_new_tokens(const DecodeArgs& a, long long
     const int s = base + lane;
     const int cx = s < S ? a.context_lens[s] : 0;
     const int cc = cx <= 0 ? 0 : min(cx, a.max_context_len);
-    const long long v = (cc + 15) >> 4;
+    const long long v = cc == 0 ? 0 : tile_view<PAGES>(a, cc).tiles;
     long long incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -806,7 +839,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   const int m_off = v_off + C::align(hpc * C::V_HEAD);  // K metadata box, then V's
   const int vm_off = m_off + C::meta_room(hpc, C::KMF);
   // 8-token pages: a 16-token tile is two pages, loaded as two boxes each
-  constexpr bool split = PAGES == kPages8;
+  constexpr bool split = PAGES == kPages8 || PAGES == kPages8Window;
   constexpr bool mixed = PAGES == kPagesMixed;
   const uint32_t ring_end = C::STAGES * stage_bytes;
   const int qrb = q_rows_bytes(G, D);
@@ -862,7 +895,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
     }
   }
   for (int s = k; s < S; s += NC) {
-    if (seq_tiles(a, s) == 0) {
+    if (seq_tiles<PAGES>(a, s) == 0) {
       uint16_t* o = a.out + (static_cast<size_t>(s) * a.num_q_heads + static_cast<size_t>(h) * G) * D;
       for (int i = lane; i < G * D; i += 32) o[i] = 0;
     }
@@ -878,7 +911,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   long long R0 = 0, R1 = 0;
   if (S <= static_cast<int>(blockDim.x)) {  // one pass: a sequence per thread
     const int s = threadIdx.x;
-    const long long v = s < S ? seq_tiles(a, s) : 0;
+    const long long v = s < S ? seq_tiles<PAGES>(a, s) : 0;
     const long long pk = v > 0 ? (1ll << 40) | v : 0;  // (sequences with tokens, tiles)
     long long incl = pk;
 #pragma unroll
@@ -921,7 +954,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   } else {  // many sequences: total first, then a chunked scan up to the range start
     bw = 0;
     long long part = 0;
-    for (int s = threadIdx.x; s < S; s += blockDim.x) part += seq_tiles(a, s);
+    for (int s = threadIdx.x; s < S; s += blockDim.x) part += seq_tiles<PAGES>(a, s);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == 0) scratch[4 + warp] = part;
@@ -935,7 +968,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
     long long running = 0;
     for (int base = 0; base < S && running <= R0; base += blockDim.x) {
       const int s = base + threadIdx.x;
-      const long long v = s < S ? seq_tiles(a, s) : 0;
+      const long long v = s < S ? seq_tiles<PAGES>(a, s) : 0;
       long long incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -962,7 +995,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   const long long ps_first = scratch[2];
   prefetch_q(s_first);
   if (a.new_key != nullptr) {  // new-token append: codes stored before any tile is loaded
-    append_new_tokens<D, KF, VF, KVARN, mixed>(a, R0, R1, s_first, ps_first, h, lane);
+    append_new_tokens<D, KF, VF, KVARN, PAGES>(a, R0, R1, s_first, ps_first, h, lane);
     // the stores (generic proxy) before the tensor loads (async proxy) the
     // barrier below lets thread 0 issue
     asm volatile("fence.proxy.async.global;" ::: "memory");
@@ -986,16 +1019,34 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   // 8-token pages: block id of the cursor tile's second page (read ahead); kept
   // out of the cursor, whose copies stay as small as for the other page sizes
   int* const cur_blk2 = reinterpret_cast<int*>(scratch + 22);
-  auto block_of = [&](const Cursor& u) {  // block id of the cursor's tile (in its class's pool)
-    return a.block_table[static_cast<size_t>(u.s) * a.max_blocks_per_seq +
-                         ((16 * u.t) >> a.block_shift[mixed ? u.cls : 0])];
+  auto token_of = [&](const Cursor& u) {  // first token of the cursor's tile
+    if constexpr (windowed(PAGES)) return tile_token<PAGES>(tile_view<PAGES>(a, u.ctx), u.t);
+    return 16 * u.t;
   };
-  auto second_half = [&](const Cursor& u) {  // 8-token pages: tokens 8..15 of the tile exist
+  // 8-token pages: tokens 0..7 / 8..15 of the tile are to be read (they exist
+  // and, with a window, one of them is in view)
+  auto first_half = [&](const Cursor& u) {
+    if constexpr (split && windowed(PAGES)) {
+      const int tok = token_of(u), lo = max(u.ctx - a.window, 0);
+      return tok < a.sinks || tok + 8 > lo;
+    }
+    return true;
+  };
+  auto second_half = [&](const Cursor& u) {
+    if constexpr (split && windowed(PAGES)) {
+      const int tok = token_of(u) + 8, lo = max(u.ctx - a.window, 0);
+      return tok < u.ctx && (tok < a.sinks || tok + 8 > lo);
+    }
     return split && 16 * u.t + 8 < u.ctx;
+  };
+  auto block_of = [&](const Cursor& u) {  // block id of the cursor's tile (in its class's pool)
+    if (!first_half(u)) return 0;  // a page out of view: its entry is never read
+    return a.block_table[static_cast<size_t>(u.s) * a.max_blocks_per_seq +
+                         (token_of(u) >> a.block_shift[mixed ? u.cls : 0])];
   };
   auto block2_of = [&](const Cursor& u) {  // their page (entries past the context are never read)
     return second_half(u) ? a.block_table[static_cast<size_t>(u.s) * a.max_blocks_per_seq +
-                                          ((16 * u.t) >> a.block_shift[0]) + 1]
+                                          (token_of(u) >> a.block_shift[0]) + 1]
                           : 0;
   };
   auto find_next = [&](Cursor& u) {  // first sequence after u.s with tokens, if the range goes on
@@ -1017,7 +1068,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
     u.s = s_first;
     u.t = static_cast<int>(R0 - ps_first);
     u.ctx = min(a.context_lens[s_first], a.max_context_len);
-    u.tiles = (u.ctx + 15) >> 4;
+    u.tiles = tile_view<PAGES>(a, u.ctx).tiles;
     u.cls = mixed ? seq_class_of(a, u.s) : 0;
     u.lam = static_cast<int>(lam_first);
     u.blk = block_of(u);
@@ -1033,13 +1084,16 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
     TileHeader& hd = hdr[st];
     hd.s = u.s;
     hd.t = u.t;
-    hd.valid = min(16, u.ctx - 16 * u.t);
+    const int tok = token_of(u);
+    hd.valid = min(16, u.ctx - tok);
+    if constexpr (windowed(PAGES))
+      hd.valid |= (min(max(a.sinks - tok, 0), 16) << 8) |
+                  (min(max(max(u.ctx - a.window, 0) - tok, 0), 16) << 16);
     hd.flags = (u.i == 0 || u.t == 0 ? 1 : 0) | (u.i == n - 1 || u.t == u.tiles - 1 ? 2 : 0);
     hd.ps = static_cast<int>(u.ps);
     hd.tiles = u.tiles;
     hd.next_s = u.nx < S ? u.nx : -1;
     hd.lam = u.lam;
-    const int tok = 16 * u.t;
     int blk = u.blk;
     const int cl = mixed ? u.cls : 0;
     if (blk < 0 || blk >= a.num_blocks[cl]) {
@@ -1054,14 +1108,14 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
     } else if constexpr (split) {  // 8-token pages: the tile is two pages, each loaded as
       // per-head 8-row boxes (rows 0-7, then 8-15 of the head's [16][row] box)
       // and [head][field][8] metadata boxes (the second meta_half bytes on)
-      const bool two = second_half(u);
+      const bool one = first_half(u), two = second_half(u);
       int blk2 = *cur_blk2;
       if (two && (blk2 < 0 || blk2 >= a.num_blocks[0])) {
         raise_error(2u);
         blk2 = 0;
       }
-      mbar_arrive_expect(bar, two ? tile_bytes : tile_bytes / 2);
-      for (int hf = 0; hf < (two ? 2 : 1); ++hf) {
+      mbar_arrive_expect(bar, one && two ? tile_bytes : tile_bytes / 2);
+      for (int hf = one ? 0 : 1; hf < (two ? 2 : 1); ++hf) {
         const int b = hf ? blk2 : blk;
         for (int hh = 0; hh < hpc; ++hh) {
           tma_codes_head<C::KB>(sb + hh * C::K_HEAD + hf * 8 * C::KB, &maps.k[0], hg * hpc + hh, 0,
@@ -1106,7 +1160,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
       }
       u.s = u.nx;
       u.ctx = u.nx_ctx;
-      u.tiles = (u.ctx + 15) >> 4;
+      u.tiles = tile_view<PAGES>(a, u.ctx).tiles;
       if constexpr (mixed) u.cls = seq_class_of(a, u.s);
       find_next(u);
     }
@@ -1243,7 +1297,13 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
       for (int e = 0; e < E; ++e) Oa[e] = Ob[e] = 0.f;
       seg_t0 = hd.t;
     }
-    const int valid = hd.valid;
+    const int valid = windowed(PAGES) ? hd.valid & 0xFF : hd.valid;
+    // rows of the tile that the query sees
+    auto in_view = [&](int r) {
+      if constexpr (windowed(PAGES))
+        return r < valid && (r < ((hd.valid >> 8) & 0xFF) || r >= (hd.valid >> 16));
+      return r < valid;
+    };
 
     // ---- K rows (and K metadata) of the stage into registers
     uint32_t kw[2][C::KW];
@@ -1304,7 +1364,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
         sl[3] = (ks1 * (sacc[3] - qb1) + kz1 * qsum1) * a.qk_scale;
       }
     }
-    const bool ok0 = row0 < valid, ok1 = row1 < valid;
+    const bool ok0 = in_view(row0), ok1 = in_view(row1);
     if (!ok0) sl[0] = sl[1] = -INFINITY;
     if (!ok1) sl[2] = sl[3] = -INFINITY;
 
@@ -1347,10 +1407,10 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
 #pragma unroll
         for (int q = 0; q < C::VW; ++q) vw[u][q] ^= 0x80808080u;
     }
-    if (valid < 16) {
+    if (valid < 16 || (windowed(PAGES) && (hd.valid >> 16) != 0)) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (v_token(c, u) >= valid) {
+        if (!in_view(v_token(c, u))) {
 #pragma unroll
           for (int q = 0; q < C::VW; ++q) vw[u][q] = (VF == INT8) ? 0x80808080u : 0u;
         }

@@ -141,6 +141,8 @@ cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
   auto kern_one = decode_partition_kernel<D, KF, VF, KVARN, kPagesOne>;
   auto kern_split = decode_partition_kernel<D, KF, VF, KVARN, kPages8>;
   auto kern_mixed = decode_partition_kernel<D, KF, VF, KVARN, kPagesMixed>;
+  auto kern_window = decode_partition_kernel<D, KF, VF, KVARN, kPagesWindow>;
+  auto kern_split_window = decode_partition_kernel<D, KF, VF, KVARN, kPages8Window>;
   const int smem = decode_smem_bytes<C>(hpc, a.gqa);
   static std::atomic<unsigned long long> attr_done{0};  // one bit per device
   int dev = 0;
@@ -151,7 +153,9 @@ cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
     const int most = decode_smem_bytes<C>(kHeadsPerCta, 8);
     for (const void* k : {reinterpret_cast<const void*>(kern_one),
                           reinterpret_cast<const void*>(kern_split),
-                          reinterpret_cast<const void*>(kern_mixed)}) {
+                          reinterpret_cast<const void*>(kern_mixed),
+                          reinterpret_cast<const void*>(kern_window),
+                          reinterpret_cast<const void*>(kern_split_window)}) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
       if (e != cudaSuccess) return e;
     }
@@ -166,7 +170,11 @@ cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
     one.v[0] = maps.v[0];
     one.km[0] = maps.km[0];
     one.vm[0] = maps.vm[0];
-    if (a.block_shift[0] < 4)
+    if (a.window > 0 && a.block_shift[0] < 4)
+      kern_split_window<<<grid, hpc * 32, smem, st>>>(args, one);
+    else if (a.window > 0)
+      kern_window<<<grid, hpc * 32, smem, st>>>(args, one);
+    else if (a.block_shift[0] < 4)
       kern_split<<<grid, hpc * 32, smem, st>>>(args, one);
     else
       kern_one<<<grid, hpc * 32, smem, st>>>(args, one);

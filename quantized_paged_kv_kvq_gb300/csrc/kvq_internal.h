@@ -71,6 +71,8 @@ struct DecodeArgs {
   int max_blocks_per_seq;
   int max_context_len;
   int num_ctas;          // NC: stream-K ranges (CTAs per head group)
+  int window;            // kvq_decode_window: last tokens in view (0: every token)
+  int sinks;             // first tokens that stay in view
   float qk_scale;        // sm_scale * log2(e) [* k_scale for symmetric K]
   float v_scale;         // symmetric V: multiplies the output
   float qk_base;         // sm_scale * log2(e)
@@ -98,6 +100,120 @@ struct DecodeArgs {
   int withhold_cta;
   int withhold_tile;
 };
+
+// One step's plan (kvq_plan_step).
+struct PlanArgs {
+  const int32_t* context_lens;
+  const int32_t* new_lens;
+  int32_t* block_table;  // [S, max_blocks_per_seq]
+  const int32_t* free_blocks;
+  const int32_t* free_range;  // [2]: first usable entry, behind the last
+  int64_t* slot_mapping;      // [max_tokens]
+  int32_t* positions;         // [max_tokens]
+  int32_t* context_lens_out;
+  int32_t* cu_new;  // [S + 1]
+  int32_t* free_range_out;
+  long long max_tokens;
+  int num_seqs;
+  int max_blocks_per_seq;
+  int block_shift;
+  int num_blocks;
+  int free_capacity;
+};
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st);
+
+// Turns (of 2^64) that one position adds to each pair of a rotation.
+constexpr int kMaxRopePairs = 128;
+struct RopeTurns {
+  unsigned long long t[kMaxRopePairs];
+};
+cudaError_t launch_rope_table(float* table, int64_t num_positions, int pairs, float amplitude,
+                              const RopeTurns& turns, cudaStream_t st);
+
+// Norm and rotation (kvq_norm_rope), with the cache to store into
+// (kvq_norm_rope_write; the cache's fields as in WriteArgs).
+struct NormRopeArgs {
+  const uint16_t* query;  // bf16 bits
+  const uint16_t* key;
+  const uint16_t* value;
+  uint16_t* query_out;
+  uint16_t* key_out;
+  int64_t query_stride;  // elements between tokens
+  int64_t key_stride;
+  int64_t value_stride;
+  int64_t query_out_stride;
+  int64_t key_out_stride;
+  const int32_t* positions;
+  const float* table;  // [num_positions, rot_dim / 2, 2]
+  const uint16_t* q_weight;  // bf16 [head_dim] or nullptr: no norm
+  const uint16_t* k_weight;
+  int64_t num_positions;
+  int64_t num_tokens;
+  int num_q_heads;
+  int num_kv_heads;
+  int rot_dim;
+  int interleaved;
+  float eps;
+  float weight_offset;
+  int q_items, kv_items, items_per_token;  // warps per token (set by the launcher)
+  const int64_t* slot_mapping;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  __half* k_meta;
+  __half* v_meta;
+  int block_size;
+  int block_shift;
+  int num_blocks;
+  float k_inv;
+  float v_inv;
+  const float* k_head_scale;
+  const float* v_head_scale;
+  const int8_t* signs;
+  float cR;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int head_dim, cudaStream_t st);
+cudaError_t launch_norm_rope_write(const NormRopeArgs& a, int head_dim, int kf, int vf, bool kvarn,
+                                   cudaStream_t st);
+cudaError_t launch_norm_rope_write_asym(const NormRopeArgs& a, int head_dim, int kf, int vf, bool kvarn,
+                                        cudaStream_t st);
+
+// Attention of many new tokens per sequence (kvq_paged_prefill).
+struct PrefillArgs {
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const __half* k_meta;
+  const __half* v_meta;
+  int k_fmt, v_fmt;
+  int kvarn;
+  int block_shift;
+  int num_blocks;
+  const uint16_t* query;  // bf16 [total_q, Hq, D]
+  uint16_t* out;
+  const int32_t* cu_query;  // [S + 1]
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  const int8_t* signs;
+  const float* k_head_scale;
+  const float* v_head_scale;
+  float k_scale, v_scale;
+  float sm_scale_log2;  // sm_scale * log2(e)
+  float cR;
+  int num_seqs;
+  int num_q_heads;
+  int num_kv_heads;
+  int gqa;
+  int64_t total_q;
+  int max_query_len;
+  int max_blocks_per_seq;
+  int max_context_len;
+  int window;  // 0: every earlier token
+  int sinks;
+  int tiles;      // row tiles the launch has room for
+  int num_splits; // parts each row tile's keys are cut into
+  float* ws_out;  // [splits, tiles, Hkv, rows, D] partial outputs
+  float* ws_ml;   // [splits, tiles, Hkv, rows, 2]
+};
+cudaError_t launch_prefill(const PrefillArgs& a, int head_dim, cudaStream_t st);
 
 cudaError_t launch_write(const WriteArgs& a, int head_dim, int kf, int vf, bool kvarn,
                          cudaStream_t st);
@@ -129,6 +245,11 @@ KVQ_DECODE_UNITS(KVQ_DECLARE_UNIT)
 // read-and-clear of the write units' device error words
 cudaError_t take_error_bits_write(unsigned* bits);
 cudaError_t take_error_bits_write_asym(unsigned* bits);
+// and of the units of the serving step's other operators
+cudaError_t take_error_bits_plan(unsigned* bits);
+cudaError_t take_error_bits_norm_rope(unsigned* bits);
+cudaError_t take_error_bits_norm_rope_asym(unsigned* bits);
+cudaError_t take_error_bits_prefill(unsigned* bits);
 
 cudaError_t launch_hadamard(void* x, int dtype, int64_t rows, int head_dim, const int8_t* signs,
                             int inverse, float cR, cudaStream_t st);

@@ -29,6 +29,10 @@ DEVERR_COMBINE = 8
 DEVERR_TIMEOUT = 16
 DEVERR_CLASS_RANGE = 32
 DEVERR_QUERY_RANGE = 64
+DEVERR_FREE_BLOCKS = 128
+DEVERR_TOKENS = 256
+DEVERR_POSITION = 512
+ROPE_KIND = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 
 class KvqError(RuntimeError):
@@ -47,9 +51,25 @@ class _CacheDesc(ctypes.Structure):
                 ("k_head_scales", ctypes.c_void_p), ("v_head_scales", ctypes.c_void_p)]
 
 
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("num_positions", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I32, _I64, _F32, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_F64 = ctypes.c_double
 _DESC = ctypes.POINTER(_CacheDesc)
+_ROPE = ctypes.POINTER(_RopeDesc)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -68,6 +88,19 @@ SIGNATURES = {
                                 _I64, _I64, _P, _P, _I32, _I32, _P, _I32, _P, _I32, _F32, _I32,
                                 _P, _SZ, _P]),
     "kvq_paged_decode_static_capacity": (_SZ, []),
+    "kvq_plan_step": (_I32, [_P, _P, _I32, _P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _I64, _P,
+                             _P, _P, _P]),
+    "kvq_rope_table": (_I32, [_P, _I64, _I32, _F64, ctypes.POINTER(_RopeScaling), _P]),
+    "kvq_norm_rope": (_I32, [_ROPE, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I32,
+                             _P]),
+    "kvq_norm_rope_write": (_I32, [_ROPE, _DESC, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                   _P, _P, _I64, _I32, _P]),
+    "kvq_decode_window": (_I32, [_DESC, _P, _P, _P, _P, _I64, _I64, _P, _P, _I32, _I32, _P, _I32,
+                                 _P, _I32, _F32, _I32, _I32, _I32, _P, _SZ, _P]),
+    "kvq_prefill_workspace_size": (_I32, [_DESC, _I32, _I32, _I64, _I32, _I32,
+                                          ctypes.POINTER(_SZ)]),
+    "kvq_paged_prefill": (_I32, [_DESC, _P, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _P, _I32, _P,
+                                 _I32, _F32, _I32, _I32, _P, _SZ, _P]),
     "kvq_hadamard": (_I32, [_P, _I32, _I64, _I32, _P, _I32, _P]),
     "kvq_calibrate_scale": (_I32, [_P, _I64, _F32, _P, _P]),
     "kvq_calibrate_head_scales": (_I32, [_P, _I64, _I32, _I32, _I64, _F32, _P, _P]),
@@ -319,6 +352,221 @@ def kvq_paged_decode_static(cache: KVCache, query: torch.Tensor, out: torch.Tens
 
 def kvq_paged_decode_static_capacity() -> int:
     return int(load_library().kvq_paged_decode_static_capacity())
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(name: str, t: torch.Tensor, dtype: torch.dtype, shape, contiguous: bool = True) -> None:
+    """A CUDA tensor of the current device with this dtype and shape (None: any extent)."""
+    _need(t.is_cuda and t.device.index == torch.cuda.current_device(),
+          f"{name} must be on the current CUDA device")
+    _need(t.dtype == dtype, f"{name} must be {dtype}")
+    _need(t.dim() == len(shape) and all(e is None or e == n for e, n in zip(shape, t.shape)),
+          f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _need(not contiguous or t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _rows(name: str, t: torch.Tensor, shape) -> int:
+    """Checks bf16 [T, heads, D] rows with a free token stride; returns that stride."""
+    _tensor(name, t, torch.bfloat16, shape, contiguous=False)
+    heads, d = t.shape[1:]
+    _need(t.numel() == 0 or ((d == 1 or t.stride(2) == 1) and (heads == 1 or t.stride(1) == d)),
+          f"{name}: heads and elements must be contiguous")
+    # one token: any stride serves, and torch may report one that is too small
+    return t.stride(0) if t.shape[0] > 1 else (heads * d + 7) // 8 * 8
+
+
+def _workspace(workspace: Optional[torch.Tensor]) -> int:
+    if workspace is None:
+        return 0
+    _need(workspace.is_cuda and workspace.device.index == torch.cuda.current_device()
+          and workspace.is_contiguous(), "workspace must be contiguous, on the current CUDA device")
+    return workspace.numel() * workspace.element_size()
+
+
+def kvq_plan_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                  free_blocks: torch.Tensor, free_range: torch.Tensor, block_size: int,
+                  num_blocks: int, slot_mapping: torch.Tensor, positions: torch.Tensor,
+                  context_lens_out: torch.Tensor, cu_new: torch.Tensor,
+                  free_range_out: torch.Tensor, stream=None) -> None:
+    """Plan one serving step on the GPU: context_lens and new_lens (int32 [S]) give the
+    tokens cached and added; block_table (int32 [S, W]) gets the free blocks its new pages
+    need (free_blocks int32 [F], entries free_range[0]..free_range[1]-1), slot_mapping
+    (int64 [T]) and positions (int32 [T]) describe the packed new tokens (slot -1 behind
+    the last), context_lens_out (int32 [S]), cu_new (int32 [S+1]) and free_range_out
+    (int32 [2]) the state after the step."""
+    s, t = context_lens.numel(), slot_mapping.numel()
+    _tensor("context_lens", context_lens, torch.int32, (s,))
+    _tensor("new_lens", new_lens, torch.int32, (s,))
+    _tensor("block_table", block_table, torch.int32, (s, None))
+    _tensor("free_blocks", free_blocks, torch.int32, (None,))
+    _tensor("free_range", free_range, torch.int32, (2,))
+    _tensor("slot_mapping", slot_mapping, torch.int64, (t,))
+    _tensor("positions", positions, torch.int32, (t,))
+    _tensor("context_lens_out", context_lens_out, torch.int32, (s,))
+    _tensor("cu_new", cu_new, torch.int32, (s + 1,))
+    _tensor("free_range_out", free_range_out, torch.int32, (2,))
+    st = load_library().kvq_plan_step(
+        _ptr(context_lens), _ptr(new_lens), s, _ptr(block_table), block_table.shape[1], block_size,
+        num_blocks, _ptr(free_blocks), free_blocks.numel(), _ptr(free_range), _ptr(slot_mapping),
+        _ptr(positions), t, _ptr(context_lens_out), _ptr(cu_new), _ptr(free_range_out),
+        _stream(stream))
+    _check(st, "kvq_plan_step")
+
+
+@dataclass
+class RopeScaling:
+    """How a rotation table is stretched (kvq_rope_kind in include/kvq.h): kind "linear",
+    "ntk", "yarn" or "bands" by `factor`; original_len, low and high for the last two."""
+    kind: str
+    factor: float = 1.0
+    original_len: float = 1.0
+    low: float = 1.0
+    high: float = 2.0
+    amplitude: float = 1.0
+
+
+def kvq_rope_table(table: torch.Tensor, base: float, scaling: Optional[RopeScaling] = None,
+                   stream=None) -> torch.Tensor:
+    """table (fp32 [positions, rot_dim / 2, 2]) <- cos and sin of every position and pair."""
+    _tensor("table", table, torch.float32, (None, None, 2))
+    sc = None
+    if scaling is not None:
+        sc = ctypes.byref(_RopeScaling(ROPE_KIND[scaling.kind], scaling.factor,
+                                       scaling.original_len, scaling.low, scaling.high,
+                                       scaling.amplitude))
+    st = load_library().kvq_rope_table(_ptr(table), table.shape[0], 2 * table.shape[1], float(base),
+                                       sc, _stream(stream))
+    _check(st, "kvq_rope_table")
+    return table
+
+
+@dataclass
+class Rope:
+    """A layer's norm and rotation: table of kvq_rope_table (None: no rotation), pairs
+    (2i, 2i+1) if interleaved else (i, i + rot_dim/2), and the norms' weights (bf16
+    [head_dim], None: no norm)."""
+    table: Optional[torch.Tensor]
+    interleaved: bool = False
+    q_weight: Optional[torch.Tensor] = None
+    k_weight: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    weight_offset: float = 0.0
+
+    def desc(self, head_dim: int) -> _RopeDesc:
+        rot, count = 0, 0
+        if self.table is not None:
+            _tensor("table", self.table, torch.float32, (None, None, 2))
+            rot, count = 2 * self.table.shape[1], self.table.shape[0]
+        for name in ("q_weight", "k_weight"):
+            if getattr(self, name) is not None:
+                _tensor(name, getattr(self, name), torch.bfloat16, (head_dim,))
+        ptr = lambda t: None if t is None else t.data_ptr()
+        return _RopeDesc(head_dim, rot, int(self.interleaved), float(self.eps),
+                         float(self.weight_offset), ptr(self.q_weight), ptr(self.k_weight),
+                         ptr(self.table), count)
+
+
+def kvq_norm_rope(rope: Rope, query: torch.Tensor, key: torch.Tensor, positions: torch.Tensor,
+                  query_out: torch.Tensor, key_out: torch.Tensor, stream=None) -> None:
+    """query_out, key_out <- normalised and rotated query [T, Hq, D] and key [T, Hkv, D]
+    (bf16, token strides free; an output may be its own input)."""
+    t, hq, d = query.shape
+    hkv = key.shape[1]
+    qs, ks = _rows("query", query, (t, hq, d)), _rows("key", key, (t, hkv, d))
+    qos, kos = _rows("query_out", query_out, (t, hq, d)), _rows("key_out", key_out, (t, hkv, d))
+    _tensor("positions", positions, torch.int32, (t,))
+    r = rope.desc(d)
+    st = load_library().kvq_norm_rope(ctypes.byref(r), _ptr(query_out), qos, _ptr(key_out), kos,
+                                      _ptr(query), qs, _ptr(key), ks, _ptr(positions), t, hq, hkv,
+                                      _stream(stream))
+    _check(st, "kvq_norm_rope")
+
+
+def kvq_norm_rope_write(rope: Rope, cache: KVCache, query: torch.Tensor, key: torch.Tensor,
+                        value: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
+                        query_out: torch.Tensor, stream=None) -> torch.Tensor:
+    """kvq_norm_rope of the queries into query_out, and of the keys straight into the
+    cache, together with the values, at slot_mapping (int64 [T])."""
+    t, hq, d = query.shape
+    kv = (t, cache.num_kv_heads, cache.head_dim)
+    qs, qos = _rows("query", query, (t, hq, cache.head_dim)), _rows("query_out", query_out, (t, hq, d))
+    ks, vs = _rows("key", key, kv), _rows("value", value, kv)
+    _tensor("positions", positions, torch.int32, (t,))
+    _tensor("slot_mapping", slot_mapping, torch.int64, (t,))
+    r, c = rope.desc(d), cache.desc()
+    st = load_library().kvq_norm_rope_write(
+        ctypes.byref(r), ctypes.byref(c), _ptr(cache.k_cache), _ptr(cache.v_cache), _ptr(query_out),
+        qos, _ptr(query), qs, _ptr(key), ks, _ptr(value), vs, _ptr(positions), _ptr(slot_mapping),
+        t, hq, _stream(stream))
+    _check(st, "kvq_norm_rope_write")
+    return query_out
+
+
+def kvq_decode_window(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
+                      block_table: torch.Tensor, context_lens: torch.Tensor, max_context_len: int,
+                      sm_scale: float, window: int, num_sinks: int = 0,
+                      workspace: Optional[torch.Tensor] = None, num_ctas: int = 0,
+                      new_key: Optional[torch.Tensor] = None,
+                      new_value: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """kvq_paged_decode (or, with new_key / new_value, kvq_decode_append) of queries that
+    see the last `window` tokens of their context and its first num_sinks."""
+    s, hq, d = query.shape
+    _tensor("query", query, torch.bfloat16, (s, hq, cache.head_dim))
+    _tensor("out", out, torch.bfloat16, (s, hq, d))
+    _tensor("block_table", block_table, torch.int32, (s, None))
+    _tensor("context_lens", context_lens, torch.int32, (s,))
+    _need((new_key is None) == (new_value is None), "new_key and new_value come together")
+    ks = vs = 0
+    if new_key is not None:
+        kv = (s, cache.num_kv_heads, cache.head_dim)
+        ks, vs = _rows("new_key", new_key, kv), _rows("new_value", new_value, kv)
+    c = cache.desc()
+    st = load_library().kvq_decode_window(
+        ctypes.byref(c), _ptr(cache.k_cache), _ptr(cache.v_cache), _ptr(new_key), _ptr(new_value),
+        ks, vs, _ptr(out), _ptr(query), s, hq, _ptr(block_table), block_table.shape[1],
+        _ptr(context_lens), max_context_len, float(sm_scale), window, num_sinks, num_ctas,
+        _ptr(workspace), _workspace(workspace), _stream(stream))
+    _check(st, "kvq_decode_window")
+    return out
+
+
+def kvq_prefill_workspace_size(cache: KVCache, num_seqs: int, num_q_heads: int, total_q: int,
+                               max_query_len: int, max_context_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    c = cache.desc()
+    _check(load_library().kvq_prefill_workspace_size(ctypes.byref(c), num_seqs, num_q_heads,
+                                                     total_q, max_query_len, max_context_len,
+                                                     ctypes.byref(n)), "kvq_prefill_workspace_size")
+    return int(n.value)
+
+
+def kvq_paged_prefill(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
+                      cu_query: torch.Tensor, block_table: torch.Tensor,
+                      context_lens: torch.Tensor, max_query_len: int, max_context_len: int,
+                      sm_scale: float, window: int = 0, num_sinks: int = 0,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out <- attention of each sequence's new tokens (query: bf16 [total, Hq, D], packed;
+    rows cu_query[s]..cu_query[s+1]-1 are sequence s's last positions) to its cached context
+    of context_lens[s] tokens, causal, through `window` (0: no limit) and num_sinks."""
+    s = context_lens.numel()
+    n, hq, d = query.shape
+    _tensor("query", query, torch.bfloat16, (n, hq, cache.head_dim))
+    _tensor("out", out, torch.bfloat16, (n, hq, d))
+    _tensor("cu_query", cu_query, torch.int32, (s + 1,))
+    _tensor("block_table", block_table, torch.int32, (s, None))
+    _tensor("context_lens", context_lens, torch.int32, (s,))
+    c = cache.desc()
+    st = load_library().kvq_paged_prefill(
+        ctypes.byref(c), _ptr(cache.k_cache), _ptr(cache.v_cache), _ptr(out), _ptr(query),
+        _ptr(cu_query), s, n, max_query_len, hq, _ptr(block_table), block_table.shape[1],
+        _ptr(context_lens), max_context_len, float(sm_scale), window, num_sinks, _ptr(workspace),
+        _workspace(workspace), _stream(stream))
+    _check(st, "kvq_paged_prefill")
+    return out
 
 
 def kvq_hadamard(x: torch.Tensor, signs: Optional[torch.Tensor] = None, inverse: bool = False,

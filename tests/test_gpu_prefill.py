@@ -1,0 +1,215 @@
+"""kvq_paged_prefill against the oracle."""
+import numpy as np
+import pytest
+import torch
+
+from quantized_paged_kv_kvq_gb300 import kvq
+
+from step_testing import DEV, FORMATS, Paged, bits, check_close, garbage, ints, random_query
+
+pytestmark = pytest.mark.gpu
+
+
+def prefill(p, q, cu, window=0, sinks=0, sm=None, max_q=None, out=None):
+    out = torch.full_like(q, 7.0) if out is None else out
+    counts = np.diff(cu)
+    max_q = int(counts.max(initial=0)) if max_q is None else max_q
+    ws = garbage(kvq.kvq_prefill_workspace_size(p.cache, len(p.lens), q.shape[1], q.shape[0], max_q, p.max_len))
+    return kvq.kvq_paged_prefill(p.cache, q, out, ints(cu), p.block_table, p.context_lens, max_q, p.max_len,
+                                 p.d ** -0.5 if sm is None else sm, window, sinks, ws)
+
+
+def offsets(counts):
+    return np.concatenate([[0], np.cumsum(counts)])
+
+
+def check(fmt, lens, counts, hkv, g, d, bs, window=0, sinks=0, **kw):
+    lens, counts = np.asarray(lens), np.asarray(counts)
+    keep = None
+    if window:
+        keep = lambda s, t: counts[s] > 0 and (t > lens[s] - counts[s] - window or t < sinks)
+    p = Paged(fmt, lens, hkv, d, bs, seed=d + bs, keep=keep, **kw)
+    cu = offsets(counts)
+    q = random_query(int(cu[-1]), hkv * g, d)
+    ref, tol = p.expect(q, cu, d ** -0.5, window, sinks)
+    check_close(prefill(p, q, cu, window, sinks), ref, tol, fmt)
+    assert kvq.kvq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", sorted(FORMATS))
+@pytest.mark.parametrize("hkv,g,d,bs", [(2, 4, 128, 16), (2, 3, 64, 8), (1, 8, 128, 128), (4, 1, 64, 32)])
+def test_ragged_batches(fmt, hkv, g, d, bs):
+    # prompts from nothing, chunks behind cached tokens, single tokens, no tokens
+    check(fmt, [40, 130, 1, 300, 200, 0, 129], [40, 7, 1, 1, 70, 0, 128], hkv, g, d, bs)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "kvarn", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (17, 0), (64, 5), (128, 130), (129, 4), (5000, 9)])
+def test_windows(fmt, window, sinks):
+    check(fmt, [300, 257, 33, 600], [300, 1, 33, 90], 2, 4, 128, 16, window, sinks)
+    check(fmt, [500, 18], [200, 9], 2, 2, 64, 8, window, sinks)
+
+
+@pytest.mark.parametrize("g", range(1, 9))
+def test_every_head_ratio(g):
+    check("int8", [150, 261], [35, 64], 2, g, 64, 16)
+
+
+@pytest.mark.parametrize("n,q", [(127, 127), (128, 128), (129, 129), (255, 32), (256, 33), (257, 64), (385, 63), (1, 1), (16, 16)])
+def test_tile_edges(n, q):
+    check("e4m3_int8", [n], [q], 1, 4, 128, 16)
+    check("bf16", [n], [q], 2, 8, 64, 64)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3_int8", "e5m2"])
+def test_head_scales(fmt):
+    check(fmt, [200, 50], [20, 50], 3, 2, 128, 16, head_scales=True)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "kvarn"])
+def test_long_contexts(fmt):
+    """Few rows and many keys (the keys are split), and many rows."""
+    check(fmt, [9000], [3], 1, 8, 128, 32)
+    check(fmt, [2500, 30], [1, 1], 2, 4, 64, 16)
+    check(fmt, [1500], [700], 1, 4, 128, 16)
+
+
+def test_large_logits():
+    """Keys whose logits span hundreds: the running maximum moves by more than any fixed range."""
+    check("bf16", [400], [130], 1, 4, 128, 16, k_std=20.0)
+    check("int8", [400, 1000], [130, 2], 1, 4, 128, 16)
+    p = Paged("bf16", [640], 1, 64, 16)
+    # keys that grow along the sequence, all in the queries' direction: a new maximum in every tile
+    q = torch.ones((300, 4, 64), dtype=torch.bfloat16, device=DEV)
+    k = torch.ones((640, 1, 64), device=DEV) * torch.linspace(-8, 8, 640, device=DEV)[:, None, None]
+    v = torch.randn((640, 1, 64), device=DEV).to(torch.bfloat16)
+    slots = ints([p.table[0, t // 16] * 16 + t % 16 for t in range(640)], torch.int64)
+    kvq.kvq_write_cache(p.cache, k.to(torch.bfloat16), v, slots)
+    for keys in (k, k.flip(0)):
+        kvq.kvq_write_cache(p.cache, keys.to(torch.bfloat16).contiguous(), v, slots)
+        ref, tol = p.expect(q, [0, 300], 1.0)
+        check_close(prefill(p, q, np.array([0, 300]), sm=1.0), ref, tol)
+        ref, tol = p.expect(q, [0, 300], -1.0)
+        check_close(prefill(p, q, np.array([0, 300]), sm=-1.0), ref, tol)
+
+
+def test_rows_outside_the_batch_stay():
+    p = Paged("int8", [50, 20], 2, 64, 16)
+    q = random_query(40, 4, 64)
+    cu = np.array([3, 13, 30])
+    out = torch.full_like(q, 7.0)
+    prefill(p, q, cu, out=out)
+    ref, tol = p.expect(q, cu, 0.125)
+    check_close(out[3:30], ref[3:30], tol[3:30])
+    assert (out[:3] == 7).all() and (out[30:] == 7).all()
+    assert kvq.kvq_get_device_error() == 0
+
+
+def test_more_rows_than_context():
+    """Rows before the first position see nothing: zero, and flagged."""
+    p = Paged("int8", [5, 40, 0], 2, 64, 16)
+    q = random_query(21, 4, 64)
+    cu = np.array([0, 9, 19, 21])
+    out = prefill(p, q, cu)
+    assert kvq.kvq_get_device_error() == kvq.DEVERR_CONTEXT_RANGE
+    ref, tol = p.expect(q, cu, 0.125)
+    assert (ref[:4] == 0).all()
+    check_close(out, ref, tol)
+    assert (out[:4] == 0).all() and (out[19:] == 0).all()
+
+
+def test_bad_offsets_are_flagged_and_cut():
+    p = Paged("int8", [50, 20], 2, 64, 16)
+    q = random_query(30, 4, 64)
+    for cu, max_q in (([0, 40, 50], 30), ([0, 10, 5], 20), ([-4, 10, 20], 20), ([0, 20, 30], 12)):
+        out = torch.full((40, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+        prefill(p, q, np.array(cu), max_q=max_q, out=out[:30])
+        assert kvq.kvq_get_device_error() & kvq.DEVERR_TOKENS
+        assert (out[30:] == 7).all()
+
+
+def test_bad_pages_and_queries_are_flagged():
+    p = Paged("int8", [50], 2, 64, 16)
+    p.block_table[0, 1] = -1
+    q = random_query(3, 4, 64)
+    out = prefill(p, q, np.array([0, 3]))
+    assert kvq.kvq_get_device_error() == kvq.DEVERR_BLOCK_RANGE and torch.isfinite(out).all()
+    p = Paged("int8", [50], 2, 64, 16)
+    q[1, 2, 3] = 1e30
+    out = prefill(p, q, np.array([0, 3]))
+    assert kvq.kvq_get_device_error() == kvq.DEVERR_QUERY_RANGE
+    ref, tol = p.expect(q[:1], [0, 1], 0.125)  # rows 0 and 2 are untouched by it
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2]).all()
+
+
+@pytest.mark.parametrize("fmt", ["e5m2", "bf16"])
+def test_values_not_finite(fmt):
+    """A value that is not finite reaches the rows that see it and no others."""
+    p = Paged(fmt, [100], 2, 64, 16)
+    b = p.table[0, 60 // 16]
+    if fmt == "bf16":
+        p.cache.v_cache.view(torch.bfloat16)[b, 60 % 16, 0, 5] = float("inf")
+        p.cache.v_cache.view(torch.bfloat16)[b, 60 % 16, 0, 9] = float("nan")
+    else:
+        p.cache.v_cache[b, 60 % 16, 0, 5] = 0x7C  # inf
+        p.cache.v_cache[b, 60 % 16, 0, 9] = 0x7F  # NaN
+    q = random_query(100, 4, 64)
+    out = prefill(p, q, np.array([0, 100]))
+    good = torch.isfinite(out)
+    assert good[:60].all() and good[:, 2:].all()
+    assert not good[60:, :2, 5].any() and not good[60:, :2, 9].any()
+    good[60:, :2, 5] = good[60:, :2, 9] = True
+    assert good.all()
+
+
+@pytest.mark.parametrize("fmt", ["e5m2", "bf16", "uint8"])
+def test_nan_where_no_row_looks(fmt):
+    """NaN beyond the context and between the kept tokens and the window."""
+    p = Paged(fmt, [200], 2, 64, 128)
+    for t in range(3, 90):
+        blk = p.table[0, t // 128]
+        p.cache.k_cache[blk, t % 128] = 0xFF
+        p.cache.v_cache[blk, t % 128] = 0xFF
+        if p.cache.k_meta is not None:
+            for m in (p.cache.k_meta, p.cache.v_meta):
+                m[blk, :, :, t % 128] = float("nan")
+    q = random_query(10, 4, 64)
+    ref, tol = p.expect(q, [0, 10], 0.125, 100, 3)
+    check_close(prefill(p, q, np.array([0, 10]), 100, 3), ref, tol)
+
+
+def test_rows_repeat_and_streams_and_graphs():
+    p = Paged("kvarn", [260, 1000], 2, 128, 16)
+    cu = np.array([0, 100, 103])
+    q = random_query(103, 8, 128)
+    one = prefill(p, q, cu)
+    assert torch.equal(bits(prefill(p, q, cu)), bits(one))  # no order of sums varies
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    n = kvq.kvq_prefill_workspace_size(p.cache, 2, 8, 103, 100, p.max_len)
+    ws, out, cut = garbage(n), torch.empty_like(q), ints(cu)
+    call = lambda: kvq.kvq_paged_prefill(p.cache, q, out, cut, p.block_table, p.context_lens, 100, p.max_len,
+                                         p.d ** -0.5, 0, 0, ws)
+    with torch.cuda.stream(s):
+        call()
+    s.synchronize()
+    assert torch.equal(bits(out), bits(one))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        call()
+    for i in range(3):
+        q.copy_(random_query(103, 8, 128, seed=30 + i))
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), bits(prefill(p, q, cu)))
+
+
+def test_matches_the_decode_for_single_tokens():
+    p = Paged("int8", [77, 300, 1], 4, 128, 16)
+    q = random_query(3, 16, 128)
+    out = torch.empty_like(q)
+    kvq.kvq_paged_decode(p.cache, q, out, p.block_table, p.context_lens, p.max_len, p.d ** -0.5, garbage(1 << 22))
+    ref, tol = p.expect(q, [0, 1, 2, 3], p.d ** -0.5)
+    check_close(out, ref, tol)
+    check_close(prefill(p, q, np.array([0, 1, 2, 3])), ref, tol)
