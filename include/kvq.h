@@ -540,7 +540,7 @@ kvq_status kvq_decode_window(const kvq_cache_desc* cache, void* k_cache, void* v
  *   Two calls that overlap on the GPU must not share one.
  * Arithmetic: 16-bit operands in the tensor cores, float32 sums and softmax.
  *   int8 and FP8 codes are exact in fp16; asymmetric rows are rounded to fp16
- *   once dequantized ((code * scale + zero_point) [* sigma], saturated at 65504);
+ *   once dequantized ((code * scale + zero_point) [* sigma]; past 65504 infinite);
  *   the query is rounded to fp16 as in kvq_paged_decode (KVQ_DEVERR_QUERY_RANGE);
  *   probabilities are rounded to fp16.  The 16-bit cache uses bf16 throughout.
  *   A value (V) that is not finite makes the rows that see it not finite; rows

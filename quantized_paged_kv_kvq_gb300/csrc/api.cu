@@ -4,6 +4,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <chrono>
 
@@ -251,6 +252,7 @@ kvq_status check_rope(const kvq_rope_desc* r, const int32_t* positions, int64_t 
 
 // Row tiles and key splits of a prefill launch.
 struct PrefillShape {
+  int rows = 128;           // rows of a tile
   int tiles = 0;            // row tiles, of all sequences, that the batch may need
   int splits = 1;
   size_t partial_rows = 0;  // rows of partial results in the workspace
@@ -266,6 +268,24 @@ kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
   if (num_q_heads % c->num_kv_heads) return KVQ_ERR_INVALID_ARGUMENT;
   if (num_q_heads / c->num_kv_heads > 8) return KVQ_ERR_UNSUPPORTED;
   if (total_q > INT32_MAX || max_context_len > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || total_q == 0 || max_query_len == 0) return KVQ_OK;
+  const int sms = sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  const int64_t g = num_q_heads / c->num_kv_heads, hkv = c->num_kv_heads;
+  sh->rows = max_query_len * g <= 128 ? 128 : 256;
+  // no more than every sequence at its longest, nor than the rows there are with
+  // a tile per sequence not full
+  const int64_t longest = (max_query_len * g + sh->rows - 1) / sh->rows;
+  const int64_t tiles = std::min(num_seqs * longest, total_q * g / sh->rows + num_seqs);
+  if (tiles * hkv > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+  sh->tiles = static_cast<int>(tiles);
+  // too few tiles for the SMs: cut the keys, into parts of two key tiles or more
+  const int64_t parts = std::min<int64_t>(sms / (tiles * hkv), (max_context_len + 255) / 256);
+  sh->splits = static_cast<int>(std::min<int64_t>(std::max<int64_t>(parts, 1), 64));
+  if (sh->splits > 1) {
+    sh->partial_rows = static_cast<size_t>(sh->splits) * tiles * hkv * sh->rows;
+    sh->workspace = sh->partial_rows * (c->head_dim + 2) * sizeof(float);
+  }
   return KVQ_OK;
 }
 
@@ -863,6 +883,7 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
   a.max_context_len = max_context_len;
   a.window = window;
   a.sinks = num_sinks;
+  a.rows_per_tile = sh.rows;
   a.tiles = sh.tiles;
   a.num_splits = sh.splits;
   a.ws_out = static_cast<float*>(workspace);

@@ -1,8 +1,34 @@
 // Attention of each sequence's new tokens to its paged, quantized context
-// (kvq_paged_prefill).  One warp per (token, query head), each lane D/32
-// consecutive elements; online softmax over the visible positions.
+// (kvq_paged_prefill).
+//
+// out = sum_t p_t v_t / sum_t p_t, p_t = 2^(z_t - m), z_t = sm_scale log2(e) <q, k_t>,
+// with a running maximum m over tiles of 128 keys and float32 sums: one pass over
+// the context, no score leaves the SM.
+//
+// Split: a CTA owns 128 or 256 rows (token, query head) of one sequence and
+// kv-head; row R of the sequence is query head R % G of new token R / G, so the
+// G heads that share keys fill a tile together.  Per 128 keys and 128 rows it
+// runs two tcgen05 products, S = Q K^T (operands in shared memory) and
+// O += P V (P in tensor memory, over S's own columns), S and O in tensor memory.
+// With 256 rows the second half's products run while the first half's softmax
+// does, and each key tile is dequantized once for both.
+//
+// Warps: one warpgroup per 128 rows for the softmax (a thread a row: no
+// shuffles), one warpgroup that loads and dequantizes K and V, one warp whose
+// first lane issues the products.  Loads: each producer thread copies 16-byte
+// pieces (cp.async) into a queue of its own, AHEAD tiles ahead, then turns its
+// pieces into 16-bit operands in the 128-byte swizzle that the products read:
+// codes become exact fp16 values with byte permutes onto 1024.0 or the native
+// fp8 conversion, asymmetric rows one fma more.  The 16-bit cache is copied
+// straight into place.
+//
+// Few rows over long contexts: the keys are cut into num_splits parts, whose
+// (m, sum, accumulators) a second kernel joins.
+#include <atomic>
+
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "tcgen05.cuh"
 
 namespace kvq {
 
@@ -10,127 +36,923 @@ KVQ_ERROR_ACCESSOR(take_error_bits_prefill)
 
 namespace {
 
-// Element e of a row (kv-head `h` of token offset `off` in block `blk`), dequantized.
-__device__ __forceinline__ float cached_value(const uint8_t* cache, const __half* meta, int fmt, int kvarn,
-                                              int d, int hkv, int bs, int blk, int off, int h, int e) {
-  const size_t row = ((static_cast<size_t>(blk) * bs + off) * hkv + h) * row_bytes(fmt, d);
-  if (fmt == BF16) return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(cache + row)[e]) << 16);
-  if (fmt == INT8) return static_cast<float>(reinterpret_cast<const int8_t*>(cache + row)[e]);
-  if (fmt == E4M3) {
-    const uint32_t h2 = e4m3x2_to_f16x2(cache[row + e]);
-    return __half2float(__ushort_as_half(static_cast<uint16_t>(h2 & 0xFFFFu)));
-  }
-  if (fmt == E5M2) return __half2float(__ushort_as_half(static_cast<uint16_t>(cache[row + e] << 8)));
-  const int code = fmt == INT4A ? (cache[row + e / 2] >> (4 * (e & 1))) & 15 : cache[row + e];
-  const __half* m = meta + (static_cast<size_t>(blk) * hkv + h) * (kvarn ? 3 : 2) * bs + off;
-  const float x = code * __half2float(m[0]) + __half2float(m[bs]);
-  return kvarn ? x * __half2float(m[2 * bs]) : x;
+constexpr int kKeys = 128;            // keys per tile
+constexpr int kSpin = 1 << 22;        // polls of an mbarrier before giving up
+constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is not raised: p <= 2^8
+
+template <int D_, int NW_>  // head_dim, softmax warpgroups
+struct Cfg {
+  static constexpr int D = D_, NW = NW_;
+  static constexpr int ROWS = 128 * NW;
+  static constexpr int THREADS = 128 * (NW + 2);
+  static constexpr int GROUPS = D / 64;              // 64-element column groups of an operand row
+  static constexpr int GROUP_BYTES = 128 * 128;      // 128 rows of 128 bytes
+  static constexpr int TILE = GROUPS * GROUP_BYTES;  // a 128-row operand
+  static constexpr int RAW = 128 * D;                // largest code tile that is dequantized
+  static constexpr int AHEAD = NW == 2 ? 2 : 3;      // K or V tiles a producer's loads run ahead
+  // shared memory: queries, K and V stages, raw queue, raw metadata, control
+  static constexpr int Q = 0;
+  static constexpr int K = Q + NW * TILE;
+  static constexpr int V = K + 2 * TILE;
+  static constexpr int RAWQ = V + 2 * TILE;
+  static constexpr int META = RAWQ + AHEAD * RAW;
+  static constexpr int CTRL = META + AHEAD * 3 * kKeys * 2;
+  static constexpr int SMEM = CTRL + 256 + 1024;
+  // tensor memory columns
+  static constexpr uint32_t S(int w) { return w * 128; }
+  static constexpr uint32_t O(int w) { return NW * 128 + w * 128; }
+  static constexpr uint32_t TMEM = NW == 2 ? 512 : 256;
+  // registers per thread of the softmax, producer and issuing warpgroups: together
+  // no more than the block is launched with (128 or 168 each)
+  static constexpr int R_SOFTMAX = NW == 2 ? 184 : 216;
+  static constexpr int R_PRODUCE = NW == 2 ? 96 : 160;
+  static constexpr int R_ISSUE = NW == 2 ? 48 : 120;
+};
+
+// Control words in shared memory.
+struct Ctrl {
+  unsigned long long q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drained;
+  uint32_t tmem;
+  int abort;
+  int seq, tile, q0, q, n;  // this CTA's rows
+  int scan[16];
+  int bad_lo, bad_hi;  // tiles with values that are not finite
+};
+
+static_assert(sizeof(Ctrl) <= 256, "control words");
+
+__device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return min(max(x, lo), hi); }
+
+// The rows of sequence s: first packed row and count, cut to fit.
+__device__ __forceinline__ int2 seq_rows(const PrefillArgs& a, int s, bool& bad) {
+  const int c0 = a.cu_query[s], c1 = a.cu_query[s + 1];
+  const int total = static_cast<int>(a.total_q);
+  const int q0 = clamp_int(c0, 0, total), q1 = clamp_int(c1, q0, total);
+  const int q = min(q1 - q0, a.max_query_len);
+  bad = c0 != q0 || c1 != q1 || q != q1 - q0;
+  return make_int2(q0, q);
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) prefill_kernel(const PrefillArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t t = item / a.num_q_heads;
-  const int hq = static_cast<int>(item - t * a.num_q_heads), h = hq / a.gqa;
-  if (t >= a.total_q) return;
-  // the sequence whose rows hold t
-  int s = -1, j = 0, q = 0;
-  for (int i = 0; i < a.num_seqs; ++i) {
-    const int c0 = a.cu_query[i], c1 = a.cu_query[i + 1];
-    if (c0 < 0 || c1 < c0 || c1 > a.total_q || c1 - c0 > a.max_query_len) {
-      raise_error(256u);
-      continue;
+// The sequence and row tile that tile number `want` (of all sequences, ROWS
+// rows each) is: a scan of the sequences' tile counts by the whole block.
+template <int ROWS>
+__device__ void find_tile(const PrefillArgs& a, Ctrl* c, int want) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  if (tid == 0) c->seq = -1;
+  int before = 0;  // tiles of the sequences before the chunk
+  unsigned err = 0;
+  for (int base = 0; base < a.num_seqs; base += blockDim.x) {
+    const int s = base + tid;
+    int2 r = make_int2(0, 0);
+    int v = 0;
+    if (s < a.num_seqs) {
+      bool bad;
+      r = seq_rows(a, s, bad);
+      if (bad) err |= 256u;  // KVQ_DEVERR_TOKENS
+      const long long rows = static_cast<long long>(r.y) * a.gqa;
+      v = static_cast<int>((rows + ROWS - 1) / ROWS);
+      const int n = a.context_lens[s];
+      if (n < 0 || n > a.max_context_len || clamp_int(n, 0, a.max_context_len) < r.y) err |= 4u;
     }
-    if (c0 <= t && t < c1) {
-      s = i;
-      j = static_cast<int>(t - c0);
-      q = c1 - c0;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) c->scan[warp] = incl;
+    __syncthreads();
+    int first = before, total = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) first += c->scan[w];
+      total += c->scan[w];
+    }
+    first += incl - v;
+    if (first <= want && want < first + v) {
+      c->seq = s;
+      c->tile = want - first;
+      c->q0 = r.x;
+      c->q = r.y;
+      c->n = clamp_int(a.context_lens[s], 0, a.max_context_len);
+    }
+    before += total;
+    __syncthreads();
+    if (before > want && blockIdx.x != 0) break;  // block 0 checks every sequence
+  }
+  if (err && blockIdx.x == 0) raise_error(err);
+}
+
+// What the rows [R0, R1) of a sequence see: positions p_lo..p_hi of their
+// tokens, and the key tiles, `kept` leading ones and then those from `skip`
+// tiles later on.
+struct Span {
+  int p_lo, p_hi;
+  int win;  // first position in the window of the first row (0 without a window)
+  int kept, skip, tiles;
+};
+__device__ __forceinline__ Span row_span(const PrefillArgs& a, int n, int q, int R0, int R1) {
+  Span s{0, -1, 0, 0, 0, 0};
+  s.p_lo = max(n - q + R0 / a.gqa, 0);
+  s.p_hi = n - q + (R1 - 1) / a.gqa;
+  if (s.p_hi < 0) return s;
+  s.tiles = s.p_hi / kKeys + 1;
+  if (a.window > 0) {
+    s.win = max(s.p_lo - a.window + 1, 0);
+    s.kept = (min(a.sinks, s.win) + kKeys - 1) / kKeys;
+    s.skip = max(s.win / kKeys - s.kept, 0);
+    s.tiles -= s.skip;
+  }
+  return s;
+}
+__device__ __forceinline__ int tile_key(const Span& s, int i) { return kKeys * (i < s.kept ? i : i + s.skip); }
+
+// 16 bytes of codes as 16-bit operands: 16 (8-bit codes) or 32 (int4) fp16
+// values, in order.  s, z: fp16 pairs of the row's scale and zero point, and g of
+// its deviation (rotated rows).
+template <int F, bool KVARN>
+__device__ __forceinline__ void dequantize16(const uint4& raw, uint32_t s, uint32_t z, uint32_t g,
+                                             uint32_t (&o)[F == INT4A ? 16 : 8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  constexpr uint32_t K64 = 0x64646464u;
+  auto affine = [&](uint32_t c) {  // fp16(c * s + z), then fp16(. * deviation)
+    const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&s),
+                              *reinterpret_cast<const __half2*>(&z));
+    const __half2 y = KVARN ? __hmul2(x, *reinterpret_cast<const __half2*>(&g)) : x;
+    return *reinterpret_cast<const uint32_t*>(&y);
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F == INT8) {
+      const uint32_t b = w[i] ^ 0x80808080u;
+      o[2 * i] = hsub2_u32(prmt(b, K64, 0x4140), 0x64806480u);
+      o[2 * i + 1] = hsub2_u32(prmt(b, K64, 0x4342), 0x64806480u);
+    } else if constexpr (F == E4M3) {
+      o[2 * i] = e4m3x2_to_f16x2(w[i] & 0xFFFFu);
+      o[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
+    } else if constexpr (F == E5M2) {
+      o[2 * i] = prmt(w[i], 0u, 0x1404);
+      o[2 * i + 1] = prmt(w[i], 0u, 0x3424);
+    } else if constexpr (F == UINT8A) {
+      o[2 * i] = affine(hsub2_u32(prmt(w[i], K64, 0x4140), 0x64006400u));
+      o[2 * i + 1] = affine(hsub2_u32(prmt(w[i], K64, 0x4342), 0x64006400u));
+    } else {  // INT4A: element 2i in the low nibble of byte i
+      const uint32_t lo = w[i] & 0x0F0F0F0Fu, hi = (w[i] >> 4) & 0x0F0F0F0Fu;
+      const uint32_t a = prmt(lo, hi, 0x5140), b = prmt(lo, hi, 0x7362);
+      o[4 * i] = affine(hsub2_u32(prmt(a, K64, 0x4140), 0x64006400u));
+      o[4 * i + 1] = affine(hsub2_u32(prmt(a, K64, 0x4342), 0x64006400u));
+      o[4 * i + 2] = affine(hsub2_u32(prmt(b, K64, 0x4140), 0x64006400u));
+      o[4 * i + 3] = affine(hsub2_u32(prmt(b, K64, 0x4342), 0x64006400u));
     }
   }
-  if (s < 0) return;
-  int n = a.context_lens[s];
-  if (n < 0 || n > a.max_context_len) {
-    raise_error(4u);
-    n = min(max(n, 0), a.max_context_len);
-  }
-  const int p = n - q + j;
-  if (p < 0) raise_error(4u);
-  float x[E], o[E];
-  const uint16_t* src = a.query + (t * a.num_q_heads + hq) * D + lane * E;
+}
+
+// Whether one of N pairs of 16-bit values is not finite.
+template <bool BF, int N>
+__device__ __forceinline__ bool any_not_finite(const uint32_t (&o)[N]) {
+  uint32_t acc = 0;  // 0 times a finite value is 0, times any other NaN
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    x[e] = __uint_as_float(static_cast<uint32_t>(src[e]) << 16);
-    if (a.kvarn && a.signs != nullptr && a.signs[lane * E + e] < 0) x[e] = -x[e];
-    o[e] = 0.f;
+  for (int i = 0; i < N; ++i) {
+    if constexpr (BF) {
+      const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&o[i]), __nv_bfloat162(),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&acc));
+      acc = *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+      const __half2 zero = __half2half2(__ushort_as_half(0));
+      const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&o[i]), zero,
+                                *reinterpret_cast<const __half2*>(&acc));
+      acc = *reinterpret_cast<const uint32_t*>(&r);
+    }
   }
-  if (a.kvarn) {
-    fwht_lanes<E, 32>(x, lane);
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] *= a.cR;
+  return (acc & 0x7FFF7FFFu) != 0;
+}
+template <bool BF>
+__device__ __forceinline__ bool finite16(uint32_t h) {
+  return BF ? (h & 0x7F80u) != 0x7F80u : (h & 0x7C00u) != 0x7C00u;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+  return (finite16<BF>(w) ? w & 0xFFFFu : 0u) | (finite16<BF>(w >> 16) ? w & 0xFFFF0000u : 0u);
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 ldsv4(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_pair(uint32_t a) {  // a 16-bit value, twice
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
+  return r | (static_cast<uint32_t>(r) << 16);
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool read) {
+  const int n = read ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+
+// Address of 16-byte chunk q of row `row` in an operand tile.
+__device__ __forceinline__ uint32_t chunk_addr(uint32_t tile, int row, int q) {
+  return tile + (q >> 3) * (128 * 128) + row * 128 + (((q & 7) ^ (row & 7)) << 4);
+}
+
+// One of the two caches, as the producers read it.
+struct Source {
+  const uint8_t* codes;  // of the kv-head
+  const __half* meta;    // of the kv-head, or nullptr
+  long long page_bytes, meta_page;  // codes of a block in bytes; metadata of a block in halves
+  int token_bytes;
+  int fmt, fields;
+  int chunk_bits;  // log2 of a row's 16-byte pieces
+};
+__device__ __forceinline__ Source make_source(const uint8_t* cache, const __half* meta, int fmt, int kvarn, int d,
+                                              int hkv, int h, int bs) {
+  Source s;
+  const int rb = row_bytes(fmt, d);
+  s.codes = cache + static_cast<size_t>(h) * rb;
+  s.token_bytes = hkv * rb;
+  s.page_bytes = static_cast<long long>(bs) * s.token_bytes;
+  s.fmt = fmt;
+  s.fields = is_asym(fmt) ? (kvarn ? 3 : 2) : 0;
+  s.meta = is_asym(fmt) ? meta + static_cast<size_t>(h) * s.fields * bs : nullptr;
+  s.meta_page = static_cast<long long>(hkv) * s.fields * bs;
+  s.chunk_bits = 31 - __clz(rb / 16);
+  return s;
+}
+
+// Barrier of the producer warpgroup; whether every warp came with `ok` (so that
+// all leave together, and none waits here for one that gave up).
+__device__ __forceinline__ bool producers_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.red.and.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return all != 0;
+}
+// The producer warpgroup's view of one key tile.
+struct KeyTile {
+  int t0;     // first key
+  int block;  // lane l: block id of the tile's l-th page
+};
+
+template <class C>
+struct Producer {
+  const PrefillArgs& a;
+  const Span& span;
+  uint32_t smem;
+  Ctrl* ctrl;
+  int tid;  // 0..127
+  int seq;
+
+  __device__ __forceinline__ bool needed(int t) const {
+    return t <= span.p_hi && (t >= span.win || t < a.sinks);
   }
-  if (a.k_fmt != BF16) {
+  // Block ids of tile i's pages, one per lane; pages that no row sees are not looked up.
+  __device__ __forceinline__ KeyTile look_up(int i) const {
+    KeyTile k;
+    k.t0 = tile_key(span, i);
+    k.block = 0;
+    const int lane = tid & 31, bs = 1 << a.block_shift;
+    const int t = k.t0 + lane * bs;
+    if (lane < (kKeys >> a.block_shift) && t <= span.p_hi && (t + bs > span.win || t < a.sinks)) {
+      k.block = a.block_table[static_cast<size_t>(seq) * a.max_blocks_per_seq + (t >> a.block_shift)];
+      if (k.block < 0 || k.block >= a.num_blocks) {
+        raise_error(2u);  // KVQ_DEVERR_BLOCK_RANGE: block 0 is read instead
+        k.block = 0;
+      }
+    }
+    return k;
+  }
+  // Start copying the tile's codes: 8-bit and 4-bit ones into slot `slot` of this
+  // thread's queue, 16-bit ones into the operand tile `dst`; and its metadata.
+  __device__ __forceinline__ void copy(const Source& s, const KeyTile& k, int slot, uint32_t dst) const {
+    const int chunk = tid & ((1 << s.chunk_bits) - 1), row0 = tid >> s.chunk_bits;
+    const int passes = 1 << s.chunk_bits, step = kKeys >> s.chunk_bits;
+    const int mask = (1 << a.block_shift) - 1;
+    const uint32_t raw = smem + C::RAWQ + slot * C::RAW + tid * 16;
+#pragma unroll 4
+    for (int i = 0; i < passes; ++i) {
+      const int row = row0 + i * step, t = k.t0 + row;
+      const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
+      const uint8_t* src = s.codes + blk * s.page_bytes + static_cast<long long>((t & mask) * s.token_bytes) + chunk * 16;
+      cp_async_or_zero<16>(s.fmt == BF16 ? chunk_addr(dst, row, chunk) : raw + i * 2048, src, needed(t));
+    }
+    if (s.fields > 0) {  // a pair of tokens per thread and field
+      const int row = 2 * (tid & 63), t = k.t0 + row;
+      const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
+      const __half* src = s.meta + blk * s.meta_page + (t & mask);
+      for (int f = tid >> 6; f < s.fields; f += 2)
+        cp_async_or_zero<4>(smem + C::META + (slot * 3 + f) * kKeys * 2 + row * 2, src + (f << a.block_shift),
+                            needed(t) || needed(t + 1));
+    }
+  }
+  // The pieces in slot `slot` as operands; values that are not finite (V) become
+  // 0 there and are noted.
+  template <int F, bool KVARN, bool IS_V>
+  __device__ __forceinline__ bool convert(const KeyTile& k, int slot, uint32_t dst) const {
+    constexpr int CHUNKS = row_bytes(F, C::D) / 16;  // pieces of a row, and passes
+    constexpr int OUT = F == INT4A ? 4 : 2;          // 16-byte operand chunks of a piece
+    const int chunk = tid % CHUNKS, row0 = tid / CHUNKS;
+    const uint32_t raw = smem + C::RAWQ + slot * C::RAW + tid * 16;
+    const uint32_t meta = smem + C::META + slot * 3 * kKeys * 2;
     bool bad = false;
+#pragma unroll 2
+    for (int i = 0; i < CHUNKS; ++i) {
+      const int row = row0 + i * (kKeys / CHUNKS);
+      const uint4 w = ldsv4(raw + i * 2048);
+      uint32_t s = 0, z = 0, g = 0;
+      if (is_asym(F) && needed(k.t0 + row)) {
+        s = lds_pair(meta + row * 2);
+        z = lds_pair(meta + kKeys * 2 + row * 2);
+        if (KVARN) g = lds_pair(meta + 2 * kKeys * 2 + row * 2);
+      }
+      uint32_t o[4 * OUT];
+      dequantize16<F, KVARN>(w, s, z, g, o);
+      if (IS_V && F != INT8 && any_not_finite<false>(o)) {
+        bad = true;
 #pragma unroll
-    for (int e = 0; e < E; ++e) bad |= !isfinite(__half2float(__float2half_rn(x[e])));
-    if (bad) raise_error(64u);
+        for (int e = 0; e < 4 * OUT; ++e) o[e] = finite_or_zero<false>(o[e]);
+      }
+      // the order in which a piece's chunks are stored differs between the lanes of
+      // a quarter-warp so that their 16-byte stores meet different banks
+      const int turn = C::GROUPS == 2 ? (F == INT4A ? 2 * (chunk >> 1) : (chunk * OUT) >> 3) : 0;
+#pragma unroll
+      for (int j = 0; j < OUT; ++j) {
+        const bool swap = turn != 0;
+        const int jj = j ^ (OUT == 4 ? 2 : 1);  // the chunk stored j-th where swapped
+        const int q = chunk * OUT + (swap ? jj : j);
+        sts128(chunk_addr(dst, row, q), swap ? o[4 * jj] : o[4 * j], swap ? o[4 * jj + 1] : o[4 * j + 1],
+               swap ? o[4 * jj + 2] : o[4 * j + 2], swap ? o[4 * jj + 3] : o[4 * j + 3]);
+      }
+    }
+    return bad;
   }
+  // 16-bit values are in place already; of V's those that are not finite become 0.
+  __device__ __forceinline__ bool check_bf16(uint32_t dst) const {
+    constexpr int CHUNKS = 2 * C::D / 16;
+    const int chunk = tid % CHUNKS, row0 = tid / CHUNKS;
+    bool bad = false;
+#pragma unroll 4
+    for (int i = 0; i < CHUNKS; ++i) {
+      const uint32_t at = chunk_addr(dst, row0 + i * (kKeys / CHUNKS), chunk);
+      const uint4 w = ldsv4(at);
+      const uint32_t o[4] = {w.x, w.y, w.z, w.w};
+      if (any_not_finite<true>(o)) {
+        bad = true;
+        sts128(at, finite_or_zero<true>(w.x), finite_or_zero<true>(w.y), finite_or_zero<true>(w.z),
+               finite_or_zero<true>(w.w));
+      }
+    }
+    return bad;
+  }
+  template <bool IS_V>
+  __device__ __forceinline__ bool finish(const Source& s, const KeyTile& k, int slot, uint32_t dst) const {
+    switch (s.fmt) {
+      case INT8: return convert<INT8, false, IS_V>(k, slot, dst);
+      case E4M3: return convert<E4M3, false, IS_V>(k, slot, dst);
+      case E5M2: return convert<E5M2, false, IS_V>(k, slot, dst);
+      case INT4A:
+        return s.fields == 3 ? convert<INT4A, true, IS_V>(k, slot, dst) : convert<INT4A, false, IS_V>(k, slot, dst);
+      case UINT8A:
+        return s.fields == 3 ? convert<UINT8A, true, IS_V>(k, slot, dst) : convert<UINT8A, false, IS_V>(k, slot, dst);
+      default: return IS_V ? check_bf16(dst) : false;
+    }
+  }
+};
+
+// x <- cR H x for a row held by one thread.
+template <int D>
+__device__ __forceinline__ void rotate_thread_row(float (&x)[D], float cR) {
+#pragma unroll
+  for (int h = 1; h < D; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      if ((i & h) == 0) {
+        const float u = x[i], v = x[i + h];
+        x[i] = u + v;
+        x[i + h] = u - v;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < D; ++i) x[i] *= cR;
+}
+
+__device__ __forceinline__ uint32_t pack16(bool bf, float lo, float hi) {
+  return bf ? pack_bf162(lo, hi) : pack_half2(lo, hi);
+}
+
+// Values that are not finite among those that the row at position p sees, per
+// dimension: bit d of hi for +inf, of lo for -inf, of both for NaN.  Only called
+// when the producers met one; reads the codes of tiles t_lo..t_hi again.
+template <class C>
+__device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& span, int seq, int h, int p, int i_lo,
+                                             int i_hi, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   const int bs = 1 << a.block_shift;
-  const float ks = a.k_head_scale ? a.k_head_scale[h] : a.k_scale;
-  const float vs = a.v_head_scale ? a.v_head_scale[h] : a.v_scale;
-  float m = -INFINITY, l = 0.f;
-  const int w0 = a.window > 0 ? max(p - a.window + 1, 0) : 0;
-  for (int k = 0; k <= p; ++k) {
-    if (k < w0 && k >= a.sinks) k = w0;
-    const int b = a.block_table[static_cast<size_t>(s) * a.max_blocks_per_seq + (k >> a.block_shift)];
-    int blk = b;
-    if (b < 0 || b >= a.num_blocks) {
-      raise_error(2u);
-      blk = 0;
+  const Source s = make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, C::D, a.num_kv_heads, h, bs);
+  for (int i = i_lo; i <= i_hi; ++i) {
+    const int t0 = tile_key(span, i);
+    for (int t = t0; t < t0 + kKeys && t <= p; ++t) {
+      if (a.window > 0 && t <= p - a.window && t >= a.sinks) continue;
+      int blk = a.block_table[static_cast<size_t>(seq) * a.max_blocks_per_seq + (t >> a.block_shift)];
+      if (blk < 0 || blk >= a.num_blocks) blk = 0;
+      const int off = t & (bs - 1);
+      const uint8_t* row = s.codes + blk * s.page_bytes + static_cast<long long>(off) * s.token_bytes;
+      __half sc{}, zp{}, sg{};
+      if (s.fields > 0) {
+        const __half* m = s.meta + blk * s.meta_page + off;
+        sc = m[0];
+        zp = m[bs];
+        if (s.fields == 3) sg = m[2 * bs];
+      }
+      for (int d = 0; d < C::D; ++d) {
+        uint32_t v;
+        if (s.fmt == BF16) {
+          v = reinterpret_cast<const uint16_t*>(row)[d];
+          if (finite16<true>(v)) continue;
+          v = (v & 0x7F) ? 0x7FFFu : (v & 0x8000u) | 0x7C00u;
+        } else if (s.fmt == E5M2) {
+          v = static_cast<uint32_t>(row[d]) << 8;
+        } else if (s.fmt == E4M3) {
+          v = e4m3x2_to_f16x2(row[d]) & 0xFFFFu;
+        } else if (s.fields > 0) {
+          const int c = s.fmt == INT4A ? (row[d / 2] >> (4 * (d & 1))) & 15 : row[d];
+          __half x = __hfma(__int2half_rn(c), sc, zp);
+          if (s.fields == 3) x = __hmul(x, sg);
+          v = __half_as_ushort(x);
+        } else {
+          return;
+        }
+        if (finite16<false>(v)) continue;
+        const bool nan = (v & 0x3FFu) != 0;
+        if (s.fields == 3) {  // the inverse rotation spreads it over the whole row
+          for (int w = 0; w < 4; ++w) hi[w] = lo[w] = 0xFFFFFFFFu;
+          return;
+        }
+        if (nan || !(v & 0x8000u)) hi[d >> 5] |= 1u << (d & 31);
+        if (nan || (v & 0x8000u)) lo[d >> 5] |= 1u << (d & 31);
+      }
     }
-    float dot = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      dot += x[e] * cached_value(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, bs, blk,
-                                 k & (bs - 1), h, lane * E + e);
-#pragma unroll
-    for (int i = 16; i >= 1; i >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
-    const float z = dot * a.sm_scale_log2 * ks;
-    const float mn = fmaxf(m, z);
-    const float al = exp2f(m - mn), pr = exp2f(z - mn);
-    m = mn;
-    l = l * al + pr;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * al + pr * cached_value(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, bs,
-                                           blk, k & (bs - 1), h, lane * E + e);
   }
-  const float il = l > 0.f ? vs / l : 0.f;
+}
+
+template <int D, int NW>
+__global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
+  using C = Cfg<D, NW>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzled tiles: 1024-byte aligned
+  uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + C::CTRL);
+  volatile int* abort = &ctrl->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7;
+  const int h = blockIdx.x % a.num_kv_heads;
+  const int tile_id = a.tiles - 1 - blockIdx.x / a.num_kv_heads;  // later rows see more keys: first
+  auto bar = [&](const void* p) { return base + static_cast<uint32_t>(static_cast<const uint8_t*>(p) - smem); };
+
+  find_tile<C::ROWS>(a, ctrl, tile_id);
+  __syncthreads();
+  const int seq = ctrl->seq;
+  if (seq < 0) return;  // the launch has room for more tiles than the batch has
+  const int n = ctrl->n, q = ctrl->q;
+  const int R0 = ctrl->tile * C::ROWS, R1 = min(q * a.gqa, R0 + C::ROWS);
+  const Span span = row_span(a, n, q, R0, R1);
+  // this split's part of the key tiles
+  const int split = blockIdx.y;
+  const int i0 = static_cast<int>(static_cast<long long>(span.tiles) * split / a.num_splits);
+  const int i1 = static_cast<int>(static_cast<long long>(span.tiles) * (split + 1) / a.num_splits);
+  const int nk = i1 - i0;
+  const int nw = (NW == 2 && R1 - R0 > 128) ? 2 : 1;  // row halves in use
+  const bool bf = a.k_fmt == BF16;
+
+  if (tid == 0) {
+    mbar_init(bar(&ctrl->q_full), 4 * nw);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(&ctrl->k_full[i]), 4);
+      mbar_init(bar(&ctrl->v_full[i]), 4);
+      mbar_init(bar(&ctrl->k_empty[i]), 1);
+      mbar_init(bar(&ctrl->v_empty[i]), 1);
+      mbar_init(bar(&ctrl->s_full[i]), 1);
+      mbar_init(bar(&ctrl->p_full[i]), 4);
+      mbar_init(bar(&ctrl->o_full[i]), 1);
+    }
+    mbar_init(bar(&ctrl->drained), 1);
+    ctrl->abort = 0;
+    ctrl->bad_lo = 0x7fffffff;
+    ctrl->bad_hi = -1;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  if (nk > 0) {
+    if (warp == 4 * (NW + 1)) tmem_alloc(bar(&ctrl->tmem), C::TMEM);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  const uint32_t tmem = ctrl->tmem;
+  auto give_up = [&]() {
+    raise_error(16u);  // KVQ_DEVERR_TIMEOUT: the results of this launch are invalid
+    *abort = 1;
+  };
+
+  if (wg < NW) {
+    // ================= softmax: thread = row =================
+    reg_take<C::R_SOFTMAX>();
+    const int r = R0 + tid;  // row of the sequence (warpgroup w: rows 128 w on)
+    const bool mine = r < R1;
+    const int pos = mine ? n - q + r / a.gqa : span.p_hi;
+    const size_t out_row = (static_cast<size_t>(ctrl->q0) + (mine ? r / a.gqa : 0)) * a.num_q_heads +
+                           static_cast<size_t>(h) * a.gqa + (mine ? r % a.gqa : 0);
+    float scale = a.sm_scale_log2 * (a.k_head_scale != nullptr ? a.k_head_scale[h] : a.k_scale);
+    // a negative scale turns the queries round, so that the largest logit is the
+    // largest product; with scale 0 every logit is 0
+    const float turn = scale < 0.f ? -1.f : scale > 0.f ? 1.f : 0.f;
+    scale = scale == 0.f ? 1.f : fabsf(scale);
+    float m = -INFINITY, l = 0.f;
+    const bool active = wg < nw && nk > 0;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t s_addr = tmem + C::S(wg) + lane_base, o_addr = tmem + C::O(wg) + lane_base;
+    if (active) {
+      {  // the row's query, rotated for KVarN, as a 16-bit operand
+        const uint4* src = reinterpret_cast<const uint4*>(a.query + out_row * D);
+        const uint32_t dst = base + C::Q + wg * C::TILE;
+        const int row = tid & 127;
+        float x[D];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] *= il;
-  if (a.kvarn) {
-    fwht_lanes<E, 32>(o, lane);
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 w = mine ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o[e] *= a.cR;
-      if (a.signs != nullptr && a.signs[lane * E + e] < 0) o[e] = -o[e];
+          for (int e = 0; e < 4; ++e) {
+            x[8 * i + 2 * e] = bf16_lo(u[e]) * turn;
+            x[8 * i + 2 * e + 1] = bf16_hi(u[e]) * turn;
+          }
+        }
+        if (a.kvarn) {
+          if (a.signs != nullptr) {
+#pragma unroll
+            for (int i = 0; i < D; ++i) x[i] = a.signs[i] < 0 ? -x[i] : x[i];
+          }
+          rotate_thread_row<D>(x, a.cR);
+        }
+        bool finite = true;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[e] = pack16(bf, x[8 * i + 2 * e], x[8 * i + 2 * e + 1]);
+            finite = finite && (bf ? finite16<true>(o[e]) && finite16<true>(o[e] >> 16)
+                                   : finite16<false>(o[e]) && finite16<false>(o[e] >> 16));
+          }
+          sts128(chunk_addr(dst, row, i), o[0], o[1], o[2], o[3]);
+        }
+        if (!finite) raise_error(64u);  // KVQ_DEVERR_QUERY_RANGE
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&ctrl->q_full));
+      }
+      const int p_last = n - q + (min(R0 + 128 * (wg + 1), R1) - 1) / a.gqa;  // this warpgroup's last position
+      const int p_first = n - q + (R0 + 128 * wg) / a.gqa;
+      for (int i = 0; i < nk; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->s_full[wg]), i & 1, kSpin, abort))) {
+          give_up();
+          break;
+        }
+        tc_fence_after();
+        float s[kKeys];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(reinterpret_cast<uint32_t*>(s) + 32 * c, s_addr + 32 * c);
+        tmem_wait_ld();
+        const int t0 = tile_key(span, i0 + i);
+        // every row sees every key of the tile, or each row's own part
+        const bool whole = t0 + kKeys - 1 <= p_first &&
+                           (a.window == 0 || t0 > p_last - a.window || t0 + kKeys <= a.sinks);
+        if (!whole) {
+          const int last = pos - t0, first = a.window > 0 ? last - a.window + 1 : -1, kept = a.sinks - t0;
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            if (c > last || (c < first && c >= kept)) s[c] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < kKeys; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = c + 4 + e < kKeys ? max3f(mx[e], s[c + e], s[c + 4 + e]) : fmaxf(mx[e], s[c + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          const float up = fmaxf(m, top);
+          const float f = up == -INFINITY ? 1.f : fast_exp2(m - up);
+          m = up;
+          l *= f;
+          if (i > 0) {  // the products so far are done: S of this tile was issued behind them
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o, o_addr + c);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float x, y;
+                mul2(x, y, __uint_as_float(o[e]), __uint_as_float(o[e + 1]), f, f);
+                o[e] = __float_as_uint(x);
+                o[e + 1] = __float_as_uint(y);
+              }
+              tmem_st32(o_addr + c, o);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every p is 0
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 64) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            float x, y;
+            fma2(x, y, s[c + e], s[c + e + 1], scale, scale, off, off);
+            x = fast_exp2(x);
+            y = fast_exp2(y);
+            add2(sum[e & 2], sum[(e & 2) + 1], sum[e & 2], sum[(e & 2) + 1], x, y);
+            p[e / 2] = pack16(bf, x, y);
+          }
+          tmem_st32(s_addr + c / 2, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&ctrl->p_full[wg]));
+      }
+    }
+    // ---- the row's result
+    bool done = true;
+    if (active && !*abort) {
+      done = __all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->o_full[wg]), 0, kSpin, abort));
+      if (!done) give_up();
+    }
+    const bool partial = a.num_splits > 1;
+    if (wg < nw && done && !*abort) {
+      tc_fence_after();
+      const float vs = a.v_head_scale != nullptr ? a.v_head_scale[h] : a.v_scale;
+      const float mul = partial ? 1.f : l > 0.f ? vs / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
+      uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+      const bool bad = ctrl->bad_hi >= 0;
+      if (bad && mine) find_not_finite<C>(a, span, seq, h, pos, ctrl->bad_lo, ctrl->bad_hi, hi, lo);
+      __syncwarp();
+      const size_t ws_row = ((static_cast<size_t>(split) * a.tiles + tile_id) * a.num_kv_heads + h) * C::ROWS + tid;
+      if (partial) {
+        if (mine) *reinterpret_cast<float2*>(a.ws_ml + 2 * ws_row) = make_float2(m, nk > 0 ? l : 0.f);
+      }
+      float x[D];
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (nk > 0) {
+          tmem_ld32(o, o_addr + c);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[c + e] = __uint_as_float(o[e]) * mul;
+      }
+      if (l == 0.f) {  // nothing seen (the accumulators hold 0 times what was there)
+#pragma unroll
+        for (int i = 0; i < D; ++i) x[i] = 0.f;
+      }
+      if (bad) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+          const bool up = (hi[i >> 5] >> (i & 31)) & 1, down = (lo[i >> 5] >> (i & 31)) & 1;
+          if (up || down) x[i] = up && down ? NAN : up ? INFINITY : -INFINITY;
+        }
+      }
+      if (partial) {
+        if (mine && nk > 0) {
+          float4* dst = reinterpret_cast<float4*>(a.ws_out + ws_row * D);
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+      } else {
+        if (a.kvarn) {
+          rotate_thread_row<D>(x, a.cR);
+          if (a.signs != nullptr) {
+#pragma unroll
+            for (int i = 0; i < D; ++i) x[i] = a.signs[i] < 0 ? -x[i] : x[i];
+          }
+        }
+        if (mine) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            dst[i] = make_uint4(pack_bf162(x[8 * i], x[8 * i + 1]), pack_bf162(x[8 * i + 2], x[8 * i + 3]),
+                                pack_bf162(x[8 * i + 4], x[8 * i + 5]), pack_bf162(x[8 * i + 6], x[8 * i + 7]));
+        }
+      }
+    }
+  } else if (wg == NW) {
+    // ================= producers =================
+    reg_give<C::R_PRODUCE>();
+    if (nk > 0) {
+      const int bs = 1 << a.block_shift;
+      const Source ks = make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
+      const Source vs = make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
+      Producer<C> pr{a, span, base, ctrl, tid & 127, seq};
+      KeyTile next = pr.look_up(i0), cur = next, ready = next;
+      // step j first turns the pieces of step j - AHEAD into operands, then copies
+      // tile j/2's K (j even) or V (j odd) into the slot that this leaves
+      auto wait_empty = [&](bool is_v, int i) {  // the operand stage of tile i: its last reader is done
+        if (i < 2) return true;
+        const bool ok = mbar_wait_or_abort(bar(is_v ? &ctrl->v_empty[i & 1] : &ctrl->k_empty[i & 1]),
+                                           ((i >> 1) + 1) & 1, kSpin, abort);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        give_up();
+        return false;
+      };
+      for (int j = 0; j < 2 * nk + C::AHEAD; ++j) {
+        if (j >= C::AHEAD) {
+          cp_async_wait<C::AHEAD - 1>();
+          const int d = j - C::AHEAD, i = d >> 1, slot = d % C::AHEAD;
+          const bool is_v = d & 1;
+          ready.t0 = tile_key(span, i0 + i);
+          const uint32_t dst = base + (is_v ? C::V : C::K) + (i & 1) * C::TILE;
+          const bool fields = (is_v ? vs : ks).fields > 0;
+          bool ok = bf || wait_empty(is_v, i);
+          if (fields) ok = producers_all(ok);  // and the metadata that other threads copied is there
+          if (!ok) break;
+          const bool bad = is_v ? pr.template finish<true>(vs, ready, slot, dst)
+                                : pr.template finish<false>(ks, ready, slot, dst);
+          if (bad) {
+            atomicMin(&ctrl->bad_lo, i0 + i);
+            atomicMax(&ctrl->bad_hi, i0 + i);
+          }
+          if (fields) asm volatile("bar.sync 1, 128;" ::: "memory");  // read before the slot's next copy
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(is_v ? &ctrl->v_full[i & 1] : &ctrl->k_full[i & 1]));
+        }
+        if (j < 2 * nk) {
+          const int i = j >> 1;
+          const bool is_v = j & 1;
+          if (!is_v) {
+            cur = next;
+            if (i + 1 < nk) next = pr.look_up(i0 + i + 1);
+          }
+          if (bf && !wait_empty(is_v, i)) break;  // copied straight into the operand tile
+          pr.copy(is_v ? vs : ks, cur, j % C::AHEAD, base + (is_v ? C::V : C::K) + (i & 1) * C::TILE);
+        }
+        cp_async_commit();
+      }
+      cp_async_wait<0>();
+    }
+  } else {
+    // ================= products =================
+    reg_give<C::R_ISSUE>();
+    if (warp == 4 * (NW + 1) && nk > 0) {
+      if (lane == 0) {
+        const uint32_t qk_desc = bf ? mma_desc(128, kKeys, true, false) : mma_desc(128, kKeys, false, false);
+        const uint32_t pv_desc = bf ? mma_desc(128, D, true, true) : mma_desc(128, D, false, true);
+        auto wait = [&](const void* b, uint32_t parity) {
+          if (mbar_wait_or_abort(bar(b), parity, kSpin, abort)) return true;
+          give_up();
+          return false;
+        };
+        auto scores = [&](int w, int stage) {  // S_w = Q_w K^T
+          const uint32_t qa = base + C::Q + w * C::TILE, ka = base + C::K + stage * C::TILE;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = (k >> 2) * C::GROUP_BYTES + (k & 3) * 32;
+            mma_ss(tmem + C::S(w), smem_desc(qa + o, 16), smem_desc(ka + o, 16), qk_desc, k > 0);
+          }
+          tc_commit(bar(&ctrl->s_full[w]));
+        };
+        auto values = [&](int w, int stage, bool add) {  // O_w += P_w V
+          const uint32_t va = base + C::V + stage * C::TILE;
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ts(tmem + C::O(w), tmem + C::S(w) + 8 * k, smem_desc(va + k * 2048, C::GROUP_BYTES), pv_desc,
+                   add || k > 0);
+        };
+        bool ok = wait(&ctrl->q_full, 0) && wait(&ctrl->k_full[0], 0);
+        if (ok) {
+          tc_fence_after();
+          for (int w = 0; w < nw; ++w) scores(w, 0);
+          tc_commit(bar(&ctrl->k_empty[0]));
+        }
+        for (int i = 0; ok && i < nk; ++i) {
+          const int st = i & 1, ns = (i + 1) & 1;
+          ok = wait(&ctrl->v_full[st], (i >> 1) & 1);
+          if (ok && i + 1 < nk) ok = wait(&ctrl->k_full[ns], ((i + 1) >> 1) & 1);
+          for (int w = 0; ok && w < nw; ++w) {
+            ok = wait(&ctrl->p_full[w], i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            values(w, st, i > 0);
+            if (w == nw - 1) tc_commit(bar(&ctrl->v_empty[st]));
+            // products run in the order of their issue, so these scores overwrite
+            // the probabilities only once they are read
+            if (i + 1 < nk) scores(w, ns);
+            else tc_commit(bar(&ctrl->o_full[w]));
+          }
+          if (ok && i + 1 < nk) tc_commit(bar(&ctrl->k_empty[ns]));
+        }
+        if (!ok) {  // leave with nothing in flight
+          tc_commit(bar(&ctrl->drained));
+          mbar_wait(bar(&ctrl->drained), 0, kSpin);
+        }
+      }
+      __syncwarp();
     }
   }
-  uint16_t* dst = a.out + (t * a.num_q_heads + hq) * D + lane * E;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (nk > 0 && warp == 4 * (NW + 1)) tmem_dealloc(tmem, C::TMEM);
+}
+
+// Joins the splits' partial results: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
+// A warp per row, D/32 consecutive elements per lane.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs a, int rows_per_tile) {
+  __shared__ Ctrl ctrl;
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, h = blockIdx.x % a.num_kv_heads, tile_id = blockIdx.x / a.num_kv_heads;
+  if (rows_per_tile == 128) find_tile<128>(a, &ctrl, tile_id); else find_tile<256>(a, &ctrl, tile_id);
+  __syncthreads();
+  if (ctrl.seq < 0) return;
+  const int R0 = ctrl.tile * rows_per_tile, R1 = min(ctrl.q * a.gqa, R0 + rows_per_tile);
+  const float vs = a.v_head_scale != nullptr ? a.v_head_scale[h] : a.v_scale;
+  for (int r = R0 + (threadIdx.x >> 5); r < R1; r += blockDim.x >> 5) {
+    const size_t step = static_cast<size_t>(a.tiles) * a.num_kv_heads * rows_per_tile;
+    const size_t row0 = (static_cast<size_t>(tile_id) * a.num_kv_heads + h) * rows_per_tile + (r - R0);
+    float M = -INFINITY;
+    for (int i = 0; i < a.num_splits; ++i) M = fmaxf(M, a.ws_ml[2 * (row0 + i * step)]);
+    float L = 0.f, x[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) dst[e] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e]));
+    for (int e = 0; e < E; ++e) x[e] = 0.f;
+    for (int i = 0; i < a.num_splits; ++i) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + 2 * (row0 + i * step));
+      if (ml.y == 0.f) continue;  // saw nothing
+      const float w = fast_exp2(ml.x - M);
+      L += w * ml.y;
+      const float* src = a.ws_out + (row0 + i * step) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] += w * src[e];
+    }
+    const float mul = L == 0.f ? 0.f : vs / L;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = L == 0.f ? 0.f : x[e] * mul;
+    if (a.kvarn) {
+      fwht_lanes<E, 32>(x, lane);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[e] *= a.cR;
+        if (a.signs != nullptr && a.signs[lane * E + e] < 0) x[e] = -x[e];
+      }
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(
+        a.out + ((static_cast<size_t>(ctrl.q0) + r / a.gqa) * a.num_q_heads + static_cast<size_t>(h) * a.gqa + r % a.gqa) * D +
+        lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf162(x[e], x[e + 1]);
+  }
+}
+
+template <int D, int NW>
+cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
+  using C = Cfg<D, NW>;
+  static std::atomic<unsigned long long> attr_done{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(attr_done.load() & bit)) {
+    e = cudaFuncSetAttribute(prefill_kernel<D, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit);
+  }
+  const dim3 grid(static_cast<unsigned>(a.tiles) * a.num_kv_heads, a.num_splits, 1);
+  prefill_kernel<D, NW><<<grid, C::THREADS, C::SMEM, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.num_splits == 1) return e;
+  prefill_join_kernel<D><<<grid.x, 256, 0, st>>>(a, C::ROWS);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillArgs& a, int head_dim, cudaStream_t st) {
-  const int64_t grid = (a.total_q * a.num_q_heads + 3) / 4;
-  if (grid > 0x7fffffffll) return cudaErrorNotSupported;
-  if (head_dim == 64) prefill_kernel<64><<<static_cast<unsigned>(grid), 128, 0, st>>>(a);
-  else if (head_dim == 128) prefill_kernel<128><<<static_cast<unsigned>(grid), 128, 0, st>>>(a);
-  else return cudaErrorNotSupported;
-  return cudaGetLastError();
+  if (head_dim == 64) return a.rows_per_tile == 128 ? launch_t<64, 1>(a, st) : launch_t<64, 2>(a, st);
+  if (head_dim == 128) return a.rows_per_tile == 128 ? launch_t<128, 1>(a, st) : launch_t<128, 2>(a, st);
+  return cudaErrorNotSupported;
 }
 
 }  // namespace kvq
