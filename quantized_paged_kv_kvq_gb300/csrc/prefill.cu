@@ -37,6 +37,7 @@ KVQ_ERROR_ACCESSOR(take_error_bits_prefill)
 namespace {
 
 constexpr int kKeys = 128;            // keys per tile
+constexpr int kProducers = 256;       // threads that load and dequantize
 constexpr int kSpin = 1 << 22;        // polls of an mbarrier before giving up
 constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is not raised: p <= 2^8
 
@@ -44,7 +45,7 @@ template <int D_, int NW_>  // head_dim, softmax warpgroups
 struct Cfg {
   static constexpr int D = D_, NW = NW_;
   static constexpr int ROWS = 128 * NW;
-  static constexpr int THREADS = 128 * (NW + 2);
+  static constexpr int THREADS = 128 * NW + kProducers + 128;
   static constexpr int GROUPS = D / 64;              // 64-element column groups of an operand row
   static constexpr int GROUP_BYTES = 128 * 128;      // 128 rows of 128 bytes
   static constexpr int TILE = GROUPS * GROUP_BYTES;  // a 128-row operand
@@ -63,10 +64,10 @@ struct Cfg {
   static constexpr uint32_t O(int w) { return NW * 128 + w * 128; }
   static constexpr uint32_t TMEM = NW == 2 ? 512 : 256;
   // registers per thread of the softmax, producer and issuing warpgroups: together
-  // no more than the block is launched with (128 or 168 each)
-  static constexpr int R_SOFTMAX = NW == 2 ? 184 : 216;
-  static constexpr int R_PRODUCE = NW == 2 ? 96 : 160;
-  static constexpr int R_ISSUE = NW == 2 ? 48 : 120;
+  // no more than the block is launched with (96 or 128 each)
+  static constexpr int R_SOFTMAX = NW == 2 ? 144 : 192;
+  static constexpr int R_PRODUCE = NW == 2 ? 72 : 104;
+  static constexpr int R_ISSUE = NW == 2 ? 48 : 64;
 };
 
 // Control words in shared memory.
@@ -268,7 +269,6 @@ struct Source {
   long long page_bytes, meta_page;  // codes of a block in bytes; metadata of a block in halves
   int token_bytes;
   int fmt, fields;
-  int chunk_bits;  // log2 of a row's 16-byte pieces
 };
 __device__ __forceinline__ Source make_source(const uint8_t* cache, const __half* meta, int fmt, int kvarn, int d,
                                               int hkv, int h, int bs) {
@@ -281,7 +281,6 @@ __device__ __forceinline__ Source make_source(const uint8_t* cache, const __half
   s.fields = is_asym(fmt) ? (kvarn ? 3 : 2) : 0;
   s.meta = is_asym(fmt) ? meta + static_cast<size_t>(h) * s.fields * bs : nullptr;
   s.meta_page = static_cast<long long>(hkv) * s.fields * bs;
-  s.chunk_bits = 31 - __clz(rb / 16);
   return s;
 }
 
@@ -290,12 +289,33 @@ __device__ __forceinline__ Source make_source(const uint8_t* cache, const __half
 __device__ __forceinline__ bool producers_all(bool ok) {
   uint32_t all;
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.red.and.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.red.and.pred q, 1, 256, p; selp.u32 %0, 1, 0, q; }"
       : "=r"(all)
       : "r"(static_cast<uint32_t>(ok))
       : "memory");
   return all != 0;
 }
+
+// The 16-byte pieces of a 128-row code tile that a producer thread owns: piece
+// `chunk` of rows row0 + i * STEP, i < PASSES.  The lanes of a quarter-warp take 8 / CL
+// neighbouring rows and CL pieces of each, which makes the 16-byte stores of
+// their j-th operand chunks (OUT per piece) meet distinct banks under the
+// swizzle; a warp's loads still cover whole rows.
+template <int F, int D>
+struct Pieces {
+  static constexpr int CHUNKS = row_bytes(F, D) / 16;  // pieces of a row
+  static constexpr int OUT = F == BF16 ? 1 : F == INT4A ? 4 : 2;
+  static constexpr int STEP = kProducers / CHUNKS;  // a multiple of 8: the swizzle is the same in every pass
+  static constexpr int PASSES = kKeys / STEP;
+  static constexpr int CL = CHUNKS < 8 / OUT ? CHUNKS : 8 / OUT;
+  int chunk, row0;
+  __device__ __forceinline__ explicit Pieces(int tid) {
+    constexpr int RL = 8 / CL, CH = CHUNKS / CL;
+    chunk = tid % CL + CL * (tid / 8 % CH);
+    row0 = tid / CL % RL + RL * (tid / (8 * CH));
+  }
+};
+
 // The producer warpgroup's view of one key tile.
 struct KeyTile {
   int t0;     // first key
@@ -307,12 +327,14 @@ struct Producer {
   const PrefillArgs& a;
   const Span& span;
   uint32_t smem;
-  Ctrl* ctrl;
-  int tid;  // 0..127
+  int tid;  // 0 .. kProducers - 1
   int seq;
 
   __device__ __forceinline__ bool needed(int t) const {
     return t <= span.p_hi && (t >= span.win || t < a.sinks);
+  }
+  __device__ __forceinline__ bool all_needed(int t0) const {
+    return t0 + kKeys - 1 <= span.p_hi && (t0 >= span.win || t0 + kKeys <= a.sinks);
   }
   // Block ids of tile i's pages, one per lane; pages that no row sees are not looked up.
   __device__ __forceinline__ KeyTile look_up(int i) const {
@@ -321,93 +343,119 @@ struct Producer {
     k.block = 0;
     const int lane = tid & 31, bs = 1 << a.block_shift;
     const int t = k.t0 + lane * bs;
-    if (lane < (kKeys >> a.block_shift) && t <= span.p_hi && (t + bs > span.win || t < a.sinks)) {
+    if (lane < (kKeys >> a.block_shift) && t <= span.p_hi && (t + bs > span.win || t < a.sinks))
       k.block = a.block_table[static_cast<size_t>(seq) * a.max_blocks_per_seq + (t >> a.block_shift)];
-      if (k.block < 0 || k.block >= a.num_blocks) {
-        raise_error(2u);  // KVQ_DEVERR_BLOCK_RANGE: block 0 is read instead
-        k.block = 0;
-      }
-    }
     return k;
   }
-  // Start copying the tile's codes: 8-bit and 4-bit ones into slot `slot` of this
-  // thread's queue, 16-bit ones into the operand tile `dst`; and its metadata.
-  __device__ __forceinline__ void copy(const Source& s, const KeyTile& k, int slot, uint32_t dst) const {
-    const int chunk = tid & ((1 << s.chunk_bits) - 1), row0 = tid >> s.chunk_bits;
-    const int passes = 1 << s.chunk_bits, step = kKeys >> s.chunk_bits;
-    const int mask = (1 << a.block_shift) - 1;
-    const uint32_t raw = smem + C::RAWQ + slot * C::RAW + tid * 16;
-#pragma unroll 4
-    for (int i = 0; i < passes; ++i) {
-      const int row = row0 + i * step, t = k.t0 + row;
-      const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
-      const uint8_t* src = s.codes + blk * s.page_bytes + static_cast<long long>((t & mask) * s.token_bytes) + chunk * 16;
-      cp_async_or_zero<16>(s.fmt == BF16 ? chunk_addr(dst, row, chunk) : raw + i * 2048, src, needed(t));
+  // Checked when they are first used, a tile after the look-up, so that nothing waits for it.
+  __device__ __forceinline__ void check(KeyTile& k) const {
+    if (k.block < 0 || k.block >= a.num_blocks) {
+      raise_error(2u);  // KVQ_DEVERR_BLOCK_RANGE: block 0 is read instead
+      k.block = 0;
     }
+  }
+  // Start copying the tile's codes: 8-bit and 4-bit ones into slot `slot` of this
+  // thread's queue, 16-bit ones into the operand tile `dst`.
+  template <int F>
+  __device__ __forceinline__ void copy_codes(const Source& s, const KeyTile& k, int slot, uint32_t dst) const {
+    using P = Pieces<F, C::D>;
+    const P p(tid);
+    const int mask = (1 << a.block_shift) - 1;
+    const uint8_t* src0 = s.codes + p.chunk * 16;
+    const uint32_t to = F == BF16 ? chunk_addr(dst, p.row0, p.chunk) : smem + C::RAWQ + slot * C::RAW + tid * 16;
+    constexpr int TO_STEP = F == BF16 ? P::STEP * 128 : kProducers * 16;
+    if (all_needed(k.t0)) {
+#pragma unroll 4
+      for (int i = 0; i < P::PASSES; ++i) {
+        const int row = p.row0 + i * P::STEP;
+        const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
+        cp_async<16>(to + i * TO_STEP, src0 + blk * s.page_bytes + (row & mask) * s.token_bytes);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < P::PASSES; ++i) {
+        const int row = p.row0 + i * P::STEP;
+        const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
+        cp_async_or_zero<16>(to + i * TO_STEP, src0 + blk * s.page_bytes + (row & mask) * s.token_bytes,
+                             needed(k.t0 + row));
+      }
+    }
+  }
+  __device__ __forceinline__ void copy(const Source& s, const KeyTile& k, int slot, uint32_t dst) const {
+    if (s.fmt == BF16) copy_codes<BF16>(s, k, slot, dst);
+    else if (s.fmt == INT4A) copy_codes<INT4A>(s, k, slot, dst);
+    else copy_codes<INT8>(s, k, slot, dst);  // any 8-bit code
     if (s.fields > 0) {  // a pair of tokens per thread and field
       const int row = 2 * (tid & 63), t = k.t0 + row;
       const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
-      const __half* src = s.meta + blk * s.meta_page + (t & mask);
-      for (int f = tid >> 6; f < s.fields; f += 2)
-        cp_async_or_zero<4>(smem + C::META + (slot * 3 + f) * kKeys * 2 + row * 2, src + (f << a.block_shift),
-                            needed(t) || needed(t + 1));
+      const __half* src = s.meta + blk * s.meta_page + (row & ((1 << a.block_shift) - 1));
+      const bool read = needed(t) || needed(t + 1);
+      const int f = tid >> 6;
+      if (f < s.fields)
+        cp_async_or_zero<4>(smem + C::META + (slot * 3 + f) * kKeys * 2 + row * 2, src + (f << a.block_shift), read);
     }
   }
   // The pieces in slot `slot` as operands; values that are not finite (V) become
   // 0 there and are noted.
   template <int F, bool KVARN, bool IS_V>
   __device__ __forceinline__ bool convert(const KeyTile& k, int slot, uint32_t dst) const {
-    constexpr int CHUNKS = row_bytes(F, C::D) / 16;  // pieces of a row, and passes
-    constexpr int OUT = F == INT4A ? 4 : 2;          // 16-byte operand chunks of a piece
-    const int chunk = tid % CHUNKS, row0 = tid / CHUNKS;
+    using P = Pieces<F, C::D>;
+    const P p(tid);
     const uint32_t raw = smem + C::RAWQ + slot * C::RAW + tid * 16;
-    const uint32_t meta = smem + C::META + slot * 3 * kKeys * 2;
+    const uint32_t meta = smem + C::META + slot * 3 * kKeys * 2 + p.row0 * 2;
+    const bool all = !is_asym(F) || all_needed(k.t0);
+    uint32_t to[P::OUT];
+#pragma unroll
+    for (int j = 0; j < P::OUT; ++j) to[j] = chunk_addr(dst, p.row0, p.chunk * P::OUT + j);
     bool bad = false;
-#pragma unroll 2
-    for (int i = 0; i < CHUNKS; ++i) {
-      const int row = row0 + i * (kKeys / CHUNKS);
-      const uint4 w = ldsv4(raw + i * 2048);
-      uint32_t s = 0, z = 0, g = 0;
-      if (is_asym(F) && needed(k.t0 + row)) {
-        s = lds_pair(meta + row * 2);
-        z = lds_pair(meta + kKeys * 2 + row * 2);
-        if (KVARN) g = lds_pair(meta + 2 * kKeys * 2 + row * 2);
-      }
-      uint32_t o[4 * OUT];
-      dequantize16<F, KVARN>(w, s, z, g, o);
-      if (IS_V && F != INT8 && any_not_finite<false>(o)) {
-        bad = true;
+    constexpr int U = P::PASSES < 2 ? 1 : 2;  // pieces in flight
+#pragma unroll 1
+    for (int i0 = 0; i0 < P::PASSES; i0 += U) {
+      uint4 w[U];
+      uint32_t sc[U], zp[U], sg[U];
 #pragma unroll
-        for (int e = 0; e < 4 * OUT; ++e) o[e] = finite_or_zero<false>(o[e]);
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u;
+        w[u] = ldsv4(raw + i * (kProducers * 16));
+        sc[u] = zp[u] = sg[u] = 0;
+        if constexpr (is_asym(F)) {
+          if (all || needed(k.t0 + p.row0 + i * P::STEP)) {
+            sc[u] = lds_pair(meta + i * P::STEP * 2);
+            zp[u] = lds_pair(meta + (kKeys + i * P::STEP) * 2);
+            if (KVARN) sg[u] = lds_pair(meta + (2 * kKeys + i * P::STEP) * 2);
+          }
+        }
       }
-      // the order in which a piece's chunks are stored differs between the lanes of
-      // a quarter-warp so that their 16-byte stores meet different banks
-      const int turn = C::GROUPS == 2 ? (F == INT4A ? 2 * (chunk >> 1) : (chunk * OUT) >> 3) : 0;
 #pragma unroll
-      for (int j = 0; j < OUT; ++j) {
-        const bool swap = turn != 0;
-        const int jj = j ^ (OUT == 4 ? 2 : 1);  // the chunk stored j-th where swapped
-        const int q = chunk * OUT + (swap ? jj : j);
-        sts128(chunk_addr(dst, row, q), swap ? o[4 * jj] : o[4 * j], swap ? o[4 * jj + 1] : o[4 * j + 1],
-               swap ? o[4 * jj + 2] : o[4 * j + 2], swap ? o[4 * jj + 3] : o[4 * j + 3]);
+      for (int u = 0; u < U; ++u) {
+        uint32_t o[4 * P::OUT];
+        dequantize16<F, KVARN>(w[u], sc[u], zp[u], sg[u], o);
+        if (IS_V && F != INT8 && any_not_finite<false>(o)) {
+          bad = true;
+#pragma unroll
+          for (int e = 0; e < 4 * P::OUT; ++e) o[e] = finite_or_zero<false>(o[e]);
+        }
+#pragma unroll
+        for (int j = 0; j < P::OUT; ++j)
+          sts128(to[j] + (i0 + u) * P::STEP * 128, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
       }
     }
     return bad;
   }
   // 16-bit values are in place already; of V's those that are not finite become 0.
   __device__ __forceinline__ bool check_bf16(uint32_t dst) const {
-    constexpr int CHUNKS = 2 * C::D / 16;
-    const int chunk = tid % CHUNKS, row0 = tid / CHUNKS;
+    using P = Pieces<BF16, C::D>;
+    const P p(tid);
+    const uint32_t at = chunk_addr(dst, p.row0, p.chunk);
     bool bad = false;
 #pragma unroll 4
-    for (int i = 0; i < CHUNKS; ++i) {
-      const uint32_t at = chunk_addr(dst, row0 + i * (kKeys / CHUNKS), chunk);
-      const uint4 w = ldsv4(at);
+    for (int i = 0; i < P::PASSES; ++i) {
+      const uint4 w = ldsv4(at + i * P::STEP * 128);
       const uint32_t o[4] = {w.x, w.y, w.z, w.w};
       if (any_not_finite<true>(o)) {
         bad = true;
-        sts128(at, finite_or_zero<true>(w.x), finite_or_zero<true>(w.y), finite_or_zero<true>(w.z),
-               finite_or_zero<true>(w.w));
+        sts128(at + i * P::STEP * 128, finite_or_zero<true>(w.x), finite_or_zero<true>(w.y),
+               finite_or_zero<true>(w.z), finite_or_zero<true>(w.w));
       }
     }
     return bad;
@@ -427,26 +475,162 @@ struct Producer {
   }
 };
 
-// x <- cR H x for a row held by one thread.
+__device__ __forceinline__ uint32_t pack16(bool bf, float lo, float hi) {
+  return bf ? pack_bf162(lo, hi) : pack_half2(lo, hi);
+}
+
+// Scores that the row does not see become -inf: columns c > last, and those
+// < first that are not < kept.
+__device__ __forceinline__ void mask_scores(uint32_t s_addr, int last, int first, int kept) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < kKeys; c0 += 32) {
+    uint32_t s[32];
+    tmem_ld32(s, s_addr + c0);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (c0 + e > last || (c0 + e < first && c0 + e >= kept)) s[e] = 0xFF800000u;
+    tmem_st32(s_addr + c0, s);
+  }
+  tmem_wait_st();
+}
+__device__ __forceinline__ float largest_score(uint32_t s_addr) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int c0 = 0; c0 < kKeys; c0 += 64) {
+    float s[64];
+    tmem_ld32(reinterpret_cast<uint32_t*>(s), s_addr + c0);
+    tmem_ld32(reinterpret_cast<uint32_t*>(s) + 32, s_addr + c0 + 32);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 64; e += 8)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = max3f(mx[i], s[e + 2 * i], s[e + 2 * i + 1]);
+  }
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+// p = 2^(s * scale + off) over the scores, as 16-bit pairs in their first half;
+// returns the sum (before that rounding).
+template <bool BF>
+__device__ __forceinline__ float probabilities(uint32_t s_addr, float scale, float off) {
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int c0 = 0; c0 < kKeys; c0 += 64) {
+    float s[64];
+    uint32_t p[32];
+    tmem_ld32(reinterpret_cast<uint32_t*>(s), s_addr + c0);
+    tmem_ld32(reinterpret_cast<uint32_t*>(s) + 32, s_addr + c0 + 32);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 64; e += 2) {
+      float x, y;
+      fma2(x, y, s[e], s[e + 1], scale, scale, off, off);
+      x = fast_exp2(x);
+      y = fast_exp2(y);
+      add2(sum[e & 2], sum[(e & 2) + 1], sum[e & 2], sum[(e & 2) + 1], x, y);
+      p[e / 2] = BF ? pack_bf162(x, y) : pack_half2(x, y);
+    }
+    tmem_st32(s_addr + c0 / 2, p);  // over scores that have been read
+  }
+  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+__device__ __forceinline__ void scale_columns(uint32_t addr, int columns, float f) {
+#pragma unroll 1
+  for (int c = 0; c < columns; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(o, addr + c);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float x, y;
+      mul2(x, y, __uint_as_float(o[e]), __uint_as_float(o[e + 1]), f, f);
+      o[e] = __float_as_uint(x);
+      o[e + 1] = __float_as_uint(y);
+    }
+    tmem_st32(addr + c, o);
+  }
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float r;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a));
+  return r;
+}
+
+// Signs of the rotation's diagonal for this lane's E elements, as bits.
+template <int E>
+__device__ __forceinline__ uint32_t lane_signs(const PrefillArgs& a, int lane) {
+  uint32_t bits = 0;
+  if (a.kvarn && a.signs != nullptr) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) bits |= a.signs[lane * E + e] < 0 ? 1u << e : 0u;
+  }
+  return bits;
+}
+
+// x <- d . (cR H x) of a row held by a warp, E elements a lane.
+template <int E>
+__device__ __forceinline__ void unrotate_row(float (&x)[E], uint32_t signs, float cR, int lane) {
+  fwht_lanes<E, 32>(x, lane);
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = (signs >> e & 1) ? -(x[e] * cR) : x[e] * cR;
+}
+// Row R of a sequence whose rows start at packed token q0, rounded to bf16.
+template <int E>
+__device__ __forceinline__ void store_row(const PrefillArgs& a, size_t q0, int R, int h, int D, const float (&x)[E],
+                                          int lane) {
+  uint16_t* dst = a.out + ((q0 + R / a.gqa) * a.num_q_heads + static_cast<size_t>(h) * a.gqa + R % a.gqa) * D + lane * E;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf162(x[0], x[1]);
+}
+// Rows R .. R+31 (those below R1; zeros behind) of a sequence's queries of one
+// kv-head into rows row0 on of an operand tile, a warp a row, four at a time:
+// turned (sign), rotated for KVarN and rounded to 16 bits.
 template <int D>
-__device__ __forceinline__ void rotate_thread_row(float (&x)[D], float cR) {
+__device__ __forceinline__ void load_queries(const PrefillArgs& a, uint32_t tile, int row0, int R, int R1,
+                                             const uint16_t* src, float turn, bool bf, int lane) {
+  constexpr int E = D / 32;
+  const uint32_t signs = lane_signs<E>(a, lane);
+  bool finite = true;
+#pragma unroll 1
+  for (int i = 0; i < 32; i += 4) {
+    uint32_t w[4][E / 2];
 #pragma unroll
-  for (int h = 1; h < D; h <<= 1) {
+    for (int u = 0; u < 4; ++u) {
+      const int r = R + i + u;
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(
+          src + (static_cast<size_t>(r / a.gqa) * a.num_q_heads + r % a.gqa) * D + lane * E);
 #pragma unroll
-    for (int i = 0; i < D; ++i) {
-      if ((i & h) == 0) {
-        const float u = x[i], v = x[i + h];
-        x[i] = u + v;
-        x[i + h] = u - v;
+      for (int e = 0; e < E / 2; ++e) w[u][e] = r < R1 ? __ldg(p + e) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        x[2 * e] = bf16_lo(w[u][e]) * turn;
+        x[2 * e + 1] = bf16_hi(w[u][e]) * turn;
+      }
+      if (a.kvarn) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = (signs >> e & 1) ? -x[e] : x[e];
+        fwht_lanes<E, 32>(x, lane);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] *= a.cR;
+      }
+      const uint32_t at = chunk_addr(tile, row0 + i + u, lane * E / 8) + lane * E % 8 * 2;
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const uint32_t o = pack16(bf, x[2 * e], x[2 * e + 1]);
+        finite = finite && (bf ? finite16<true>(o) && finite16<true>(o >> 16)
+                               : finite16<false>(o) && finite16<false>(o >> 16));
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * e), "r"(o) : "memory");
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < D; ++i) x[i] *= cR;
-}
-
-__device__ __forceinline__ uint32_t pack16(bool bf, float lo, float hi) {
-  return bf ? pack_bf162(lo, hi) : pack_half2(lo, hi);
+  if (!finite) raise_error(64u);  // KVQ_DEVERR_QUERY_RANGE
 }
 
 // Values that are not finite among those that the row at position p sees, per
@@ -512,6 +696,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + C::CTRL);
   volatile int* abort = &ctrl->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7;
+  constexpr int kIssuer = C::THREADS / 32 - 4;  // the warp that issues the products
   const int h = blockIdx.x % a.num_kv_heads;
   const int tile_id = a.tiles - 1 - blockIdx.x / a.num_kv_heads;  // later rows see more keys: first
   auto bar = [&](const void* p) { return base + static_cast<uint32_t>(static_cast<const uint8_t*>(p) - smem); };
@@ -534,8 +719,8 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
   if (tid == 0) {
     mbar_init(bar(&ctrl->q_full), 4 * nw);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(&ctrl->k_full[i]), 4);
-      mbar_init(bar(&ctrl->v_full[i]), 4);
+      mbar_init(bar(&ctrl->k_full[i]), kProducers / 32);
+      mbar_init(bar(&ctrl->v_full[i]), kProducers / 32);
       mbar_init(bar(&ctrl->k_empty[i]), 1);
       mbar_init(bar(&ctrl->v_empty[i]), 1);
       mbar_init(bar(&ctrl->s_full[i]), 1);
@@ -550,7 +735,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
   }
   __syncthreads();
   if (nk > 0) {
-    if (warp == 4 * (NW + 1)) tmem_alloc(bar(&ctrl->tmem), C::TMEM);
+    if (warp == kIssuer) tmem_alloc(bar(&ctrl->tmem), C::TMEM);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -567,8 +752,6 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
     const int r = R0 + tid;  // row of the sequence (warpgroup w: rows 128 w on)
     const bool mine = r < R1;
     const int pos = mine ? n - q + r / a.gqa : span.p_hi;
-    const size_t out_row = (static_cast<size_t>(ctrl->q0) + (mine ? r / a.gqa : 0)) * a.num_q_heads +
-                           static_cast<size_t>(h) * a.gqa + (mine ? r % a.gqa : 0);
     float scale = a.sm_scale_log2 * (a.k_head_scale != nullptr ? a.k_head_scale[h] : a.k_scale);
     // a negative scale turns the queries round, so that the largest logit is the
     // largest product; with scale 0 every logit is 0
@@ -579,45 +762,12 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_addr = tmem + C::S(wg) + lane_base, o_addr = tmem + C::O(wg) + lane_base;
     if (active) {
-      {  // the row's query, rotated for KVarN, as a 16-bit operand
-        const uint4* src = reinterpret_cast<const uint4*>(a.query + out_row * D);
-        const uint32_t dst = base + C::Q + wg * C::TILE;
-        const int row = tid & 127;
-        float x[D];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 w = mine ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[8 * i + 2 * e] = bf16_lo(u[e]) * turn;
-            x[8 * i + 2 * e + 1] = bf16_hi(u[e]) * turn;
-          }
-        }
-        if (a.kvarn) {
-          if (a.signs != nullptr) {
-#pragma unroll
-            for (int i = 0; i < D; ++i) x[i] = a.signs[i] < 0 ? -x[i] : x[i];
-          }
-          rotate_thread_row<D>(x, a.cR);
-        }
-        bool finite = true;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[e] = pack16(bf, x[8 * i + 2 * e], x[8 * i + 2 * e + 1]);
-            finite = finite && (bf ? finite16<true>(o[e]) && finite16<true>(o[e] >> 16)
-                                   : finite16<false>(o[e]) && finite16<false>(o[e] >> 16));
-          }
-          sts128(chunk_addr(dst, row, i), o[0], o[1], o[2], o[3]);
-        }
-        if (!finite) raise_error(64u);  // KVQ_DEVERR_QUERY_RANGE
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(&ctrl->q_full));
-      }
+      load_queries<D>(a, base + C::Q + wg * C::TILE, 32 * (warp & 3), R0 + 32 * warp, R1,
+                      a.query + (static_cast<size_t>(ctrl->q0) * a.num_q_heads + static_cast<size_t>(h) * a.gqa) * D,
+                      turn, bf, lane);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&ctrl->q_full));
       const int p_last = n - q + (min(R0 + 128 * (wg + 1), R1) - 1) / a.gqa;  // this warpgroup's last position
       const int p_first = n - q + (R0 + 128 * wg) / a.gqa;
       for (int i = 0; i < nk; ++i) {
@@ -626,65 +776,25 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
           break;
         }
         tc_fence_after();
-        float s[kKeys];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(reinterpret_cast<uint32_t*>(s) + 32 * c, s_addr + 32 * c);
-        tmem_wait_ld();
         const int t0 = tile_key(span, i0 + i);
         // every row sees every key of the tile, or each row's own part
         const bool whole = t0 + kKeys - 1 <= p_first &&
                            (a.window == 0 || t0 > p_last - a.window || t0 + kKeys <= a.sinks);
         if (!whole) {
-          const int last = pos - t0, first = a.window > 0 ? last - a.window + 1 : -1, kept = a.sinks - t0;
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (c > last || (c < first && c >= kept)) s[c] = -INFINITY;
+          const int last = pos - t0;
+          mask_scores(s_addr, last, a.window > 0 ? last - a.window + 1 : -1, a.sinks - t0);
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < kKeys; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = c + 4 + e < kKeys ? max3f(mx[e], s[c + e], s[c + 4 + e]) : fmaxf(mx[e], s[c + e]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        const float top = largest_score(s_addr) * scale;
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           const float up = fmaxf(m, top);
           const float f = up == -INFINITY ? 1.f : fast_exp2(m - up);
           m = up;
           l *= f;
-          if (i > 0) {  // the products so far are done: S of this tile was issued behind them
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o, o_addr + c);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float x, y;
-                mul2(x, y, __uint_as_float(o[e]), __uint_as_float(o[e + 1]), f, f);
-                o[e] = __float_as_uint(x);
-                o[e + 1] = __float_as_uint(y);
-              }
-              tmem_st32(o_addr + c, o);
-            }
-          }
+          // the products so far are done: S of this tile was issued behind them
+          if (i > 0) scale_columns(o_addr, D, f);
         }
         const float off = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every p is 0
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 64) {
-          uint32_t p[32];
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            float x, y;
-            fma2(x, y, s[c + e], s[c + e + 1], scale, scale, off, off);
-            x = fast_exp2(x);
-            y = fast_exp2(y);
-            add2(sum[e & 2], sum[(e & 2) + 1], sum[e & 2], sum[(e & 2) + 1], x, y);
-            p[e / 2] = pack16(bf, x, y);
-          }
-          tmem_st32(s_addr + c / 2, p);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += bf ? probabilities<true>(s_addr, scale, off) : probabilities<false>(s_addr, scale, off);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -701,71 +811,72 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
     if (wg < nw && done && !*abort) {
       tc_fence_after();
       const float vs = a.v_head_scale != nullptr ? a.v_head_scale[h] : a.v_scale;
-      const float mul = partial ? 1.f : l > 0.f ? vs / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
+      const float mul = partial || l != l ? 1.f : l > 0.f ? vs / l : 0.f;
       uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-      const bool bad = ctrl->bad_hi >= 0;
+      const bool bad = nk > 0 && ctrl->bad_hi >= 0;
       if (bad && mine) find_not_finite<C>(a, span, seq, h, pos, ctrl->bad_lo, ctrl->bad_hi, hi, lo);
       __syncwarp();
       const size_t ws_row = ((static_cast<size_t>(split) * a.tiles + tile_id) * a.num_kv_heads + h) * C::ROWS + tid;
-      if (partial) {
-        if (mine) *reinterpret_cast<float2*>(a.ws_ml + 2 * ws_row) = make_float2(m, nk > 0 ? l : 0.f);
-      }
-      float x[D];
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
+      if (partial && mine) *reinterpret_cast<float2*>(a.ws_ml + 2 * ws_row) = make_float2(m, l);
+      // The rows change from a thread each to a warp each through the operand
+      // stages, which no product reads any more (16-byte chunks permuted by the
+      // row), to be rotated and stored a row at a time.
+      constexpr int E = D / 32;
+      const uint32_t mine_s = base + C::K + wg * (128 * D * 4) + (warp & 3) * (32 * D * 4);
+#pragma unroll 1
+      for (int c = 0; nk > 0 && c < D; c += 32) {
         uint32_t o[32];
-        if (nk > 0) {
-          tmem_ld32(o, o_addr + c);
-          tmem_wait_ld();
-        } else {
+        tmem_ld32(o, o_addr + c);
+        tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
-        }
+        for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : l != l ? 0x7FC00000u : __float_as_uint(__uint_as_float(o[e]) * mul);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[c + e] = __uint_as_float(o[e]) * mul;
+        for (int k = 0; k < 8; ++k)
+          sts128(mine_s + lane * (D * 4) + (((c / 4 + k) ^ (lane & 7)) << 4), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
-      if (l == 0.f) {  // nothing seen (the accumulators hold 0 times what was there)
+      __syncwarp();
+      const uint32_t signs = lane_signs<E>(a, lane);
+      const int rows = min(R1 - (R0 + 32 * warp), 32);
+#pragma unroll 1
+      for (int i = 0; i < rows; ++i) {
+        float x[E];
 #pragma unroll
-        for (int i = 0; i < D; ++i) x[i] = 0.f;
-      }
-      if (bad) {
-#pragma unroll
-        for (int i = 0; i < D; ++i) {
-          const bool up = (hi[i >> 5] >> (i & 31)) & 1, down = (lo[i >> 5] >> (i & 31)) & 1;
-          if (up || down) x[i] = up && down ? NAN : up ? INFINITY : -INFINITY;
+        for (int e = 0; e < E; ++e) {
+          const uint32_t at = mine_s + i * (D * 4) + ((((lane * E + e) / 4) ^ (i & 7)) << 4) + (lane * E + e) % 4 * 4;
+          x[e] = nk > 0 ? lds_f32(at) : 0.f;
         }
-      }
-      if (partial) {
-        if (mine && nk > 0) {
-          float4* dst = reinterpret_cast<float4*>(a.ws_out + ws_row * D);
+        if (bad) {
 #pragma unroll
-          for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        }
-      } else {
-        if (a.kvarn) {
-          rotate_thread_row<D>(x, a.cR);
-          if (a.signs != nullptr) {
-#pragma unroll
-            for (int i = 0; i < D; ++i) x[i] = a.signs[i] < 0 ? -x[i] : x[i];
+          for (int e = 0; e < E; ++e) {
+            uint32_t up = 0, down = 0;
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t u = __shfl_sync(0xffffffffu, hi[k], i), d = __shfl_sync(0xffffffffu, lo[k], i);
+              if (k == (lane * E + e) / 32) {
+                up = u >> ((lane * E + e) & 31) & 1;
+                down = d >> ((lane * E + e) & 31) & 1;
+              }
+            }
+            if (up || down) x[e] = up && down ? NAN : up ? INFINITY : -INFINITY;
           }
         }
-        if (mine) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D);
+        if (partial) {
+          float* dst = a.ws_out + (ws_row - lane + i) * D + lane * E;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            dst[i] = make_uint4(pack_bf162(x[8 * i], x[8 * i + 1]), pack_bf162(x[8 * i + 2], x[8 * i + 3]),
-                                pack_bf162(x[8 * i + 4], x[8 * i + 5]), pack_bf162(x[8 * i + 6], x[8 * i + 7]));
+          for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(dst + e) = make_float2(x[e], x[e + 1]);
+          continue;
         }
+        if (a.kvarn) unrotate_row<E>(x, signs, a.cR, lane);
+        store_row<E>(a, static_cast<size_t>(ctrl->q0), R0 + 32 * warp + i, h, D, x, lane);
       }
     }
-  } else if (wg == NW) {
+  } else if (wg < NW + kProducers / 128) {
     // ================= producers =================
     reg_give<C::R_PRODUCE>();
     if (nk > 0) {
       const int bs = 1 << a.block_shift;
       const Source ks = make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
       const Source vs = make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
-      Producer<C> pr{a, span, base, ctrl, tid & 127, seq};
+      const Producer<C> pr{a, span, base, tid - 128 * NW, seq};
       KeyTile next = pr.look_up(i0), cur = next, ready = next;
       // step j first turns the pieces of step j - AHEAD into operands, then copies
       // tile j/2's K (j even) or V (j odd) into the slot that this leaves
@@ -794,7 +905,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
             atomicMin(&ctrl->bad_lo, i0 + i);
             atomicMax(&ctrl->bad_hi, i0 + i);
           }
-          if (fields) asm volatile("bar.sync 1, 128;" ::: "memory");  // read before the slot's next copy
+          if (fields) asm volatile("bar.sync 1, 256;" ::: "memory");  // read before the slot's next copy
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(is_v ? &ctrl->v_full[i & 1] : &ctrl->k_full[i & 1]));
@@ -804,6 +915,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
           const bool is_v = j & 1;
           if (!is_v) {
             cur = next;
+            pr.check(cur);
             if (i + 1 < nk) next = pr.look_up(i0 + i + 1);
           }
           if (bf && !wait_empty(is_v, i)) break;  // copied straight into the operand tile
@@ -816,7 +928,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
   } else {
     // ================= products =================
     reg_give<C::R_ISSUE>();
-    if (warp == 4 * (NW + 1) && nk > 0) {
+    if (warp == kIssuer && nk > 0) {
       if (lane == 0) {
         const uint32_t qk_desc = bf ? mma_desc(128, kKeys, true, false) : mma_desc(128, kKeys, false, false);
         const uint32_t pv_desc = bf ? mma_desc(128, D, true, true) : mma_desc(128, D, false, true);
@@ -850,7 +962,6 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
         for (int i = 0; ok && i < nk; ++i) {
           const int st = i & 1, ns = (i + 1) & 1;
           ok = wait(&ctrl->v_full[st], (i >> 1) & 1);
-          if (ok && i + 1 < nk) ok = wait(&ctrl->k_full[ns], ((i + 1) >> 1) & 1);
           for (int w = 0; ok && w < nw; ++w) {
             ok = wait(&ctrl->p_full[w], i & 1);
             if (!ok) break;
@@ -859,8 +970,14 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
             if (w == nw - 1) tc_commit(bar(&ctrl->v_empty[st]));
             // products run in the order of their issue, so these scores overwrite
             // the probabilities only once they are read
-            if (i + 1 < nk) scores(w, ns);
-            else tc_commit(bar(&ctrl->o_full[w]));
+            if (i + 1 < nk) {
+              if (w == 0) ok = wait(&ctrl->k_full[ns], ((i + 1) >> 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              scores(w, ns);
+            } else {
+              tc_commit(bar(&ctrl->o_full[w]));
+            }
           }
           if (ok && i + 1 < nk) tc_commit(bar(&ctrl->k_empty[ns]));
         }
@@ -875,7 +992,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (nk > 0 && warp == 4 * (NW + 1)) tmem_dealloc(tmem, C::TMEM);
+  if (nk > 0 && warp == kIssuer) tmem_dealloc(tmem, C::TMEM);
 }
 
 // Joins the splits' partial results: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
@@ -910,19 +1027,8 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs a, 
     const float mul = L == 0.f ? 0.f : vs / L;
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = L == 0.f ? 0.f : x[e] * mul;
-    if (a.kvarn) {
-      fwht_lanes<E, 32>(x, lane);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        x[e] *= a.cR;
-        if (a.signs != nullptr && a.signs[lane * E + e] < 0) x[e] = -x[e];
-      }
-    }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(
-        a.out + ((static_cast<size_t>(ctrl.q0) + r / a.gqa) * a.num_q_heads + static_cast<size_t>(h) * a.gqa + r % a.gqa) * D +
-        lane * E);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf162(x[e], x[e + 1]);
+    if (a.kvarn) unrotate_row<E>(x, lane_signs<E>(a, lane), a.cR, lane);
+    store_row<E>(a, static_cast<size_t>(ctrl.q0), r, h, D, x, lane);
   }
 }
 

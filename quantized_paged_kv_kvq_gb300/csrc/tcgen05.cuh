@@ -50,6 +50,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       KVQ_W8(r, 0), KVQ_W8(r, 8), KVQ_W8(r, 16), KVQ_W8(r, 24)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : KVQ_R8(r, 0), KVQ_R8(r, 8)
+      : "r"(addr));
+}
 #undef KVQ_R8
 #undef KVQ_W8
 
