@@ -37,7 +37,7 @@ KVQ_ERROR_ACCESSOR(take_error_bits_prefill)
 namespace {
 
 constexpr int kKeys = 128;            // keys per tile
-constexpr int kProducers = 256;       // threads that load and dequantize
+constexpr int kProducers = 128;       // threads that load and dequantize K; as many for V
 constexpr int kSpin = 1 << 22;        // polls of an mbarrier before giving up
 constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is not raised: p <= 2^8
 
@@ -45,19 +45,21 @@ template <int D_, int NW_>  // head_dim, softmax warpgroups
 struct Cfg {
   static constexpr int D = D_, NW = NW_;
   static constexpr int ROWS = 128 * NW;
-  static constexpr int THREADS = 128 * NW + kProducers + 128;
+  static constexpr int THREADS = 128 * NW + 2 * kProducers + 128;
   static constexpr int GROUPS = D / 64;              // 64-element column groups of an operand row
   static constexpr int GROUP_BYTES = 128 * 128;      // 128 rows of 128 bytes
   static constexpr int TILE = GROUPS * GROUP_BYTES;  // a 128-row operand
   static constexpr int RAW = 128 * D;                // largest code tile that is dequantized
-  static constexpr int AHEAD = NW == 2 ? 2 : 3;      // K or V tiles a producer's loads run ahead
+  // tiles that the producers' loads run ahead (slots of their queues); what shared
+  // memory leaves room for
+  static constexpr int AHEAD_K = NW == 2 ? 1 : 2, AHEAD_V = 1;
   // shared memory: queries, K and V stages, raw queue, raw metadata, control
   static constexpr int Q = 0;
   static constexpr int K = Q + NW * TILE;
   static constexpr int V = K + 2 * TILE;
   static constexpr int RAWQ = V + 2 * TILE;
-  static constexpr int META = RAWQ + AHEAD * RAW;
-  static constexpr int CTRL = META + AHEAD * 3 * kKeys * 2;
+  static constexpr int META = RAWQ + (AHEAD_K + AHEAD_V) * RAW;  // slots of K, then of V
+  static constexpr int CTRL = META + (AHEAD_K + AHEAD_V) * 3 * kKeys * 2;
   static constexpr int SMEM = CTRL + 256 + 1024;
   // tensor memory columns
   static constexpr uint32_t S(int w) { return w * 128; }
@@ -65,8 +67,8 @@ struct Cfg {
   static constexpr uint32_t TMEM = NW == 2 ? 512 : 256;
   // registers per thread of the softmax, producer and issuing warpgroups: together
   // no more than the block is launched with (96 or 128 each)
-  static constexpr int R_SOFTMAX = NW == 2 ? 144 : 192;
-  static constexpr int R_PRODUCE = NW == 2 ? 72 : 104;
+  static constexpr int R_SOFTMAX = NW == 2 ? 128 : 192;
+  static constexpr int R_PRODUCE = NW == 2 ? 88 : 104;
   static constexpr int R_ISSUE = NW == 2 ? 48 : 64;
 };
 
@@ -284,14 +286,14 @@ __device__ __forceinline__ Source make_source(const uint8_t* cache, const __half
   return s;
 }
 
-// Barrier of the producer warpgroup; whether every warp came with `ok` (so that
-// all leave together, and none waits here for one that gave up).
-__device__ __forceinline__ bool producers_all(bool ok) {
+// Barrier of a producer warpgroup (K's or V's); whether every warp came with `ok`
+// (so that all leave together, and none waits here for one that gave up).
+__device__ __forceinline__ bool producers_all(bool is_v, bool ok) {
   uint32_t all;
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.red.and.pred q, 1, 256, p; selp.u32 %0, 1, 0, q; }"
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.red.and.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
       : "=r"(all)
-      : "r"(static_cast<uint32_t>(ok))
+      : "r"(static_cast<uint32_t>(ok)), "r"(is_v ? 2 : 1)
       : "memory");
   return all != 0;
 }
@@ -390,8 +392,7 @@ struct Producer {
       const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
       const __half* src = s.meta + blk * s.meta_page + (row & ((1 << a.block_shift) - 1));
       const bool read = needed(t) || needed(t + 1);
-      const int f = tid >> 6;
-      if (f < s.fields)
+      for (int f = tid >> 6; f < s.fields; f += 2)
         cp_async_or_zero<4>(smem + C::META + (slot * 3 + f) * kKeys * 2 + row * 2, src + (f << a.block_shift), read);
     }
   }
@@ -408,7 +409,7 @@ struct Producer {
 #pragma unroll
     for (int j = 0; j < P::OUT; ++j) to[j] = chunk_addr(dst, p.row0, p.chunk * P::OUT + j);
     bool bad = false;
-    constexpr int U = P::PASSES < 2 ? 1 : 2;  // pieces in flight
+    constexpr int U = P::PASSES < 4 || F == INT4A ? 2 : 4;  // pieces in flight
 #pragma unroll 1
     for (int i0 = 0; i0 < P::PASSES; i0 += U) {
       uint4 w[U];
@@ -869,59 +870,61 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
         store_row<E>(a, static_cast<size_t>(ctrl->q0), R0 + 32 * warp + i, h, D, x, lane);
       }
     }
-  } else if (wg < NW + kProducers / 128) {
+  } else if (wg < NW + 2) {
     // ================= producers =================
     reg_give<C::R_PRODUCE>();
     if (nk > 0) {
       const int bs = 1 << a.block_shift;
-      const Source ks = make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
-      const Source vs = make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
-      const Producer<C> pr{a, span, base, tid - 128 * NW, seq};
-      KeyTile next = pr.look_up(i0), cur = next, ready = next;
-      // step j first turns the pieces of step j - AHEAD into operands, then copies
-      // tile j/2's K (j even) or V (j odd) into the slot that this leaves
-      auto wait_empty = [&](bool is_v, int i) {  // the operand stage of tile i: its last reader is done
+      const bool is_v = wg == NW + 1;
+      const Source src = is_v ? make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs)
+                              : make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
+      const Producer<C> pr{a, span, base, tid & 127, seq};
+      const uint32_t operand = base + (is_v ? C::V : C::K);
+      unsigned long long* full = is_v ? ctrl->v_full : ctrl->k_full;
+      unsigned long long* empty = is_v ? ctrl->v_empty : ctrl->k_empty;
+      // 16-bit tiles are copied straight into the operand stages, one ahead
+      const int ahead = bf ? 1 : is_v ? C::AHEAD_V : C::AHEAD_K;
+      const int slot0 = is_v ? C::AHEAD_K : 0;
+      auto wait_empty = [&](int i) {  // the operand stage of tile i: its last reader is done
         if (i < 2) return true;
-        const bool ok = mbar_wait_or_abort(bar(is_v ? &ctrl->v_empty[i & 1] : &ctrl->k_empty[i & 1]),
-                                           ((i >> 1) + 1) & 1, kSpin, abort);
+        const bool ok = mbar_wait_or_abort(bar(empty + (i & 1)), ((i >> 1) + 1) & 1, kSpin, abort);
         if (__all_sync(0xffffffffu, ok)) return true;
         give_up();
         return false;
       };
-      for (int j = 0; j < 2 * nk + C::AHEAD; ++j) {
-        if (j >= C::AHEAD) {
-          cp_async_wait<C::AHEAD - 1>();
-          const int d = j - C::AHEAD, i = d >> 1, slot = d % C::AHEAD;
-          const bool is_v = d & 1;
-          ready.t0 = tile_key(span, i0 + i);
-          const uint32_t dst = base + (is_v ? C::V : C::K) + (i & 1) * C::TILE;
-          const bool fields = (is_v ? vs : ks).fields > 0;
-          bool ok = bf || wait_empty(is_v, i);
-          if (fields) ok = producers_all(ok);  // and the metadata that other threads copied is there
-          if (!ok) break;
-          const bool bad = is_v ? pr.template finish<true>(vs, ready, slot, dst)
-                                : pr.template finish<false>(ks, ready, slot, dst);
-          if (bad) {
+      KeyTile next = pr.look_up(i0);
+      auto copy_next = [&](int i) {  // tile i's codes, if there is a tile i
+        if (i < nk) {
+          KeyTile cur = next;
+          pr.check(cur);
+          if (i + 1 < nk) next = pr.look_up(i0 + i + 1);
+          pr.copy(src, cur, slot0 + (ahead == 2 ? i & 1 : 0), operand + (i & 1) * C::TILE);
+        }
+        cp_async_commit();
+      };
+      for (int i = 0; i < ahead; ++i) copy_next(i);
+      for (int i = 0; i < nk; ++i) {
+        if (ahead == 2) cp_async_wait<1>(); else cp_async_wait<0>();
+        bool ok = bf || wait_empty(i);
+        if (src.fields > 0) ok = producers_all(is_v, ok);  // and the metadata that other threads copied is there
+        if (!ok) break;
+        const int slot = slot0 + (ahead == 2 ? i & 1 : 0);
+        const uint32_t dst = operand + (i & 1) * C::TILE;
+        const KeyTile ready{tile_key(span, i0 + i), 0};
+        if (is_v) {
+          if (pr.template finish<true>(src, ready, slot, dst)) {
             atomicMin(&ctrl->bad_lo, i0 + i);
             atomicMax(&ctrl->bad_hi, i0 + i);
           }
-          if (fields) asm volatile("bar.sync 1, 256;" ::: "memory");  // read before the slot's next copy
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(is_v ? &ctrl->v_full[i & 1] : &ctrl->k_full[i & 1]));
+        } else {
+          pr.template finish<false>(src, ready, slot, dst);
         }
-        if (j < 2 * nk) {
-          const int i = j >> 1;
-          const bool is_v = j & 1;
-          if (!is_v) {
-            cur = next;
-            pr.check(cur);
-            if (i + 1 < nk) next = pr.look_up(i0 + i + 1);
-          }
-          if (bf && !wait_empty(is_v, i)) break;  // copied straight into the operand tile
-          pr.copy(is_v ? vs : ks, cur, j % C::AHEAD, base + (is_v ? C::V : C::K) + (i & 1) * C::TILE);
-        }
-        cp_async_commit();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(full + (i & 1)));
+        if (src.fields > 0) producers_all(is_v, true);  // the slot's metadata is read before its next copy
+        if (bf && i + 1 < nk && !wait_empty(i + 1)) break;
+        copy_next(i + ahead);
       }
       cp_async_wait<0>();
     }
@@ -929,62 +932,65 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
     // ================= products =================
     reg_give<C::R_ISSUE>();
     if (warp == kIssuer && nk > 0) {
-      if (lane == 0) {
-        const uint32_t qk_desc = bf ? mma_desc(128, kKeys, true, false) : mma_desc(128, kKeys, false, false);
-        const uint32_t pv_desc = bf ? mma_desc(128, D, true, true) : mma_desc(128, D, false, true);
-        auto wait = [&](const void* b, uint32_t parity) {
-          if (mbar_wait_or_abort(bar(b), parity, kSpin, abort)) return true;
-          give_up();
-          return false;
-        };
-        auto scores = [&](int w, int stage) {  // S_w = Q_w K^T
-          const uint32_t qa = base + C::Q + w * C::TILE, ka = base + C::K + stage * C::TILE;
+      // the same in every lane, and known as such
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int tiles = __shfl_sync(0xffffffffu, nk, 0), halves = __shfl_sync(0xffffffffu, nw, 0);
+      const uint32_t leader = elect_lane();
+      const uint32_t qk_desc = mma_desc(128, kKeys, bf, false), pv_desc = mma_desc(128, D, bf, true);
+      const uint64_t q_op = smem_desc(base + C::Q, 16), k_op = smem_desc(base + C::K, 16);
+      const uint64_t v_op = smem_desc(base + C::V, C::GROUP_BYTES);
+      auto wait = [&](const void* b, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_wait_or_abort(bar(b), parity, kSpin, abort))) return true;
+        give_up();
+        return false;
+      };
+      auto scores = [&](int w, int stage) {  // S_w = Q_w K^T
+        const uint64_t qa = q_op + w * (C::TILE >> 4), ka = k_op + stage * (C::TILE >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = (k >> 2) * C::GROUP_BYTES + (k & 3) * 32;
-            mma_ss(tmem + C::S(w), smem_desc(qa + o, 16), smem_desc(ka + o, 16), qk_desc, k > 0);
-          }
-          tc_commit(bar(&ctrl->s_full[w]));
-        };
-        auto values = [&](int w, int stage, bool add) {  // O_w += P_w V
-          const uint32_t va = base + C::V + stage * C::TILE;
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_ts(tmem + C::O(w), tmem + C::S(w) + 8 * k, smem_desc(va + k * 2048, C::GROUP_BYTES), pv_desc,
-                   add || k > 0);
-        };
-        bool ok = wait(&ctrl->q_full, 0) && wait(&ctrl->k_full[0], 0);
-        if (ok) {
-          tc_fence_after();
-          for (int w = 0; w < nw; ++w) scores(w, 0);
-          tc_commit(bar(&ctrl->k_empty[0]));
+        for (int k = 0; k < D / 16; ++k) {
+          const int o = ((k >> 2) * C::GROUP_BYTES + (k & 3) * 32) >> 4;
+          mma_ss(leader, tm + C::S(0) + w * 128, qa + o, ka + o, qk_desc, k > 0);
         }
-        for (int i = 0; ok && i < nk; ++i) {
-          const int st = i & 1, ns = (i + 1) & 1;
-          ok = wait(&ctrl->v_full[st], (i >> 1) & 1);
-          for (int w = 0; ok && w < nw; ++w) {
-            ok = wait(&ctrl->p_full[w], i & 1);
+        tc_commit(leader, bar(&ctrl->s_full[w]));
+      };
+      auto values = [&](int w, int stage, bool add) {  // O_w += P_w V
+        const uint64_t va = v_op + stage * (C::TILE >> 4);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(leader, tm + C::O(0) + w * 128, tm + C::S(0) + w * 128 + 8 * k, va + k * (2048 >> 4), pv_desc,
+                 add || k > 0);
+      };
+      bool ok = wait(&ctrl->q_full, 0) && wait(&ctrl->k_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        for (int w = 0; w < halves; ++w) scores(w, 0);
+        tc_commit(leader, bar(&ctrl->k_empty[0]));
+      }
+      for (int i = 0; ok && i < tiles; ++i) {
+        const int st = i & 1, ns = (i + 1) & 1;
+        ok = wait(&ctrl->v_full[st], (i >> 1) & 1);
+        for (int w = 0; ok && w < halves; ++w) {
+          ok = wait(&ctrl->p_full[w], i & 1);
+          if (!ok) break;
+          tc_fence_after();
+          values(w, st, i > 0);
+          if (w == halves - 1) tc_commit(leader, bar(&ctrl->v_empty[st]));
+          // products run in the order of their issue, so these scores overwrite
+          // the probabilities only once they are read
+          if (i + 1 < tiles) {
+            if (w == 0) ok = wait(&ctrl->k_full[ns], ((i + 1) >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            values(w, st, i > 0);
-            if (w == nw - 1) tc_commit(bar(&ctrl->v_empty[st]));
-            // products run in the order of their issue, so these scores overwrite
-            // the probabilities only once they are read
-            if (i + 1 < nk) {
-              if (w == 0) ok = wait(&ctrl->k_full[ns], ((i + 1) >> 1) & 1);
-              if (!ok) break;
-              tc_fence_after();
-              scores(w, ns);
-            } else {
-              tc_commit(bar(&ctrl->o_full[w]));
-            }
+            scores(w, ns);
+          } else {
+            tc_commit(leader, bar(&ctrl->o_full[w]));
           }
-          if (ok && i + 1 < nk) tc_commit(bar(&ctrl->k_empty[ns]));
         }
-        if (!ok) {  // leave with nothing in flight
-          tc_commit(bar(&ctrl->drained));
-          mbar_wait(bar(&ctrl->drained), 0, kSpin);
-        }
+        if (ok && i + 1 < tiles) tc_commit(leader, bar(&ctrl->k_empty[ns]));
+      }
+      if (!ok) {  // leave with nothing in flight
+        tc_commit(leader, bar(&ctrl->drained));
+        mbar_wait(bar(&ctrl->drained), 0, kSpin);
       }
       __syncwarp();
     }

@@ -23,10 +23,19 @@ __device__ __forceinline__ void tc_fence_after() {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Arrives on an mbarrier once every tcgen05 operation this thread has issued is done.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+// One lane of the (converged) warp, the same at every call: 1 there, 0 elsewhere.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r;
+}
+// Arrives on an mbarrier once every tcgen05 operation that the lane with `leader` has issued is done.
+__device__ __forceinline__ void tc_commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %1, 0;"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+      "r"(leader)
+      : "memory");
 }
 
 // 32 columns of the warp's 32 lanes, one lane a row.
@@ -74,18 +83,22 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool bf16, bool b_
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 // D[128 x N] (+)= A[128 x 16] B[16 x N]; A and B in shared memory / A in tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// Called by a whole warp and issued by its lane with `leader`: code around it that
+// the warp runs together keeps the descriptors in uniform registers, where the
+// instruction wants them (issued inside a one-lane branch, each product costs
+// some 140 cycles of moves).
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0;"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0;"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(leader)
       : "memory");
 }
 
