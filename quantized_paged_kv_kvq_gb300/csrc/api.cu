@@ -268,6 +268,8 @@ kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
   if (num_q_heads % c->num_kv_heads) return KVQ_ERR_INVALID_ARGUMENT;
   if (num_q_heads / c->num_kv_heads > 8) return KVQ_ERR_UNSUPPORTED;
   if (total_q > INT32_MAX || max_context_len > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->block_size) * c->num_kv_heads * c->head_dim * 2 > INT32_MAX)
+    return KVQ_ERR_UNSUPPORTED;  // a block's bytes fit 31 bits
   if (num_seqs == 0 || total_q == 0 || max_query_len == 0) return KVQ_OK;
   const int sms = sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;

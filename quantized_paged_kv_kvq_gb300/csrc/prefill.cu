@@ -209,10 +209,9 @@ __device__ __forceinline__ void dequantize16(const uint4& raw, uint32_t s, uint3
   }
 }
 
-// Whether one of N pairs of 16-bit values is not finite.
+// acc + 0 * each of N pairs of 16-bit values: stays 0 (or -0) while they are finite.
 template <bool BF, int N>
-__device__ __forceinline__ bool any_not_finite(const uint32_t (&o)[N]) {
-  uint32_t acc = 0;  // 0 times a finite value is 0, times any other NaN
+__device__ __forceinline__ uint32_t track_not_finite(uint32_t acc, const uint32_t (&o)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if constexpr (BF) {
@@ -226,7 +225,10 @@ __device__ __forceinline__ bool any_not_finite(const uint32_t (&o)[N]) {
       acc = *reinterpret_cast<const uint32_t*>(&r);
     }
   }
-  return (acc & 0x7FFF7FFFu) != 0;
+  return acc;
+}
+__device__ __forceinline__ float half_of_pair(uint32_t p) {
+  return fabsf(__half2float(__ushort_as_half(static_cast<uint16_t>(p))));
 }
 template <bool BF>
 __device__ __forceinline__ bool finite16(uint32_t h) {
@@ -268,7 +270,7 @@ __device__ __forceinline__ uint32_t chunk_addr(uint32_t tile, int row, int q) {
 struct Source {
   const uint8_t* codes;  // of the kv-head
   const __half* meta;    // of the kv-head, or nullptr
-  long long page_bytes, meta_page;  // codes of a block in bytes; metadata of a block in halves
+  uint32_t page_bytes, meta_page;  // codes of a block in bytes; metadata of a block in halves
   int token_bytes;
   int fmt, fields;
 };
@@ -278,11 +280,11 @@ __device__ __forceinline__ Source make_source(const uint8_t* cache, const __half
   const int rb = row_bytes(fmt, d);
   s.codes = cache + static_cast<size_t>(h) * rb;
   s.token_bytes = hkv * rb;
-  s.page_bytes = static_cast<long long>(bs) * s.token_bytes;
+  s.page_bytes = static_cast<uint32_t>(bs) * s.token_bytes;  // below 2^31: checked on the host
   s.fmt = fmt;
   s.fields = is_asym(fmt) ? (kvarn ? 3 : 2) : 0;
   s.meta = is_asym(fmt) ? meta + static_cast<size_t>(h) * s.fields * bs : nullptr;
-  s.meta_page = static_cast<long long>(hkv) * s.fields * bs;
+  s.meta_page = static_cast<uint32_t>(hkv) * s.fields * bs;
   return s;
 }
 
@@ -371,14 +373,14 @@ struct Producer {
       for (int i = 0; i < P::PASSES; ++i) {
         const int row = p.row0 + i * P::STEP;
         const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
-        cp_async<16>(to + i * TO_STEP, src0 + blk * s.page_bytes + (row & mask) * s.token_bytes);
+        cp_async<16>(to + i * TO_STEP, src0 + static_cast<unsigned long long>(static_cast<uint32_t>(blk)) * s.page_bytes + (row & mask) * s.token_bytes);
       }
     } else {
 #pragma unroll 1
       for (int i = 0; i < P::PASSES; ++i) {
         const int row = p.row0 + i * P::STEP;
         const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
-        cp_async_or_zero<16>(to + i * TO_STEP, src0 + blk * s.page_bytes + (row & mask) * s.token_bytes,
+        cp_async_or_zero<16>(to + i * TO_STEP, src0 + static_cast<unsigned long long>(static_cast<uint32_t>(blk)) * s.page_bytes + (row & mask) * s.token_bytes,
                              needed(k.t0 + row));
       }
     }
@@ -390,14 +392,15 @@ struct Producer {
     if (s.fields > 0) {  // a pair of tokens per thread and field
       const int row = 2 * (tid & 63), t = k.t0 + row;
       const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
-      const __half* src = s.meta + blk * s.meta_page + (row & ((1 << a.block_shift) - 1));
+      const __half* src = s.meta + static_cast<unsigned long long>(static_cast<uint32_t>(blk)) * s.meta_page +
+                          (row & ((1 << a.block_shift) - 1));
       const bool read = needed(t) || needed(t + 1);
       for (int f = tid >> 6; f < s.fields; f += 2)
         cp_async_or_zero<4>(smem + C::META + (slot * 3 + f) * kKeys * 2 + row * 2, src + (f << a.block_shift), read);
     }
   }
-  // The pieces in slot `slot` as operands; values that are not finite (V) become
-  // 0 there and are noted.
+  // The pieces in slot `slot` as operands; whether one may not be finite (of V,
+  // and of formats that can hold such a value; large asymmetric rows count too).
   template <int F, bool KVARN, bool IS_V>
   __device__ __forceinline__ bool convert(const KeyTile& k, int slot, uint32_t dst) const {
     using P = Pieces<F, C::D>;
@@ -408,8 +411,9 @@ struct Producer {
     uint32_t to[P::OUT];
 #pragma unroll
     for (int j = 0; j < P::OUT; ++j) to[j] = chunk_addr(dst, p.row0, p.chunk * P::OUT + j);
-    bool bad = false;
-    constexpr int U = P::PASSES < 4 || F == INT4A ? 2 : 4;  // pieces in flight
+    uint32_t nf[2] = {0u, 0u};
+    float largest = 0.f;
+    constexpr int U = P::PASSES < 4 || is_asym(F) ? 2 : 4;  // pieces in flight
 #pragma unroll 1
     for (int i0 = 0; i0 < P::PASSES; i0 += U) {
       uint4 w[U];
@@ -431,35 +435,47 @@ struct Producer {
       for (int u = 0; u < U; ++u) {
         uint32_t o[4 * P::OUT];
         dequantize16<F, KVARN>(w[u], sc[u], zp[u], sg[u], o);
-        if (IS_V && F != INT8 && any_not_finite<false>(o)) {
-          bad = true;
-#pragma unroll
-          for (int e = 0; e < 4 * P::OUT; ++e) o[e] = finite_or_zero<false>(o[e]);
+        if constexpr (IS_V && is_asym(F)) {  // |code * s + z| g is at most this
+          float top = fmaf(half_of_pair(sc[u]), static_cast<float>(asym_levels(F)), half_of_pair(zp[u]));
+          if (KVARN) top *= half_of_pair(sg[u]);
+          largest = top < 65504.f ? largest : 65504.f;  // NaN counts
+        } else if constexpr (IS_V && F != INT8) {
+          nf[u & 1] = track_not_finite<false>(nf[u & 1], o);
         }
 #pragma unroll
         for (int j = 0; j < P::OUT; ++j)
           sts128(to[j] + (i0 + u) * P::STEP * 128, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
       }
     }
-    return bad;
+    return largest != 0.f || ((nf[0] | nf[1]) & 0x7FFF7FFFu) != 0;
   }
-  // 16-bit values are in place already; of V's those that are not finite become 0.
+  // 16-bit values are in place already: whether one of them is not finite.
   __device__ __forceinline__ bool check_bf16(uint32_t dst) const {
     using P = Pieces<BF16, C::D>;
     const P p(tid);
     const uint32_t at = chunk_addr(dst, p.row0, p.chunk);
-    bool bad = false;
+    uint32_t nf[2] = {0u, 0u};
 #pragma unroll 4
     for (int i = 0; i < P::PASSES; ++i) {
       const uint4 w = ldsv4(at + i * P::STEP * 128);
       const uint32_t o[4] = {w.x, w.y, w.z, w.w};
-      if (any_not_finite<true>(o)) {
-        bad = true;
-        sts128(at + i * P::STEP * 128, finite_or_zero<true>(w.x), finite_or_zero<true>(w.y),
-               finite_or_zero<true>(w.z), finite_or_zero<true>(w.w));
-      }
+      nf[i & 1] = track_not_finite<true>(nf[i & 1], o);
     }
-    return bad;
+    return ((nf[0] | nf[1]) & 0x7FFF7FFFu) != 0;
+  }
+  // This thread's values of the operand tile that are not finite become 0 (a
+  // probability of 0 times one of them would not be 0).
+  template <int F>
+  __device__ __forceinline__ void make_finite(uint32_t dst) const {
+    using P = Pieces<F, C::D>;
+    constexpr bool BF = F == BF16;
+    const P p(tid);
+#pragma unroll 1
+    for (int i = 0; i < P::PASSES * P::OUT; ++i) {
+      const uint32_t at = chunk_addr(dst, p.row0 + i / P::OUT * P::STEP, p.chunk * P::OUT + i % P::OUT);
+      const uint4 w = ldsv4(at);
+      sts128(at, finite_or_zero<BF>(w.x), finite_or_zero<BF>(w.y), finite_or_zero<BF>(w.z), finite_or_zero<BF>(w.w));
+    }
   }
   template <bool IS_V>
   __device__ __forceinline__ bool finish(const Source& s, const KeyTile& k, int slot, uint32_t dst) const {
@@ -587,51 +603,52 @@ __device__ __forceinline__ void store_row(const PrefillArgs& a, size_t q0, int R
     *reinterpret_cast<uint32_t*>(dst) = pack_bf162(x[0], x[1]);
 }
 // Rows R .. R+31 (those below R1; zeros behind) of a sequence's queries of one
-// kv-head into rows row0 on of an operand tile, a warp a row, four at a time:
-// turned (sign), rotated for KVarN and rounded to 16 bits.
+// kv-head into rows row0 on of an operand tile: turned (sign), rotated for KVarN
+// and rounded to 16 bits.  A row is D/8 lanes of 16 bytes; all are loaded before
+// any is worked on.
 template <int D>
 __device__ __forceinline__ void load_queries(const PrefillArgs& a, uint32_t tile, int row0, int R, int R1,
                                              const uint16_t* src, float turn, bool bf, int lane) {
-  constexpr int E = D / 32;
-  const uint32_t signs = lane_signs<E>(a, lane);
-  bool finite = true;
-#pragma unroll 1
-  for (int i = 0; i < 32; i += 4) {
-    uint32_t w[4][E / 2];
+  constexpr int LPR = D / 8, RPI = 32 / LPR, LOADS = 32 / RPI;
+  const int sub = lane % LPR, grp = lane / LPR;
+  uint32_t signs = 0;
+  if (a.kvarn && a.signs != nullptr) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = R + i + u;
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(
-          src + (static_cast<size_t>(r / a.gqa) * a.num_q_heads + r % a.gqa) * D + lane * E);
+    for (int e = 0; e < 8; ++e) signs |= a.signs[sub * 8 + e] < 0 ? 1u << e : 0u;
+  }
+  uint4 w[LOADS];
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) w[u][e] = r < R1 ? __ldg(p + e) : 0u;
-    }
+  for (int i = 0; i < LOADS; ++i) {
+    const int r = R + i * RPI + grp;
+    w[i] = r < R1 ? __ldg(reinterpret_cast<const uint4*>(
+                        src + (static_cast<size_t>(r / a.gqa) * a.num_q_heads + r % a.gqa) * D + sub * 8))
+                  : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t nf = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float x[E];
+  for (int i = 0; i < LOADS; ++i) {
+    uint32_t o[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    if (!bf || turn != 1.f) {
+      float x[8];
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        x[2 * e] = bf16_lo(w[u][e]) * turn;
-        x[2 * e + 1] = bf16_hi(w[u][e]) * turn;
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(o[e]) * turn;
+        x[2 * e + 1] = bf16_hi(o[e]) * turn;
       }
       if (a.kvarn) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = (signs >> e & 1) ? -x[e] : x[e];
-        fwht_lanes<E, 32>(x, lane);
+        for (int e = 0; e < 8; ++e) x[e] = (signs >> e & 1) ? -x[e] : x[e];
+        fwht_lanes<8, LPR>(x, sub);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] *= a.cR;
+        for (int e = 0; e < 8; ++e) x[e] *= a.cR;
       }
-      const uint32_t at = chunk_addr(tile, row0 + i + u, lane * E / 8) + lane * E % 8 * 2;
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const uint32_t o = pack16(bf, x[2 * e], x[2 * e + 1]);
-        finite = finite && (bf ? finite16<true>(o) && finite16<true>(o >> 16)
-                               : finite16<false>(o) && finite16<false>(o >> 16));
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * e), "r"(o) : "memory");
-      }
+      for (int e = 0; e < 4; ++e) o[e] = pack16(bf, x[2 * e], x[2 * e + 1]);
     }
+    nf = bf ? track_not_finite<true>(nf, o) : track_not_finite<false>(nf, o);
+    sts128(chunk_addr(tile, row0 + i * RPI + grp, sub), o[0], o[1], o[2], o[3]);
   }
-  if (!finite) raise_error(64u);  // KVQ_DEVERR_QUERY_RANGE
+  if (nf & 0x7FFF7FFFu) raise_error(64u);  // KVQ_DEVERR_QUERY_RANGE
 }
 
 // Values that are not finite among those that the row at position p sees, per
@@ -649,10 +666,10 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
       int blk = a.block_table[static_cast<size_t>(seq) * a.max_blocks_per_seq + (t >> a.block_shift)];
       if (blk < 0 || blk >= a.num_blocks) blk = 0;
       const int off = t & (bs - 1);
-      const uint8_t* row = s.codes + blk * s.page_bytes + static_cast<long long>(off) * s.token_bytes;
+      const uint8_t* row = s.codes + static_cast<size_t>(blk) * s.page_bytes + static_cast<size_t>(off) * s.token_bytes;
       __half sc{}, zp{}, sg{};
       if (s.fields > 0) {
-        const __half* m = s.meta + blk * s.meta_page + off;
+        const __half* m = s.meta + static_cast<size_t>(blk) * s.meta_page + off;
         sc = m[0];
         zp = m[bs];
         if (s.fields == 3) sg = m[2 * bs];
@@ -685,6 +702,26 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
         if (nan || (v & 0x8000u)) lo[d >> 5] |= 1u << (d & 31);
       }
     }
+  }
+}
+
+// Puts the marks that lane `row` found for its row (hi, lo) on that row's elements.
+template <int E>
+__device__ __noinline__ void spread_not_finite(float (&x)[E], const uint32_t (&hi)[4], const uint32_t (&lo)[4], int row,
+                                               int lane) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int d = lane * E + e;
+    uint32_t up = 0, down = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t u = __shfl_sync(0xffffffffu, hi[k], row), v = __shfl_sync(0xffffffffu, lo[k], row);
+      if (k == d / 32) {
+        up = u >> (d & 31) & 1;
+        down = v >> (d & 31) & 1;
+      }
+    }
+    if (up || down) x[e] = up && down ? NAN : up ? INFINITY : -INFINITY;
   }
 }
 
@@ -838,36 +875,37 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
       __syncwarp();
       const uint32_t signs = lane_signs<E>(a, lane);
       const int rows = min(R1 - (R0 + 32 * warp), 32);
+      constexpr int U = 4;  // rows at a time (behind the last ones, rows that are not stored)
 #pragma unroll 1
-      for (int i = 0; i < rows; ++i) {
-        float x[E];
+      for (int i0 = 0; i0 < rows; i0 += U) {
+        float x[U][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const uint32_t at = mine_s + i * (D * 4) + ((((lane * E + e) / 4) ^ (i & 7)) << 4) + (lane * E + e) % 4 * 4;
-          x[e] = nk > 0 ? lds_f32(at) : 0.f;
-        }
-        if (bad) {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            uint32_t up = 0, down = 0;
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t u = __shfl_sync(0xffffffffu, hi[k], i), d = __shfl_sync(0xffffffffu, lo[k], i);
-              if (k == (lane * E + e) / 32) {
-                up = u >> ((lane * E + e) & 31) & 1;
-                down = d >> ((lane * E + e) & 31) & 1;
-              }
-            }
-            if (up || down) x[e] = up && down ? NAN : up ? INFINITY : -INFINITY;
+            const uint32_t at = mine_s + (i0 + u) * (D * 4) + ((((lane * E + e) / 4) ^ ((i0 + u) & 7)) << 4) + (lane * E + e) % 4 * 4;
+            x[u][e] = nk > 0 ? lds_f32(at) : 0.f;
+          }
+        if (bad) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            spread_not_finite<E>(x[u], hi, lo, i0 + u, lane);
+        }
+        if (a.kvarn && !partial) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) unrotate_row<E>(x[u], signs, a.cR, lane);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (i0 + u >= rows) break;
+          if (partial) {
+            float* dst = a.ws_out + (ws_row - lane + i0 + u) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(dst + e) = make_float2(x[u][e], x[u][e + 1]);
+          } else {
+            store_row<E>(a, static_cast<size_t>(ctrl->q0), R0 + 32 * warp + i0 + u, h, D, x[u], lane);
           }
         }
-        if (partial) {
-          float* dst = a.ws_out + (ws_row - lane + i) * D + lane * E;
-#pragma unroll
-          for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(dst + e) = make_float2(x[e], x[e + 1]);
-          continue;
-        }
-        if (a.kvarn) unrotate_row<E>(x, signs, a.cR, lane);
-        store_row<E>(a, static_cast<size_t>(ctrl->q0), R0 + 32 * warp + i, h, D, x, lane);
       }
     }
   } else if (wg < NW + 2) {
@@ -912,7 +950,10 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
         const uint32_t dst = operand + (i & 1) * C::TILE;
         const KeyTile ready{tile_key(span, i0 + i), 0};
         if (is_v) {
-          if (pr.template finish<true>(src, ready, slot, dst)) {
+          if (pr.template finish<true>(src, ready, slot, dst)) {  // rare
+            if (bf) pr.template make_finite<BF16>(dst);
+            else if (src.fmt == INT4A) pr.template make_finite<INT4A>(dst);
+            else pr.template make_finite<INT8>(dst);
             atomicMin(&ctrl->bad_lo, i0 + i);
             atomicMax(&ctrl->bad_hi, i0 + i);
           }
