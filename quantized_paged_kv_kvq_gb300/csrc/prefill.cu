@@ -60,15 +60,16 @@ struct Cfg {
   static constexpr int RAWQ = V + 2 * TILE;
   static constexpr int META = RAWQ + (AHEAD_K + AHEAD_V) * RAW;  // slots of K, then of V
   static constexpr int CTRL = META + (AHEAD_K + AHEAD_V) * 3 * kKeys * 2;
-  static constexpr int SMEM = CTRL + 256 + 1024;
+  static constexpr int SIGNS = CTRL + 256;  // the rotation's diagonal as masks of pairs of sign bits
+  static constexpr int SMEM = SIGNS + 2 * D + 1024;
   // tensor memory columns
   static constexpr uint32_t S(int w) { return w * 128; }
   static constexpr uint32_t O(int w) { return NW * 128 + w * 128; }
   static constexpr uint32_t TMEM = NW == 2 ? 512 : 256;
   // registers per thread of the softmax, producer and issuing warpgroups: together
   // no more than the block is launched with (96 or 128 each)
-  static constexpr int R_SOFTMAX = NW == 2 ? 128 : 192;
-  static constexpr int R_PRODUCE = NW == 2 ? 88 : 104;
+  static constexpr int R_SOFTMAX = NW == 2 ? 144 : 192;
+  static constexpr int R_PRODUCE = NW == 2 ? 72 : 104;
   static constexpr int R_ISSUE = NW == 2 ? 48 : 64;
 };
 
@@ -568,85 +569,96 @@ __device__ __forceinline__ void scale_columns(uint32_t addr, int columns, float 
   }
 }
 
-__device__ __forceinline__ float lds_f32(uint32_t a) {
-  float r;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a));
-  return r;
-}
-
-// Signs of the rotation's diagonal for this lane's E elements, as bits.
-template <int E>
-__device__ __forceinline__ uint32_t lane_signs(const PrefillArgs& a, int lane) {
-  uint32_t bits = 0;
-  if (a.kvarn && a.signs != nullptr) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) bits |= a.signs[lane * E + e] < 0 ? 1u << e : 0u;
-  }
-  return bits;
-}
-
-// x <- d . (cR H x) of a row held by a warp, E elements a lane.
-template <int E>
-__device__ __forceinline__ void unrotate_row(float (&x)[E], uint32_t signs, float cR, int lane) {
-  fwht_lanes<E, 32>(x, lane);
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = (signs >> e & 1) ? -(x[e] * cR) : x[e] * cR;
-}
-// Row R of a sequence whose rows start at packed token q0, rounded to bf16.
-template <int E>
-__device__ __forceinline__ void store_row(const PrefillArgs& a, size_t q0, int R, int h, int D, const float (&x)[E],
-                                          int lane) {
-  uint16_t* dst = a.out + ((q0 + R / a.gqa) * a.num_q_heads + static_cast<size_t>(h) * a.gqa + R % a.gqa) * D + lane * E;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf162(x[0], x[1]);
-}
-// Rows R .. R+31 (those below R1; zeros behind) of a sequence's queries of one
-// kv-head into rows row0 on of an operand tile: turned (sign), rotated for KVarN
-// and rounded to 16 bits.  A row is D/8 lanes of 16 bytes; all are loaded before
-// any is worked on.
+// H x of a row held by one thread, on packed pairs from the second stage on.
 template <int D>
-__device__ __forceinline__ void load_queries(const PrefillArgs& a, uint32_t tile, int row0, int R, int R1,
-                                             const uint16_t* src, float turn, bool bf, int lane) {
-  constexpr int LPR = D / 8, RPI = 32 / LPR, LOADS = 32 / RPI;
+__device__ __forceinline__ void fwht_row(float (&x)[D]) {
+#pragma unroll
+  for (int i = 0; i < D; i += 2) {
+    const float u = x[i], v = x[i + 1];
+    x[i] = u + v;
+    x[i + 1] = u - v;
+  }
+#pragma unroll
+  for (int h = 2; h < D; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < D; i += 2) {
+      if ((i & h) == 0) {
+        const float u0 = x[i], u1 = x[i + 1], v0 = x[i + h], v1 = x[i + h + 1];
+        add2(x[i], x[i + 1], u0, u1, v0, v1);
+        sub2(x[i + h], x[i + h + 1], u0, u1, v0, v1);
+      }
+    }
+  }
+}
+
+// The packed rows that consecutive rows R0 + d (d < 32) of a sequence are: row r
+// is head r % G of token r / G.  G <= 8, so d + R0 % G < 39 and a product with
+// ceil(1024 / G) divides exactly.
+struct RowMap {
+  size_t token0;
+  int first, recip, g, heads;
+  __device__ __forceinline__ RowMap(const PrefillArgs& a, int q0, int h, int R0)
+      : token0(static_cast<size_t>(q0) + R0 / a.gqa), first(R0 % a.gqa), recip((1023 + a.gqa) / a.gqa), g(a.gqa),
+        heads(a.num_q_heads) {
+    token0 = token0 * heads + static_cast<size_t>(h) * g;
+  }
+  __device__ __forceinline__ size_t operator()(int d) const {  // row of [tokens * heads, D]
+    const int x = first + d, t = (x * recip) >> 10;
+    return token0 + static_cast<size_t>(t) * heads + (x - t * g);
+  }
+};
+
+// Rows R .. R+31 (those below R1; zeros behind) of the queries into rows row0 on
+// of an operand tile, by a warp: copied as they are, a row being D/8 lanes of 16
+// bytes, then turned (sign), rotated for KVarN and rounded to fp16 a row per
+// thread.
+template <int D>
+__device__ __forceinline__ void load_queries(const PrefillArgs& a, uint32_t tile, uint32_t signs, int row0, int R,
+                                             int R1, const RowMap& map, float turn, bool bf, int lane) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR;
   const int sub = lane % LPR, grp = lane / LPR;
-  uint32_t signs = 0;
-  if (a.kvarn && a.signs != nullptr) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) signs |= a.signs[sub * 8 + e] < 0 ? 1u << e : 0u;
-  }
-  uint4 w[LOADS];
-#pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    const int r = R + i * RPI + grp;
-    w[i] = r < R1 ? __ldg(reinterpret_cast<const uint4*>(
-                        src + (static_cast<size_t>(r / a.gqa) * a.num_q_heads + r % a.gqa) * D + sub * 8))
-                  : make_uint4(0, 0, 0, 0);
-  }
+#pragma unroll 4
+  for (int d = grp; d < 32; d += RPI)
+    cp_async_or_zero<16>(chunk_addr(tile, row0 + d, sub), a.query + map(R + d < R1 ? d : 0) * D + sub * 8, R + d < R1);
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncwarp();
   uint32_t nf = 0;
+  if (a.kvarn) {
+    float x[D];
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    uint32_t o[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-    if (!bf || turn != 1.f) {
-      float x[8];
+    for (int q = 0; q < D / 8; ++q) {
+      const uint4 w = ldsv4(chunk_addr(tile, row0 + lane, q)), m = ldsv4(signs + 16 * q);
+      const uint32_t o[4] = {w.x ^ m.x, w.y ^ m.y, w.z ^ m.z, w.w ^ m.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[2 * e] = bf16_lo(o[e]) * turn;
-        x[2 * e + 1] = bf16_hi(o[e]) * turn;
+        x[8 * q + 2 * e] = bf16_lo(o[e]);
+        x[8 * q + 2 * e + 1] = bf16_hi(o[e]);
       }
-      if (a.kvarn) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (signs >> e & 1) ? -x[e] : x[e];
-        fwht_lanes<8, LPR>(x, sub);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= a.cR;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = pack16(bf, x[2 * e], x[2 * e + 1]);
     }
-    nf = bf ? track_not_finite<true>(nf, o) : track_not_finite<false>(nf, o);
-    sts128(chunk_addr(tile, row0 + i * RPI + grp, sub), o[0], o[1], o[2], o[3]);
+    fwht_row<D>(x);
+    const float f = a.cR * turn;
+#pragma unroll
+    for (int q = 0; q < D / 8; ++q) {
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = pack_half2(x[8 * q + 2 * e] * f, x[8 * q + 2 * e + 1] * f);
+      nf = track_not_finite<false>(nf, o);
+      sts128(chunk_addr(tile, row0 + lane, q), o[0], o[1], o[2], o[3]);
+    }
+  } else {
+#pragma unroll 2
+    for (int q = 0; q < D / 8; ++q) {
+      const uint32_t at = chunk_addr(tile, row0 + lane, q);
+      const uint4 w = ldsv4(at);
+      uint32_t o[4] = {w.x, w.y, w.z, w.w};
+      if (!bf || turn != 1.f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pack16(bf, bf16_lo(o[e]) * turn, bf16_hi(o[e]) * turn);
+        sts128(at, o[0], o[1], o[2], o[3]);
+      }
+      nf = bf ? track_not_finite<true>(nf, o) : track_not_finite<false>(nf, o);
+    }
   }
   if (nf & 0x7FFF7FFFu) raise_error(64u);  // KVQ_DEVERR_QUERY_RANGE
 }
@@ -705,23 +717,22 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
   }
 }
 
-// Puts the marks that lane `row` found for its row (hi, lo) on that row's elements.
-template <int E>
-__device__ __noinline__ void spread_not_finite(float (&x)[E], const uint32_t (&hi)[4], const uint32_t (&lo)[4], int row,
-                                               int lane) {
+// 32 columns of a row's accumulators times mul; 0 for a row that saw nothing (its
+// accumulators are 0 times whatever was there), NaN with a sum that is NaN, and
+// what the marked values make of theirs (bits: hi +inf, lo -inf, both NaN).
+__device__ __forceinline__ void result_columns(uint32_t (&o)[32], uint32_t addr, int c, float l, float mul, uint32_t hi,
+                                               uint32_t lo) {
+  tmem_ld32(o, addr + c);
+  tmem_wait_ld();
+  const float f = l != l ? l : mul;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int d = lane * E + e;
-    uint32_t up = 0, down = 0;
+  for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
+  if (hi | lo) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t u = __shfl_sync(0xffffffffu, hi[k], row), v = __shfl_sync(0xffffffffu, lo[k], row);
-      if (k == d / 32) {
-        up = u >> (d & 31) & 1;
-        down = v >> (d & 31) & 1;
-      }
+    for (int e = 0; e < 32; ++e) {
+      const uint32_t up = hi >> e & 1, down = lo >> e & 1;
+      o[e] = up && down ? 0x7FC00000u : up ? 0x7F800000u : down ? 0xFF800000u : o[e];
     }
-    if (up || down) x[e] = up && down ? NAN : up ? INFINITY : -INFINITY;
   }
 }
 
@@ -771,6 +782,9 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
     ctrl->bad_hi = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (a.kvarn && tid < D / 2)
+    reinterpret_cast<uint32_t*>(smem + C::SIGNS)[tid] =
+        a.signs == nullptr ? 0u : (a.signs[2 * tid] < 0 ? 0x8000u : 0u) | (a.signs[2 * tid + 1] < 0 ? 0x80000000u : 0u);
   __syncthreads();
   if (nk > 0) {
     if (warp == kIssuer) tmem_alloc(bar(&ctrl->tmem), C::TMEM);
@@ -797,12 +811,12 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
     scale = scale == 0.f ? 1.f : fabsf(scale);
     float m = -INFINITY, l = 0.f;
     const bool active = wg < nw && nk > 0;
+    const RowMap map(a, ctrl->q0, h, min(R0 + 32 * warp, R1 - 1));
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_addr = tmem + C::S(wg) + lane_base, o_addr = tmem + C::O(wg) + lane_base;
     if (active) {
-      load_queries<D>(a, base + C::Q + wg * C::TILE, 32 * (warp & 3), R0 + 32 * warp, R1,
-                      a.query + (static_cast<size_t>(ctrl->q0) * a.num_q_heads + static_cast<size_t>(h) * a.gqa) * D,
-                      turn, bf, lane);
+      load_queries<D>(a, base + C::Q + wg * C::TILE, base + C::SIGNS, 32 * (warp & 3), R0 + 32 * warp, R1, map, turn, bf,
+                      lane);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(&ctrl->q_full));
@@ -856,56 +870,71 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
       __syncwarp();
       const size_t ws_row = ((static_cast<size_t>(split) * a.tiles + tile_id) * a.num_kv_heads + h) * C::ROWS + tid;
       if (partial && mine) *reinterpret_cast<float2*>(a.ws_ml + 2 * ws_row) = make_float2(m, l);
-      // The rows change from a thread each to a warp each through the operand
-      // stages, which no product reads any more (16-byte chunks permuted by the
-      // row), to be rotated and stored a row at a time.
-      constexpr int E = D / 32;
+      // The rows, a thread each, pass through the operand stages, which no product
+      // reads any more (16-byte chunks permuted by the row), to be stored whole.
       const uint32_t mine_s = base + C::K + wg * (128 * D * 4) + (warp & 3) * (32 * D * 4);
-#pragma unroll 1
-      for (int c = 0; nk > 0 && c < D; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(o, o_addr + c);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : l != l ? 0x7FC00000u : __float_as_uint(__uint_as_float(o[e]) * mul);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          sts128(mine_s + lane * (D * 4) + (((c / 4 + k) ^ (lane & 7)) << 4), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-      }
-      __syncwarp();
-      const uint32_t signs = lane_signs<E>(a, lane);
       const int rows = min(R1 - (R0 + 32 * warp), 32);
-      constexpr int U = 4;  // rows at a time (behind the last ones, rows that are not stored)
+      if (partial) {  // float32, a warp a row
 #pragma unroll 1
-      for (int i0 = 0; i0 < rows; i0 += U) {
-        float x[U][E];
+        for (int c = 0; nk > 0 && c < D; c += 32) {
+          uint32_t o[32];
+          result_columns(o, o_addr, c, l, 1.f, hi[c / 32], lo[c / 32]);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+          for (int k = 0; k < 8; ++k)
+            sts128(mine_s + lane * (D * 4) + (((c / 4 + k) ^ (lane & 7)) << 4), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        __syncwarp();
+        constexpr int LPR = D / 4, RPI = 32 / LPR;
+        const int sub = lane % LPR;
+#pragma unroll 4
+        for (int d = lane / LPR; nk > 0 && d < rows; d += RPI)
+          *reinterpret_cast<uint4*>(a.ws_out + (ws_row - lane + d) * D + 4 * sub) =
+              ldsv4(mine_s + d * (D * 4) + ((sub ^ (d & 7)) << 4));
+      } else {  // bf16, D/8 lanes a row
+        const uint32_t row_s = mine_s + lane * (D * 2);
+        if (nk == 0) {
+#pragma unroll 1
+          for (int q = 0; q < D / 8; ++q) sts128(row_s + (q << 4), 0u, 0u, 0u, 0u);
+        } else if (a.kvarn) {
+          float x[D];
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const uint32_t at = mine_s + (i0 + u) * (D * 4) + ((((lane * E + e) / 4) ^ ((i0 + u) & 7)) << 4) + (lane * E + e) % 4 * 4;
-            x[u][e] = nk > 0 ? lds_f32(at) : 0.f;
+          for (int c = 0; c < D; c += 32) tmem_ld32(reinterpret_cast<uint32_t*>(x) + c, o_addr + c);
+          tmem_wait_ld();
+          fwht_row<D>(x);
+          const float f = hi[0] ? NAN : l == 0.f ? 0.f : a.cR * (l != l ? l : mul);
+#pragma unroll
+          for (int q = 0; q < D / 8; ++q) {
+            const uint4 m = ldsv4(base + C::SIGNS + 16 * q);
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float u = x[8 * q + 2 * e] * f, v = x[8 * q + 2 * e + 1] * f;
+              o[e] = pack_bf162(u, v);
+            }
+            if (l == 0.f) o[0] = o[1] = o[2] = o[3] = 0u;
+            sts128(row_s + ((q ^ (lane & 7)) << 4), o[0] ^ m.x, o[1] ^ m.y, o[2] ^ m.z, o[3] ^ m.w);
           }
-        if (bad) {
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            result_columns(o, o_addr, c, l, mul, hi[c / 32], lo[c / 32]);
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            spread_not_finite<E>(x[u], hi, lo, i0 + u, lane);
-        }
-        if (a.kvarn && !partial) {
+            for (int k = 0; k < 4; ++k) {
+              uint32_t p[4];
 #pragma unroll
-          for (int u = 0; u < U; ++u) unrotate_row<E>(x[u], signs, a.cR, lane);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (i0 + u >= rows) break;
-          if (partial) {
-            float* dst = a.ws_out + (ws_row - lane + i0 + u) * D + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(dst + e) = make_float2(x[u][e], x[u][e + 1]);
-          } else {
-            store_row<E>(a, static_cast<size_t>(ctrl->q0), R0 + 32 * warp + i0 + u, h, D, x[u], lane);
+              for (int e = 0; e < 4; ++e)
+                p[e] = pack_bf162(__uint_as_float(o[8 * k + 2 * e]), __uint_as_float(o[8 * k + 2 * e + 1]));
+              sts128(row_s + (((c / 8 + k) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+            }
           }
         }
+        __syncwarp();
+        constexpr int LPR = D / 8, RPI = 32 / LPR;
+        const int sub = lane % LPR;
+#pragma unroll 4
+        for (int d = lane / LPR; d < rows; d += RPI)
+          *reinterpret_cast<uint4*>(a.out + map(d) * D + 8 * sub) = ldsv4(mine_s + d * (D * 2) + ((sub ^ (d & 7)) << 4));
       }
     }
   } else if (wg < NW + 2) {
@@ -1074,8 +1103,19 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs a, 
     const float mul = L == 0.f ? 0.f : vs / L;
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = L == 0.f ? 0.f : x[e] * mul;
-    if (a.kvarn) unrotate_row<E>(x, lane_signs<E>(a, lane), a.cR, lane);
-    store_row<E>(a, static_cast<size_t>(ctrl.q0), r, h, D, x, lane);
+    if (a.kvarn) {
+      fwht_lanes<E, 32>(x, lane);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[e] *= a.cR;
+        if (a.signs != nullptr && a.signs[lane * E + e] < 0) x[e] = -x[e];
+      }
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(
+        a.out + ((static_cast<size_t>(ctrl.q0) + r / a.gqa) * a.num_q_heads + static_cast<size_t>(h) * a.gqa + r % a.gqa) * D +
+        lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf162(x[e], x[e + 1]);
   }
 }
 
