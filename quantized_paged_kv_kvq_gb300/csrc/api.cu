@@ -723,8 +723,10 @@ kvq_status kvq_rope_table(float* table, int64_t num_positions, int32_t rot_dim, 
   rope_turns(rot_dim, base, sc, &turns);
   if (num_positions == 0) return KVQ_OK;
   if (!table || !aligned(table, 16)) return KVQ_ERR_INVALID_ARGUMENT;
+  const int sms = sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
   const cudaError_t e = launch_rope_table(table, num_positions, rot_dim / 2,
-                                          static_cast<float>(sc.amplitude), turns, stream);
+                                          static_cast<float>(sc.amplitude), turns, stream, sms);
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 

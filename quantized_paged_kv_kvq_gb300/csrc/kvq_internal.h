@@ -128,7 +128,7 @@ struct RopeTurns {
   unsigned long long t[kMaxRopePairs];
 };
 cudaError_t launch_rope_table(float* table, int64_t num_positions, int pairs, float amplitude,
-                              const RopeTurns& turns, cudaStream_t st);
+                              const RopeTurns& turns, cudaStream_t st, int num_sms);
 
 // Norm and rotation (kvq_norm_rope), with the cache to store into
 // (kvq_norm_rope_write; the cache's fields as in WriteArgs).

@@ -504,7 +504,7 @@ __device__ __forceinline__ void mask_scores(uint32_t s_addr, int last, int first
   for (int c0 = 0; c0 < kKeys; c0 += 32) {
     uint32_t s[32];
     tmem_ld32(s, s_addr + c0);
-    tmem_wait_ld();
+    tmem_wait_ld32(s);
 #pragma unroll
     for (int e = 0; e < 32; ++e)
       if (c0 + e > last || (c0 + e < first && c0 + e >= kept)) s[e] = 0xFF800000u;
@@ -516,14 +516,16 @@ __device__ __forceinline__ float largest_score(uint32_t s_addr) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
   for (int c0 = 0; c0 < kKeys; c0 += 64) {
-    float s[64];
-    tmem_ld32(reinterpret_cast<uint32_t*>(s), s_addr + c0);
-    tmem_ld32(reinterpret_cast<uint32_t*>(s) + 32, s_addr + c0 + 32);
-    tmem_wait_ld();
+    uint32_t s[64];
+    tmem_ld32(s, s_addr + c0);
+    tmem_ld32(s + 32, s_addr + c0 + 32);
+    tmem_wait_ld32(s);
+    tmem_waited32(s + 32);
 #pragma unroll
     for (int e = 0; e < 64; e += 8)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mx[i] = max3f(mx[i], s[e + 2 * i], s[e + 2 * i + 1]);
+      for (int i = 0; i < 4; ++i)
+        mx[i] = max3f(mx[i], __uint_as_float(s[e + 2 * i]), __uint_as_float(s[e + 2 * i + 1]));
   }
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
@@ -534,15 +536,15 @@ __device__ __forceinline__ float probabilities(uint32_t s_addr, float scale, flo
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
   for (int c0 = 0; c0 < kKeys; c0 += 64) {
-    float s[64];
-    uint32_t p[32];
-    tmem_ld32(reinterpret_cast<uint32_t*>(s), s_addr + c0);
-    tmem_ld32(reinterpret_cast<uint32_t*>(s) + 32, s_addr + c0 + 32);
-    tmem_wait_ld();
+    uint32_t s[64], p[32];
+    tmem_ld32(s, s_addr + c0);
+    tmem_ld32(s + 32, s_addr + c0 + 32);
+    tmem_wait_ld32(s);
+    tmem_waited32(s + 32);
 #pragma unroll
     for (int e = 0; e < 64; e += 2) {
       float x, y;
-      fma2(x, y, s[e], s[e + 1], scale, scale, off, off);
+      fma2(x, y, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), scale, scale, off, off);
       x = fast_exp2(x);
       y = fast_exp2(y);
       add2(sum[e & 2], sum[(e & 2) + 1], sum[e & 2], sum[(e & 2) + 1], x, y);
@@ -557,7 +559,7 @@ __device__ __forceinline__ void scale_columns(uint32_t addr, int columns, float 
   for (int c = 0; c < columns; c += 32) {
     uint32_t o[32];
     tmem_ld32(o, addr + c);
-    tmem_wait_ld();
+    tmem_wait_ld32(o);
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
       float x, y;
@@ -723,7 +725,7 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
 __device__ __forceinline__ void result_columns(uint32_t (&o)[32], uint32_t addr, int c, float l, float mul, uint32_t hi,
                                                uint32_t lo) {
   tmem_ld32(o, addr + c);
-  tmem_wait_ld();
+  tmem_wait_ld32(o);
   const float f = l != l ? l : mul;
 #pragma unroll
   for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
@@ -896,10 +898,15 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
 #pragma unroll 1
           for (int q = 0; q < D / 8; ++q) sts128(row_s + (q << 4), 0u, 0u, 0u, 0u);
         } else if (a.kvarn) {
+          uint32_t w[D];
+#pragma unroll
+          for (int c = 0; c < D; c += 32) tmem_ld32(w + c, o_addr + c);
+          tmem_wait_ld32(w);
+#pragma unroll
+          for (int c = 32; c < D; c += 32) tmem_waited32(w + c);
           float x[D];
 #pragma unroll
-          for (int c = 0; c < D; c += 32) tmem_ld32(reinterpret_cast<uint32_t*>(x) + c, o_addr + c);
-          tmem_wait_ld();
+          for (int e = 0; e < D; ++e) x[e] = __uint_as_float(w[e]);
           fwht_row<D>(x);
           const float f = hi[0] ? NAN : l == 0.f ? 0.f : a.cR * (l != l ? l : mul);
 #pragma unroll

@@ -5,46 +5,67 @@
 // it wraps modulo one turn by itself, so the angle's reduction is one integer
 // product and exact however far the position is (float32 angles lose all digits
 // past a few thousand radians; float64 ones cost this part's slow pipe).  What
-// is left is the eighth of a turn nearest zero, converted to float32 with its
-// full relative precision, and sincospif on it.
+// is left after the nearest quarter turn goes through sincospif.
+//
+// A thread makes a run of 8 positions of one pair: the first angle's cos and sin,
+// turned by 0 .. 7 positions' (kept in registers for all of the thread's runs):
+// one complex product in place of a sincospif, 2^-23 more of error.  Threads of a
+// warp hold neighbouring pairs, so each store is a row's consecutive bytes.
+// Write-bound.
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 
 namespace kvq {
 namespace {
 
-// (cos, sin) of `turn` / 2^64 turns
+constexpr int kRun = 8;        // positions per thread and step
+constexpr int kThreads = 256;
+
+// (cos, sin) of `turn` / 2^64 turns.  The 32 bits kept of the part beyond a quarter
+// turn leave 2^-33 turns, 7e-10 radians.
 __device__ __forceinline__ float2 cos_sin_turn(unsigned long long turn) {
   const unsigned q = static_cast<unsigned>((turn + (1ull << 61)) >> 62);  // nearest quarter
-  const long long rest = static_cast<long long>(turn - (static_cast<unsigned long long>(q) << 62));
+  const int rest = static_cast<int>((turn - (static_cast<unsigned long long>(q) << 62)) >> 32);
   float s, c;
-  sincospif(static_cast<float>(rest) * 0x1p-63f, &s, &c);  // pi * (2 * turns), |.| <= pi / 4
+  sincospif(static_cast<float>(rest) * 0x1p-31f, &s, &c);  // pi * (2 * turns), |.| <= pi / 4
   const float x = (q & 1) ? s : c, y = (q & 1) ? c : s;
   return make_float2((q == 1 || q == 2) ? -x : x, (q >= 2) ? -y : y);
 }
 
-__global__ void __launch_bounds__(256) rope_table_kernel(float2* table, int64_t entries, int pairs,
-                                                         float amplitude,
-                                                         const __grid_constant__ RopeTurns turns) {
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < entries; e += step) {
-    const int64_t p = e / pairs;
-    const int i = static_cast<int>(e - p * pairs);
-    float2 v = cos_sin_turn(static_cast<unsigned long long>(p) * turns.t[i]);
+__global__ void __launch_bounds__(kThreads) rope_table_kernel(float2* table, int64_t positions, int pairs,
+                                                              float amplitude,
+                                                              const __grid_constant__ RopeTurns turns) {
+  const int rows = kThreads / pairs;  // runs of positions per CTA and step
+  const int r = threadIdx.x / pairs, i = threadIdx.x - r * pairs;
+  if (r >= rows) return;
+  const unsigned long long t = turns.t[i];
+  float2 fine[kRun];
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) fine[k] = cos_sin_turn(k * t);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows * kRun;
+  for (int64_t p = (static_cast<int64_t>(blockIdx.x) * rows + r) * kRun; p < positions; p += step) {
+    float2 v = cos_sin_turn(static_cast<unsigned long long>(p) * t);
     v.x *= amplitude;
     v.y *= amplitude;
-    table[e] = v;
+    float2* dst = table + p * pairs + i;
+    const int n = static_cast<int>(min(positions - p, static_cast<int64_t>(kRun)));
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const float c = v.x * fine[k].x - v.y * fine[k].y, s = v.y * fine[k].x + v.x * fine[k].y;
+      if (k < n) dst[k * pairs] = make_float2(c, s);
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_rope_table(float* table, int64_t num_positions, int pairs, float amplitude,
-                              const RopeTurns& turns, cudaStream_t st) {
-  const int64_t entries = num_positions * pairs;
-  const int64_t want = (entries + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(want < 65536 ? want : 65536);
-  rope_table_kernel<<<grid, 256, 0, st>>>(reinterpret_cast<float2*>(table), entries, pairs, amplitude, turns);
+                              const RopeTurns& turns, cudaStream_t st, int num_sms) {
+  const int64_t per = static_cast<int64_t>(kThreads / pairs) * kRun;
+  const int64_t want = (num_positions + per - 1) / per;
+  const int64_t most = 8ll * num_sms;  // resident CTAs
+  rope_table_kernel<<<static_cast<unsigned>(want < most ? want : most), kThreads, 0, st>>>(
+      reinterpret_cast<float2*>(table), num_positions, pairs, amplitude, turns);
   return cudaGetLastError();
 }
 

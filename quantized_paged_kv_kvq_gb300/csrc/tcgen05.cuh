@@ -21,7 +21,6 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // One lane of the (converged) warp, the same at every call: 1 there, 0 elsewhere.
 __device__ __forceinline__ uint32_t elect_lane() {
@@ -65,6 +64,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t* r, uint32_t addr) {
       : KVQ_R8(r, 0), KVQ_R8(r, 8)
       : "r"(addr));
 }
+// Waits for this warp's loads; the loaded registers pass through, so that no use
+// of them can be moved before it.
+#define KVQ_P8(r, i) \
+  "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : KVQ_P8(r, 0), KVQ_P8(r, 8), KVQ_P8(r, 16), KVQ_P8(r, 24) : : "memory");
+}
+// The same for loads that an earlier wait has covered.
+__device__ __forceinline__ void tmem_waited32(uint32_t* r) {
+  asm volatile("" : KVQ_P8(r, 0), KVQ_P8(r, 8), KVQ_P8(r, 16), KVQ_P8(r, 24));
+}
+#undef KVQ_P8
 #undef KVQ_R8
 #undef KVQ_W8
 

@@ -140,8 +140,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle (current_stream() would wrap it first, 3 us)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -359,32 +359,41 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _tensor(name: str, t: torch.Tensor, dtype: torch.dtype, shape, contiguous: bool = True) -> None:
-    """A CUDA tensor of the current device with this dtype and shape (None: any extent)."""
-    _need(t.is_cuda and t.device.index == torch.cuda.current_device(),
-          f"{name} must be on the current CUDA device")
-    _need(t.dtype == dtype, f"{name} must be {dtype}")
-    _need(t.dim() == len(shape) and all(e is None or e == n for e, n in zip(shape, t.shape)),
-          f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _need(not contiguous or t.is_contiguous(), f"{name} must be contiguous")
+def _tensors(*specs) -> None:
+    """Each (name, tensor, dtype, shape): a contiguous CUDA tensor of the current device.
+    One pass of cheap comparisons: these calls take a few microseconds on the GPU, and
+    the checks run before each of them."""
+    dev = torch.cuda.current_device()
+    for name, t, dtype, shape in specs:
+        if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA "
+                             f"device {dev}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def _rows(name: str, t: torch.Tensor, shape) -> int:
     """Checks bf16 [T, heads, D] rows with a free token stride; returns that stride."""
-    _tensor(name, t, torch.bfloat16, shape, contiguous=False)
-    heads, d = t.shape[1:]
-    _need(t.numel() == 0 or ((d == 1 or t.stride(2) == 1) and (heads == 1 or t.stride(1) == d)),
-          f"{name}: heads and elements must be contiguous")
+    n, heads, d = shape
+    if t.get_device() != torch.cuda.current_device() or t.dtype is not torch.bfloat16 or t.shape != shape:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on the current CUDA device, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+        if t.numel():
+            raise ValueError(f"{name}: heads and elements must be contiguous, got strides {t.stride()}")
     # one token: any stride serves, and torch may report one that is too small
-    return t.stride(0) if t.shape[0] > 1 else (heads * d + 7) // 8 * 8
+    return s0 if n > 1 else (heads * d + 7) // 8 * 8
 
 
 def _workspace(workspace: Optional[torch.Tensor]) -> int:
     if workspace is None:
         return 0
-    _need(workspace.is_cuda and workspace.device.index == torch.cuda.current_device()
-          and workspace.is_contiguous(), "workspace must be contiguous, on the current CUDA device")
+    _need(workspace.get_device() == torch.cuda.current_device() and workspace.is_contiguous(),
+          "workspace must be contiguous, on the current CUDA device")
     return workspace.numel() * workspace.element_size()
+
+
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def kvq_plan_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
@@ -398,22 +407,18 @@ def kvq_plan_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tabl
     (int64 [T]) and positions (int32 [T]) describe the packed new tokens (slot -1 behind
     the last), context_lens_out (int32 [S]), cu_new (int32 [S+1]) and free_range_out
     (int32 [2]) the state after the step."""
-    s, t = context_lens.numel(), slot_mapping.numel()
-    _tensor("context_lens", context_lens, torch.int32, (s,))
-    _tensor("new_lens", new_lens, torch.int32, (s,))
-    _tensor("block_table", block_table, torch.int32, (s, None))
-    _tensor("free_blocks", free_blocks, torch.int32, (None,))
-    _tensor("free_range", free_range, torch.int32, (2,))
-    _tensor("slot_mapping", slot_mapping, torch.int64, (t,))
-    _tensor("positions", positions, torch.int32, (t,))
-    _tensor("context_lens_out", context_lens_out, torch.int32, (s,))
-    _tensor("cu_new", cu_new, torch.int32, (s + 1,))
-    _tensor("free_range_out", free_range_out, torch.int32, (2,))
+    s, t, i32 = context_lens.numel(), slot_mapping.numel(), torch.int32
+    width, free = block_table.shape[-1], free_blocks.numel()
+    _tensors(("context_lens", context_lens, i32, (s,)), ("new_lens", new_lens, i32, (s,)),
+             ("block_table", block_table, i32, (s, width)), ("free_blocks", free_blocks, i32, (free,)),
+             ("free_range", free_range, i32, (2,)), ("slot_mapping", slot_mapping, torch.int64, (t,)),
+             ("positions", positions, i32, (t,)), ("context_lens_out", context_lens_out, i32, (s,)),
+             ("cu_new", cu_new, i32, (s + 1,)), ("free_range_out", free_range_out, i32, (2,)))
     st = load_library().kvq_plan_step(
-        _ptr(context_lens), _ptr(new_lens), s, _ptr(block_table), block_table.shape[1], block_size,
-        num_blocks, _ptr(free_blocks), free_blocks.numel(), _ptr(free_range), _ptr(slot_mapping),
-        _ptr(positions), t, _ptr(context_lens_out), _ptr(cu_new), _ptr(free_range_out),
-        _stream(stream))
+        context_lens.data_ptr(), new_lens.data_ptr(), s, block_table.data_ptr(), width, block_size,
+        num_blocks, free_blocks.data_ptr(), free, free_range.data_ptr(), slot_mapping.data_ptr(),
+        positions.data_ptr(), t, context_lens_out.data_ptr(), cu_new.data_ptr(),
+        free_range_out.data_ptr(), _stream(stream))
     _check(st, "kvq_plan_step")
 
 
@@ -432,14 +437,16 @@ class RopeScaling:
 def kvq_rope_table(table: torch.Tensor, base: float, scaling: Optional[RopeScaling] = None,
                    stream=None) -> torch.Tensor:
     """table (fp32 [positions, rot_dim / 2, 2]) <- cos and sin of every position and pair."""
-    _tensor("table", table, torch.float32, (None, None, 2))
+    _need(table.dim() == 3, "table must have shape (positions, rot_dim / 2, 2)")
+    n, pairs = table.shape[:2]
+    _tensors(("table", table, torch.float32, (n, pairs, 2)))
     sc = None
     if scaling is not None:
         sc = ctypes.byref(_RopeScaling(ROPE_KIND[scaling.kind], scaling.factor,
                                        scaling.original_len, scaling.low, scaling.high,
                                        scaling.amplitude))
-    st = load_library().kvq_rope_table(_ptr(table), table.shape[0], 2 * table.shape[1], float(base),
-                                       sc, _stream(stream))
+    st = load_library().kvq_rope_table(table.data_ptr(), n, 2 * pairs, float(base), sc,
+                                       _stream(stream))
     _check(st, "kvq_rope_table")
     return table
 
@@ -457,17 +464,17 @@ class Rope:
     weight_offset: float = 0.0
 
     def desc(self, head_dim: int) -> _RopeDesc:
-        rot, count = 0, 0
-        if self.table is not None:
-            _tensor("table", self.table, torch.float32, (None, None, 2))
-            rot, count = 2 * self.table.shape[1], self.table.shape[0]
-        for name in ("q_weight", "k_weight"):
-            if getattr(self, name) is not None:
-                _tensor(name, getattr(self, name), torch.bfloat16, (head_dim,))
-        ptr = lambda t: None if t is None else t.data_ptr()
-        return _RopeDesc(head_dim, rot, int(self.interleaved), float(self.eps),
-                         float(self.weight_offset), ptr(self.q_weight), ptr(self.k_weight),
-                         ptr(self.table), count)
+        rot, count, table = 0, 0, self.table
+        if table is not None:
+            _need(table.dim() == 3, "table must have shape (positions, rot_dim / 2, 2)")
+            count, pairs = table.shape[:2]
+            rot = 2 * pairs
+            _tensors(("table", table, torch.float32, (count, pairs, 2)))
+        for name, w in (("q_weight", self.q_weight), ("k_weight", self.k_weight)):
+            if w is not None:
+                _tensors((name, w, torch.bfloat16, (head_dim,)))
+        return _RopeDesc(head_dim, rot, self.interleaved, self.eps, self.weight_offset,
+                         _address(self.q_weight), _address(self.k_weight), _address(table), count)
 
 
 def kvq_norm_rope(rope: Rope, query: torch.Tensor, key: torch.Tensor, positions: torch.Tensor,
@@ -475,14 +482,14 @@ def kvq_norm_rope(rope: Rope, query: torch.Tensor, key: torch.Tensor, positions:
     """query_out, key_out <- normalised and rotated query [T, Hq, D] and key [T, Hkv, D]
     (bf16, token strides free; an output may be its own input)."""
     t, hq, d = query.shape
-    hkv = key.shape[1]
-    qs, ks = _rows("query", query, (t, hq, d)), _rows("key", key, (t, hkv, d))
-    qos, kos = _rows("query_out", query_out, (t, hq, d)), _rows("key_out", key_out, (t, hkv, d))
-    _tensor("positions", positions, torch.int32, (t,))
+    q, kv = (t, hq, d), (t, key.shape[1], d)
+    qs, ks = _rows("query", query, q), _rows("key", key, kv)
+    qos, kos = _rows("query_out", query_out, q), _rows("key_out", key_out, kv)
+    _tensors(("positions", positions, torch.int32, (t,)))
     r = rope.desc(d)
-    st = load_library().kvq_norm_rope(ctypes.byref(r), _ptr(query_out), qos, _ptr(key_out), kos,
-                                      _ptr(query), qs, _ptr(key), ks, _ptr(positions), t, hq, hkv,
-                                      _stream(stream))
+    st = load_library().kvq_norm_rope(ctypes.byref(r), query_out.data_ptr(), qos, key_out.data_ptr(),
+                                      kos, query.data_ptr(), qs, key.data_ptr(), ks,
+                                      positions.data_ptr(), t, hq, kv[1], _stream(stream))
     _check(st, "kvq_norm_rope")
 
 
@@ -491,17 +498,17 @@ def kvq_norm_rope_write(rope: Rope, cache: KVCache, query: torch.Tensor, key: to
                         query_out: torch.Tensor, stream=None) -> torch.Tensor:
     """kvq_norm_rope of the queries into query_out, and of the keys straight into the
     cache, together with the values, at slot_mapping (int64 [T])."""
-    t, hq, d = query.shape
-    kv = (t, cache.num_kv_heads, cache.head_dim)
-    qs, qos = _rows("query", query, (t, hq, cache.head_dim)), _rows("query_out", query_out, (t, hq, d))
+    t, hq, _ = query.shape
+    d = cache.head_dim
+    q, kv = (t, hq, d), (t, cache.num_kv_heads, d)
+    qs, qos = _rows("query", query, q), _rows("query_out", query_out, q)
     ks, vs = _rows("key", key, kv), _rows("value", value, kv)
-    _tensor("positions", positions, torch.int32, (t,))
-    _tensor("slot_mapping", slot_mapping, torch.int64, (t,))
+    _tensors(("positions", positions, torch.int32, (t,)), ("slot_mapping", slot_mapping, torch.int64, (t,)))
     r, c = rope.desc(d), cache.desc()
     st = load_library().kvq_norm_rope_write(
-        ctypes.byref(r), ctypes.byref(c), _ptr(cache.k_cache), _ptr(cache.v_cache), _ptr(query_out),
-        qos, _ptr(query), qs, _ptr(key), ks, _ptr(value), vs, _ptr(positions), _ptr(slot_mapping),
-        t, hq, _stream(stream))
+        ctypes.byref(r), ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(),
+        query_out.data_ptr(), qos, query.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
+        positions.data_ptr(), slot_mapping.data_ptr(), t, hq, _stream(stream))
     _check(st, "kvq_norm_rope_write")
     return query_out
 
@@ -514,11 +521,11 @@ def kvq_decode_window(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
                       new_value: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """kvq_paged_decode (or, with new_key / new_value, kvq_decode_append) of queries that
     see the last `window` tokens of their context and its first num_sinks."""
-    s, hq, d = query.shape
-    _tensor("query", query, torch.bfloat16, (s, hq, cache.head_dim))
-    _tensor("out", out, torch.bfloat16, (s, hq, d))
-    _tensor("block_table", block_table, torch.int32, (s, None))
-    _tensor("context_lens", context_lens, torch.int32, (s,))
+    s, hq, _ = query.shape
+    rows, width = (s, hq, cache.head_dim), block_table.shape[-1]
+    _tensors(("query", query, torch.bfloat16, rows), ("out", out, torch.bfloat16, rows),
+             ("block_table", block_table, torch.int32, (s, width)),
+             ("context_lens", context_lens, torch.int32, (s,)))
     _need((new_key is None) == (new_value is None), "new_key and new_value come together")
     ks = vs = 0
     if new_key is not None:
@@ -526,10 +533,10 @@ def kvq_decode_window(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
         ks, vs = _rows("new_key", new_key, kv), _rows("new_value", new_value, kv)
     c = cache.desc()
     st = load_library().kvq_decode_window(
-        ctypes.byref(c), _ptr(cache.k_cache), _ptr(cache.v_cache), _ptr(new_key), _ptr(new_value),
-        ks, vs, _ptr(out), _ptr(query), s, hq, _ptr(block_table), block_table.shape[1],
-        _ptr(context_lens), max_context_len, float(sm_scale), window, num_sinks, num_ctas,
-        _ptr(workspace), _workspace(workspace), _stream(stream))
+        ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), _address(new_key),
+        _address(new_value), ks, vs, out.data_ptr(), query.data_ptr(), s, hq, block_table.data_ptr(),
+        width, context_lens.data_ptr(), max_context_len, float(sm_scale), window, num_sinks, num_ctas,
+        _address(workspace), _workspace(workspace), _stream(stream))
     _check(st, "kvq_decode_window")
     return out
 
@@ -553,18 +560,18 @@ def kvq_paged_prefill(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
     rows cu_query[s]..cu_query[s+1]-1 are sequence s's last positions) to its cached context
     of context_lens[s] tokens, causal, through `window` (0: no limit) and num_sinks."""
     s = context_lens.numel()
-    n, hq, d = query.shape
-    _tensor("query", query, torch.bfloat16, (n, hq, cache.head_dim))
-    _tensor("out", out, torch.bfloat16, (n, hq, d))
-    _tensor("cu_query", cu_query, torch.int32, (s + 1,))
-    _tensor("block_table", block_table, torch.int32, (s, None))
-    _tensor("context_lens", context_lens, torch.int32, (s,))
+    n, hq, _ = query.shape
+    rows, width = (n, hq, cache.head_dim), block_table.shape[-1]
+    _tensors(("query", query, torch.bfloat16, rows), ("out", out, torch.bfloat16, rows),
+             ("cu_query", cu_query, torch.int32, (s + 1,)),
+             ("block_table", block_table, torch.int32, (s, width)),
+             ("context_lens", context_lens, torch.int32, (s,)))
     c = cache.desc()
     st = load_library().kvq_paged_prefill(
-        ctypes.byref(c), _ptr(cache.k_cache), _ptr(cache.v_cache), _ptr(out), _ptr(query),
-        _ptr(cu_query), s, n, max_query_len, hq, _ptr(block_table), block_table.shape[1],
-        _ptr(context_lens), max_context_len, float(sm_scale), window, num_sinks, _ptr(workspace),
-        _workspace(workspace), _stream(stream))
+        ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), out.data_ptr(),
+        query.data_ptr(), cu_query.data_ptr(), s, n, max_query_len, hq, block_table.data_ptr(), width,
+        context_lens.data_ptr(), max_context_len, float(sm_scale), window, num_sinks,
+        _address(workspace), _workspace(workspace), _stream(stream))
     _check(st, "kvq_paged_prefill")
     return out
 
