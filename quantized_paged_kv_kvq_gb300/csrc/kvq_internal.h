@@ -155,7 +155,7 @@ struct NormRopeArgs {
   int interleaved;
   float eps;
   float weight_offset;
-  int q_items, kv_items, items_per_token;  // warps per token (set by the launcher)
+  int q_items, kv_items;  // warps per token and kind (set by the launcher)
   const int64_t* slot_mapping;
   uint8_t* k_cache;
   uint8_t* v_cache;
