@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kKeys = 128;            // keys per tile
 constexpr int kProducers = 128;       // threads that load and dequantize K; as many for V
-constexpr int kSpin = 1 << 22;        // polls of an mbarrier before giving up
+constexpr int kSpin = 1 << 18;        // polls of an mbarrier before giving up (some seconds)
 constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is not raised: p <= 2^8
 
 template <int D_, int NW_>  // head_dim, softmax warpgroups
@@ -62,10 +62,11 @@ struct Cfg {
   static constexpr int CTRL = META + (AHEAD_K + AHEAD_V) * 3 * kKeys * 2;
   static constexpr int SIGNS = CTRL + 256;  // the rotation's diagonal as masks of pairs of sign bits
   static constexpr int SMEM = SIGNS + 2 * D + 1024;
-  // tensor memory columns
-  static constexpr uint32_t S(int w) { return w * 128; }
-  static constexpr uint32_t O(int w) { return NW * 128 + w * 128; }
-  static constexpr uint32_t TMEM = NW == 2 ? 512 : 256;
+  // tensor memory columns: two score buffers (one per warpgroup, or the two that one
+  // warpgroup's tiles take in turn), then the accumulators
+  static constexpr uint32_t S(int b) { return b * 128; }
+  static constexpr uint32_t O(int w) { return 256 + w * 128; }
+  static constexpr uint32_t TMEM = 512;
   // registers per thread of the softmax, producer and issuing warpgroups: together
   // no more than the block is launched with (96 or 128 each)
   static constexpr int R_SOFTMAX = NW == 2 ? 144 : 192;
@@ -75,7 +76,7 @@ struct Cfg {
 
 // Control words in shared memory.
 struct Ctrl {
-  unsigned long long q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drained;
+  unsigned long long q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done, o_full[2], drained;
   uint32_t tmem;
   int abort;
   int seq, tile, q0, q, n;  // this CTA's rows
@@ -414,7 +415,7 @@ struct Producer {
     for (int j = 0; j < P::OUT; ++j) to[j] = chunk_addr(dst, p.row0, p.chunk * P::OUT + j);
     uint32_t nf[2] = {0u, 0u};
     float largest = 0.f;
-    constexpr int U = P::PASSES < 4 || is_asym(F) ? 2 : 4;  // pieces in flight
+    constexpr int U = P::PASSES < 4 || F == INT4A ? 2 : 4;  // pieces in flight
 #pragma unroll 1
     for (int i0 = 0; i0 < P::PASSES; i0 += U) {
       uint4 w[U];
@@ -778,6 +779,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
       mbar_init(bar(&ctrl->p_full[i]), 4);
       mbar_init(bar(&ctrl->o_full[i]), 1);
     }
+    mbar_init(bar(&ctrl->pv_done), 1);
     mbar_init(bar(&ctrl->drained), 1);
     ctrl->abort = 0;
     ctrl->bad_lo = 0x7fffffff;
@@ -815,7 +817,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
     const bool active = wg < nw && nk > 0;
     const RowMap map(a, ctrl->q0, h, min(R0 + 32 * warp, R1 - 1));
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t s_addr = tmem + C::S(wg) + lane_base, o_addr = tmem + C::O(wg) + lane_base;
+    const uint32_t s_first = tmem + C::S(wg) + lane_base, o_addr = tmem + C::O(wg) + lane_base;
     if (active) {
       load_queries<D>(a, base + C::Q + wg * C::TILE, base + C::SIGNS, 32 * (warp & 3), R0 + 32 * warp, R1, map, turn, bf,
                       lane);
@@ -825,7 +827,11 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
       const int p_last = n - q + (min(R0 + 128 * (wg + 1), R1) - 1) / a.gqa;  // this warpgroup's last position
       const int p_first = n - q + (R0 + 128 * wg) / a.gqa;
       for (int i = 0; i < nk; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->s_full[wg]), i & 1, kSpin, abort))) {
+        // Two warpgroups have a score buffer each, one has both in turn, with a barrier
+        // each way for either: its warps may be a tile apart.
+        const int buf = NW == 2 ? wg : i & 1;
+        const uint32_t s_addr = NW == 2 ? s_first : s_first + buf * 128;
+        if (!__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->s_full[buf]), (NW == 2 ? i : i >> 1) & 1, kSpin, abort))) {
           give_up();
           break;
         }
@@ -844,15 +850,23 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
           const float f = up == -INFINITY ? 1.f : fast_exp2(m - up);
           m = up;
           l *= f;
-          // the products so far are done: S of this tile was issued behind them
-          if (i > 0) scale_columns(o_addr, D, f);
+          if (i > 0) {
+            // The products so far are done: with two warpgroups S of this tile was issued
+            // behind them; else they are waited for.
+            if (NW == 1 && !__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->pv_done), (i - 1) & 1, kSpin, abort))) {
+              give_up();
+              break;
+            }
+            tc_fence_after();
+            scale_columns(o_addr, D, f);
+          }
         }
         const float off = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every p is 0
         l += bf ? probabilities<true>(s_addr, scale, off) : probabilities<false>(s_addr, scale, off);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(&ctrl->p_full[wg]));
+        if (lane == 0) mbar_arrive(bar(&ctrl->p_full[buf]));
       }
     }
     // ---- the row's result
@@ -1021,49 +1035,65 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
         give_up();
         return false;
       };
-      auto scores = [&](int w, int stage) {  // S_w = Q_w K^T
+      auto scores = [&](int w, int buf, int stage) {  // S = Q_w K^T
         const uint64_t qa = q_op + w * (C::TILE >> 4), ka = k_op + stage * (C::TILE >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const int o = ((k >> 2) * C::GROUP_BYTES + (k & 3) * 32) >> 4;
-          mma_ss(leader, tm + C::S(0) + w * 128, qa + o, ka + o, qk_desc, k > 0);
+          mma_ss(leader, tm + C::S(0) + buf * 128, qa + o, ka + o, qk_desc, k > 0);
         }
-        tc_commit(leader, bar(&ctrl->s_full[w]));
+        tc_commit(leader, bar(&ctrl->s_full[buf]));
       };
-      auto values = [&](int w, int stage, bool add) {  // O_w += P_w V
+      auto values = [&](int w, int buf, int stage, bool add) {  // O_w += P V
         const uint64_t va = v_op + stage * (C::TILE >> 4);
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(leader, tm + C::O(0) + w * 128, tm + C::S(0) + w * 128 + 8 * k, va + k * (2048 >> 4), pv_desc,
+          mma_ts(leader, tm + C::O(0) + w * 128, tm + C::S(0) + buf * 128 + 8 * k, va + k * (2048 >> 4), pv_desc,
                  add || k > 0);
       };
+      // Products run in the order of their issue, so scores that overwrite
+      // probabilities only need to be issued behind the products that read them.
       bool ok = wait(&ctrl->q_full, 0) && wait(&ctrl->k_full[0], 0);
       if (ok) {
         tc_fence_after();
-        for (int w = 0; w < halves; ++w) scores(w, 0);
+        for (int w = 0; w < halves; ++w) scores(w, w, 0);
         tc_commit(leader, bar(&ctrl->k_empty[0]));
       }
       for (int i = 0; ok && i < tiles; ++i) {
         const int st = i & 1, ns = (i + 1) & 1;
+        if (NW == 1) {  // the next tile's scores, into the other buffer, ahead of this one's probabilities
+          if (i + 1 < tiles) {
+            ok = wait(&ctrl->k_full[ns], ((i + 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            scores(0, ns, ns);
+            tc_commit(leader, bar(&ctrl->k_empty[ns]));
+          }
+          ok = wait(&ctrl->v_full[st], (i >> 1) & 1) && wait(&ctrl->p_full[st], (i >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          values(0, st, st, i > 0);
+          tc_commit(leader, bar(&ctrl->v_empty[st]));
+          tc_commit(leader, bar(i + 1 < tiles ? &ctrl->pv_done : &ctrl->o_full[0]));
+          continue;
+        }
         ok = wait(&ctrl->v_full[st], (i >> 1) & 1);
         for (int w = 0; ok && w < halves; ++w) {
           ok = wait(&ctrl->p_full[w], i & 1);
           if (!ok) break;
           tc_fence_after();
-          values(w, st, i > 0);
+          values(w, w, st, i > 0);
           if (w == halves - 1) tc_commit(leader, bar(&ctrl->v_empty[st]));
-          // products run in the order of their issue, so these scores overwrite
-          // the probabilities only once they are read
           if (i + 1 < tiles) {
             if (w == 0) ok = wait(&ctrl->k_full[ns], ((i + 1) >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            scores(w, ns);
+            scores(w, w, ns);
           } else {
             tc_commit(leader, bar(&ctrl->o_full[w]));
           }
         }
-        if (ok && i + 1 < tiles) tc_commit(leader, bar(&ctrl->k_empty[ns]));
+        if (NW == 2 && ok && i + 1 < tiles) tc_commit(leader, bar(&ctrl->k_empty[ns]));
       }
       if (!ok) {  // leave with nothing in flight
         tc_commit(leader, bar(&ctrl->drained));

@@ -74,6 +74,12 @@ def test_long_contexts(fmt):
     check(fmt, [1500], [700], 1, 4, 128, 16)
 
 
+def test_more_tiles_than_the_device_holds_at_once():
+    """Short chunks over long contexts, several waves of CTAs: every warp's pace differs."""
+    lens = np.random.default_rng(3).integers(600, 1500, 48)
+    check("int8", lens, np.random.default_rng(4).integers(1, 4, 48), 8, 2, 64, 16)
+
+
 def test_large_logits():
     """Keys whose logits span hundreds: the running maximum moves by more than any fixed range."""
     check("bf16", [400], [130], 1, 4, 128, 16, k_std=20.0)
