@@ -885,8 +885,8 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
   a.max_query_len = max_query_len;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.max_context_len = max_context_len;
-  a.window = window;
-  a.sinks = num_sinks;
+  a.window = std::min(window, 1 << 30);  // contexts are no longer
+  a.sinks = std::min(num_sinks, 1 << 30);
   a.rows_per_tile = sh.rows;
   a.tiles = sh.tiles;
   a.num_splits = sh.splits;

@@ -69,8 +69,8 @@ struct Cfg {
   static constexpr uint32_t TMEM = 512;
   // registers per thread of the softmax, producer and issuing warpgroups: together
   // no more than the block is launched with (96 or 128 each)
-  static constexpr int R_SOFTMAX = NW == 2 ? 144 : 192;
-  static constexpr int R_PRODUCE = NW == 2 ? 72 : 104;
+  static constexpr int R_SOFTMAX = NW == 2 ? 128 : 192;
+  static constexpr int R_PRODUCE = NW == 2 ? 88 : 104;
   static constexpr int R_ISSUE = NW == 2 ? 48 : 64;
 };
 
@@ -80,11 +80,12 @@ struct Ctrl {
   uint32_t tmem;
   int abort;
   int seq, tile, q0, q, n;  // this CTA's rows
-  int scan[16];
+  int scan[20];  // a word per warp of the block
   int bad_lo, bad_hi;  // tiles with values that are not finite
 };
 
 static_assert(sizeof(Ctrl) <= 256, "control words");
+static_assert(Cfg<128, 2>::THREADS <= 32 * 20, "a scan word per warp");
 
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
