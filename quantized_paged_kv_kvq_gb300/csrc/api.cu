@@ -256,8 +256,14 @@ struct PrefillShape {
   int tiles = 0;            // row tiles, of all sequences, that the batch may need
   int splits = 1;
   size_t partial_rows = 0;  // rows of partial results in the workspace
+  int staged_len = 0;       // positions of a context dequantized ahead (0: not ahead)
+  size_t staged = 0;        // bytes of those, and of the flags behind them
   size_t workspace = 0;
 };
+// Dequantizing ahead pays where each key is read by this many row tiles on average,
+// and is done in at most this much workspace.
+constexpr int kStageTiles = 4;
+constexpr int64_t kStageBytes = 16ll << 30;
 kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
                          int64_t total_q, int32_t max_query_len, int32_t max_context_len,
                          PrefillShape* sh) {
@@ -287,6 +293,13 @@ kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
   if (sh->splits > 1) {
     sh->partial_rows = static_cast<size_t>(sh->splits) * tiles * hkv * sh->rows;
     sh->workspace = sh->partial_rows * (c->head_dim + 2) * sizeof(float);
+  }
+  const int64_t len = (max_context_len + 127ll) / 128 * 128, rows = num_seqs * hkv * len;
+  if (sh->rows == 256 && total_q * g >= kStageTiles * 256ll * num_seqs && 2 * rows <= INT32_MAX &&
+      num_seqs * (len / 128) <= INT32_MAX && hkv <= 65535 && 2 * rows * c->head_dim * 2 <= kStageBytes) {
+    sh->staged_len = static_cast<int>(len);
+    sh->staged = (static_cast<size_t>(2 * rows) * c->head_dim * 2 + rows / 128 + 15) / 16 * 16;
+    sh->workspace += sh->staged;
   }
   return KVQ_OK;
 }
@@ -890,8 +903,12 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
   a.rows_per_tile = sh.rows;
   a.tiles = sh.tiles;
   a.num_splits = sh.splits;
-  a.ws_out = static_cast<float*>(workspace);
-  a.ws_ml = sh.workspace ? a.ws_out + sh.partial_rows * cache->head_dim : nullptr;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.staged = sh.staged ? reinterpret_cast<uint16_t*>(ws) : nullptr;
+  a.staged_len = sh.staged_len;
+  a.staged_bad = ws + static_cast<size_t>(2) * num_seqs * cache->num_kv_heads * sh.staged_len * cache->head_dim * 2;
+  a.ws_out = reinterpret_cast<float*>(ws + sh.staged);
+  a.ws_ml = a.ws_out + sh.partial_rows * cache->head_dim;
   const cudaError_t e = launch_prefill(a, cache->head_dim, stream);
   if (e == cudaErrorNotSupported) return KVQ_ERR_UNSUPPORTED;
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

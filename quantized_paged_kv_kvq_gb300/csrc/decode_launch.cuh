@@ -3,27 +3,12 @@
 // head group merges its partitions).
 #pragma once
 
-#include <cudaTypedefs.h>
-
 #include <atomic>
 
 #include "decode.cuh"
+#include "tensor_map.cuh"
 
 namespace kvq {
-
-// cuTensorMapEncodeTiled, fetched once through the runtime (no libcuda link).
-inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
 
 inline CUtensorMapSwizzle swizzle_mode(int bits) {
   return bits == 3 ? CU_TENSOR_MAP_SWIZZLE_128B

@@ -213,6 +213,12 @@ struct PrefillArgs {
   int num_splits; // parts each row tile's keys are cut into
   float* ws_out;  // [splits, tiles, Hkv, rows, D] partial outputs
   float* ws_ml;   // [splits, tiles, Hkv, rows, 2]
+  // Contexts dequantized ahead (nullptr: each CTA dequantizes what it reads): 16-bit
+  // K rows [S, Hkv, staged_len, D], then V's, and a flag per (sequence, kv-head,
+  // 128 keys): values that are not finite.
+  uint16_t* staged;
+  uint8_t* staged_bad;
+  int staged_len;  // a multiple of 128
 };
 cudaError_t launch_prefill(const PrefillArgs& a, int head_dim, cudaStream_t st);
 

@@ -29,6 +29,7 @@
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 #include "tcgen05.cuh"
+#include "tensor_map.cuh"
 
 namespace kvq {
 
@@ -41,11 +42,11 @@ constexpr int kProducers = 128;       // threads that load and dequantize K; as 
 constexpr int kSpin = 1 << 18;        // polls of an mbarrier before giving up (some seconds)
 constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is not raised: p <= 2^8
 
-template <int D_, int NW_>  // head_dim, softmax warpgroups
+template <int D_, int NW_, bool STAGED = false>  // head_dim, softmax warpgroups, keys dequantized ahead
 struct Cfg {
   static constexpr int D = D_, NW = NW_;
   static constexpr int ROWS = 128 * NW;
-  static constexpr int THREADS = 128 * NW + 2 * kProducers + 128;
+  static constexpr int THREADS = 128 * NW + (STAGED ? 0 : 2 * kProducers) + 128;
   static constexpr int GROUPS = D / 64;              // 64-element column groups of an operand row
   static constexpr int GROUP_BYTES = 128 * 128;      // 128 rows of 128 bytes
   static constexpr int TILE = GROUPS * GROUP_BYTES;  // a 128-row operand
@@ -58,7 +59,7 @@ struct Cfg {
   static constexpr int K = Q + NW * TILE;
   static constexpr int V = K + 2 * TILE;
   static constexpr int RAWQ = V + 2 * TILE;
-  static constexpr int META = RAWQ + (AHEAD_K + AHEAD_V) * RAW;  // slots of K, then of V
+  static constexpr int META = RAWQ + (STAGED ? 0 : (AHEAD_K + AHEAD_V) * RAW);  // slots of K, then of V
   static constexpr int CTRL = META + (AHEAD_K + AHEAD_V) * 3 * kKeys * 2;
   static constexpr int SIGNS = CTRL + 256;  // the rotation's diagonal as masks of pairs of sign bits
   static constexpr int SMEM = SIGNS + 2 * D + 1024;
@@ -68,10 +69,10 @@ struct Cfg {
   static constexpr uint32_t O(int w) { return 256 + w * 128; }
   static constexpr uint32_t TMEM = 512;
   // registers per thread of the softmax, producer and issuing warpgroups: together
-  // no more than the block is launched with (96 or 128 each)
-  static constexpr int R_SOFTMAX = NW == 2 ? 128 : 192;
+  // no more than the block is launched with (96, 128 or, staged, 168 each)
+  static constexpr int R_SOFTMAX = STAGED ? 216 : NW == 2 ? 128 : 192;
   static constexpr int R_PRODUCE = NW == 2 ? 88 : 104;
-  static constexpr int R_ISSUE = NW == 2 ? 48 : 64;
+  static constexpr int R_ISSUE = STAGED ? 72 : NW == 2 ? 48 : 64;
 };
 
 // Control words in shared memory.
@@ -740,9 +741,10 @@ __device__ __forceinline__ void result_columns(uint32_t (&o)[32], uint32_t addr,
   }
 }
 
-template <int D, int NW>
-__global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
-  using C = Cfg<D, NW>;
+template <int D, int NW, bool STAGED>
+__global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
+    prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap map_staged) {
+  using C = Cfg<D, NW, STAGED>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzled tiles: 1024-byte aligned
   uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
@@ -772,8 +774,8 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
   if (tid == 0) {
     mbar_init(bar(&ctrl->q_full), 4 * nw);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(&ctrl->k_full[i]), kProducers / 32);
-      mbar_init(bar(&ctrl->v_full[i]), kProducers / 32);
+      mbar_init(bar(&ctrl->k_full[i]), STAGED ? 1 : kProducers / 32);
+      mbar_init(bar(&ctrl->v_full[i]), STAGED ? 1 : kProducers / 32);
       mbar_init(bar(&ctrl->k_empty[i]), 1);
       mbar_init(bar(&ctrl->v_empty[i]), 1);
       mbar_init(bar(&ctrl->s_full[i]), 1);
@@ -791,6 +793,15 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
     reinterpret_cast<uint32_t*>(smem + C::SIGNS)[tid] =
         a.signs == nullptr ? 0u : (a.signs[2 * tid] < 0 ? 0x8000u : 0u) | (a.signs[2 * tid + 1] < 0 ? 0x80000000u : 0u);
   __syncthreads();
+  const size_t seq_head = static_cast<size_t>(seq) * a.num_kv_heads + h;
+  if constexpr (STAGED) {  // tiles whose values were not all finite
+    for (int i = tid; i < nk; i += C::THREADS) {
+      if (a.staged_bad[seq_head * (a.staged_len / kKeys) + tile_key(span, i0 + i) / kKeys]) {
+        atomicMin(&ctrl->bad_lo, i0 + i);
+        atomicMax(&ctrl->bad_hi, i0 + i);
+      }
+    }
+  }
   if (nk > 0) {
     if (warp == kIssuer) tmem_alloc(bar(&ctrl->tmem), C::TMEM);
     tc_fence_before();
@@ -959,7 +970,7 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
           *reinterpret_cast<uint4*>(a.out + map(d) * D + 8 * sub) = ldsv4(mine_s + d * (D * 2) + ((sub ^ (d & 7)) << 4));
       }
     }
-  } else if (wg < NW + 2) {
+  } else if (!STAGED && wg < NW + 2) {
     // ================= producers =================
     reg_give<C::R_PRODUCE>();
     if (nk > 0) {
@@ -1023,6 +1034,38 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
   } else {
     // ================= products =================
     reg_give<C::R_ISSUE>();
+    if constexpr (STAGED) {
+      if (warp == kIssuer + 1 && lane == 0 && nk > 0) {
+        // K and V tiles from the staged context, a TMA box per 64 columns
+        const int rows = a.num_seqs * a.num_kv_heads * a.staged_len;  // of K; V's lie behind
+        const int row0 = static_cast<int>(seq_head) * a.staged_len;
+        int issued = 0;  // K and V tiles
+        bool ok = true;
+        for (; ok && issued < 2 * nk; ++issued) {
+          const int i = issued >> 1, st = i & 1;
+          const bool is_v = issued & 1;
+          if (i >= 2) ok = mbar_wait_or_abort(bar(is_v ? &ctrl->v_empty[st] : &ctrl->k_empty[st]), ((i >> 1) + 1) & 1, kSpin, abort);
+          if (!ok) break;
+          const uint32_t full = bar(is_v ? &ctrl->v_full[st] : &ctrl->k_full[st]);
+          const uint32_t dst = base + (is_v ? C::V : C::K) + st * C::TILE;
+          const int y = row0 + tile_key(span, i0 + i) + (is_v ? rows : 0);
+          mbar_arrive_expect(full, C::TILE);
+#pragma unroll
+          for (int g = 0; g < C::GROUPS; ++g)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                    dst + g * C::GROUP_BYTES),
+                "l"(reinterpret_cast<uint64_t>(&map_staged)), "r"(64 * g), "r"(y), "r"(full)
+                : "memory");
+        }
+        if (!ok) {
+          give_up();
+          for (int t = max(issued - 4, 0); t < issued; ++t)  // leave with no copy in flight
+            mbar_wait(bar((t & 1) ? &ctrl->v_full[t >> 1 & 1] : &ctrl->k_full[t >> 1 & 1]), (t >> 2) & 1, kSpin);
+        }
+      }
+      __syncwarp();
+    }
     if (warp == kIssuer && nk > 0) {
       // the same in every lane, and known as such
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -1109,6 +1152,109 @@ __global__ void __launch_bounds__(Cfg<D, NW>::THREADS, 1) prefill_kernel(const _
   if (nk > 0 && warp == kIssuer) tmem_dealloc(tmem, C::TMEM);
 }
 
+// The contexts' rows that some row of the batch sees as 16-bit operands in memory,
+// [S, Hkv, staged_len, D] of K and then of V, by whole tiles of 128 keys (rows that
+// no one sees are 0).  A CTA per (sequence, tile) and kv-head: half its threads K, half V.
+// Worth its writes where many row tiles read the same keys.
+template <int D, int F, bool KVARN, bool IS_V>
+__device__ __forceinline__ bool stage_tile(const PrefillArgs& a, const Source& s, const Span& span, const int* pages,
+                                           int t0, uint16_t* dst, int tid) {
+  using P = Pieces<F, D>;
+  const P p(tid);
+  const int mask = (1 << a.block_shift) - 1;
+  uint32_t nf = 0;
+  bool bad = false;
+#pragma unroll 2
+  for (int i = 0; i < P::PASSES; ++i) {
+    const int row = p.row0 + i * P::STEP, t = t0 + row;
+    const bool need = t <= span.p_hi && (t >= span.win || t < a.sinks);
+    const unsigned long long blk = static_cast<uint32_t>(pages[row >> a.block_shift]);
+    uint32_t o[4 * P::OUT];
+    const uint4 w = need ? ldg_stream16(s.codes + blk * s.page_bytes + (row & mask) * s.token_bytes + p.chunk * 16)
+                         : make_uint4(0, 0, 0, 0);
+    if constexpr (F == BF16) {
+      o[0] = w.x;
+      o[1] = w.y;
+      o[2] = w.z;
+      o[3] = w.w;
+    } else {
+      uint32_t f[3] = {0, 0, 0};
+      if (is_asym(F) && need) {
+        const __half* m = s.meta + blk * s.meta_page + (row & mask);
+#pragma unroll
+        for (int k = 0; k < (KVARN ? 3 : 2); ++k) {
+          const uint32_t x = __half_as_ushort(m[k << a.block_shift]);
+          f[k] = x | x << 16;
+        }
+      }
+      dequantize16<F, KVARN>(w, f[0], f[1], f[2], o);
+    }
+    if constexpr (IS_V && F != INT8) {
+      nf = track_not_finite<F == BF16>(0u, o);
+      if (nf & 0x7FFF7FFFu) {
+        bad = true;
+#pragma unroll
+        for (int e = 0; e < 4 * P::OUT; ++e) o[e] = finite_or_zero<F == BF16>(o[e]);
+      }
+    }
+    uint4* to = reinterpret_cast<uint4*>(dst + static_cast<size_t>(row) * D) + p.chunk * P::OUT;
+#pragma unroll
+    for (int j = 0; j < P::OUT; ++j) to[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+  }
+  return bad;
+}
+template <int D, bool IS_V>
+__device__ __forceinline__ bool stage_any(const PrefillArgs& a, const Source& s, const Span& span, const int* pages,
+                                          int t0, uint16_t* dst, int tid) {
+  switch (s.fmt) {
+    case INT8: return stage_tile<D, INT8, false, IS_V>(a, s, span, pages, t0, dst, tid);
+    case E4M3: return stage_tile<D, E4M3, false, IS_V>(a, s, span, pages, t0, dst, tid);
+    case E5M2: return stage_tile<D, E5M2, false, IS_V>(a, s, span, pages, t0, dst, tid);
+    case INT4A:
+      return s.fields == 3 ? stage_tile<D, INT4A, true, IS_V>(a, s, span, pages, t0, dst, tid)
+                           : stage_tile<D, INT4A, false, IS_V>(a, s, span, pages, t0, dst, tid);
+    case UINT8A:
+      return s.fields == 3 ? stage_tile<D, UINT8A, true, IS_V>(a, s, span, pages, t0, dst, tid)
+                           : stage_tile<D, UINT8A, false, IS_V>(a, s, span, pages, t0, dst, tid);
+    default: return stage_tile<D, BF16, false, IS_V>(a, s, span, pages, t0, dst, tid);
+  }
+}
+template <int D>
+__global__ void __launch_bounds__(2 * kProducers) stage_kernel(const __grid_constant__ PrefillArgs a) {
+  __shared__ int pages[kKeys / 8];
+  const int tiles = a.staged_len / kKeys, tid = threadIdx.x;
+  const int seq = blockIdx.x / tiles, tile = blockIdx.x - seq * tiles, h = blockIdx.y, t0 = tile * kKeys;
+  bool cut;
+  const int q = seq_rows(a, seq, cut).y, n = clamp_int(a.context_lens[seq], 0, a.max_context_len);
+  if (q == 0) return;
+  const Span span = row_span(a, n, q, 0, q * a.gqa);
+  if (t0 > span.p_hi || (t0 + kKeys <= span.win && t0 >= a.sinks)) return;  // no one reads it
+  const int bs = 1 << a.block_shift;
+  if (tid < (kKeys >> a.block_shift)) {
+    const int t = t0 + tid * bs;
+    int blk = 0;
+    if (t <= span.p_hi && (t + bs > span.win || t < a.sinks)) {
+      blk = a.block_table[static_cast<size_t>(seq) * a.max_blocks_per_seq + (t >> a.block_shift)];
+      if (blk < 0 || blk >= a.num_blocks) {
+        raise_error(2u);  // KVQ_DEVERR_BLOCK_RANGE: block 0 is read instead
+        blk = 0;
+      }
+    }
+    pages[tid] = blk;
+  }
+  __syncthreads();
+  const size_t seq_head = static_cast<size_t>(seq) * a.num_kv_heads + h;
+  const bool is_v = tid >= kProducers;
+  const size_t row = (is_v ? static_cast<size_t>(a.num_seqs) * a.num_kv_heads * a.staged_len : 0) + seq_head * a.staged_len + t0;
+  const Source s = is_v ? make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs)
+                        : make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
+  uint16_t* dst = a.staged + row * D;
+  const bool bad = is_v ? stage_any<D, true>(a, s, span, pages, t0, dst, tid & 127)
+                        : stage_any<D, false>(a, s, span, pages, t0, dst, tid & 127);
+  const int any = __syncthreads_or(bad);
+  if (tid == 0) a.staged_bad[seq_head * tiles + tile] = any != 0;
+}
+
 // Joins the splits' partial results: out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
 // A warp per row, D/32 consecutive elements per lane.
 template <int D>
@@ -1157,32 +1303,55 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs a, 
   }
 }
 
-template <int D, int NW>
+template <int D, int NW, bool STAGED>
 cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
-  using C = Cfg<D, NW>;
+  using C = Cfg<D, NW, STAGED>;
   static std::atomic<unsigned long long> attr_done{0};  // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
-    e = cudaFuncSetAttribute(prefill_kernel<D, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(prefill_kernel<D, NW, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
   }
+  CUtensorMap map;
+  memset(&map, 0, sizeof(map));
+  if constexpr (STAGED) {
+    const size_t rows = 2 * static_cast<size_t>(a.num_seqs) * a.num_kv_heads * a.staged_len;
+    const cuuint64_t dims[2] = {cuuint64_t(D), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(D) * 2};
+    const cuuint32_t box[2] = {64, kKeys}, estr[2] = {1, 1};
+    if (tensor_map_encoder() == nullptr ||
+        tensor_map_encoder()(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.staged, dims, strides, box, estr,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+    stage_kernel<D><<<dim3(static_cast<unsigned>(a.num_seqs) * (a.staged_len / kKeys), a.num_kv_heads, 1),
+                      2 * kProducers, 0, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   const dim3 grid(static_cast<unsigned>(a.tiles) * a.num_kv_heads, a.num_splits, 1);
-  prefill_kernel<D, NW><<<grid, C::THREADS, C::SMEM, st>>>(a);
+  prefill_kernel<D, NW, STAGED><<<grid, C::THREADS, C::SMEM, st>>>(a, map);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.num_splits == 1) return e;
   prefill_join_kernel<D><<<grid.x, 256, 0, st>>>(a, C::ROWS);
   return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t launch_d(const PrefillArgs& a, cudaStream_t st) {
+  if (a.rows_per_tile == 128) return launch_t<D, 1, false>(a, st);
+  return a.staged != nullptr ? launch_t<D, 2, true>(a, st) : launch_t<D, 2, false>(a, st);
+}
+
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillArgs& a, int head_dim, cudaStream_t st) {
-  if (head_dim == 64) return a.rows_per_tile == 128 ? launch_t<64, 1>(a, st) : launch_t<64, 2>(a, st);
-  if (head_dim == 128) return a.rows_per_tile == 128 ? launch_t<128, 1>(a, st) : launch_t<128, 2>(a, st);
+  if (head_dim == 64) return launch_d<64>(a, st);
+  if (head_dim == 128) return launch_d<128>(a, st);
   return cudaErrorNotSupported;
 }
 

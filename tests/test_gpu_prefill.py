@@ -148,10 +148,27 @@ def test_bad_pages_and_queries_are_flagged():
     assert torch.isfinite(out[0]).all() and torch.isfinite(out[2]).all()
 
 
+@pytest.mark.parametrize("fmt", sorted(FORMATS))
+@pytest.mark.parametrize("g,d,bs", [(4, 128, 16), (5, 64, 8), (8, 128, 128)])
+def test_contexts_dequantized_ahead(fmt, g, d, bs):
+    """Enough rows a sequence that the keys are dequantized once, ahead of the attention."""
+    check(fmt, [420, 700], [400, 300], 2, g, d, bs)
+    check(fmt, [600], [400], 1, g, d, bs, 100, 20)
+    check(fmt, [700], [260], 1, g, d, bs, 300, 130)
+
+
+@pytest.mark.parametrize("n,q", [(300, 300), (256, 256), (384, 257), (513, 300), (1000, 320)])
+def test_ahead_at_tile_edges(n, q):
+    check("int8", [n], [q], 1, 4, 64, 32)
+    check("uint8", [n], [q], 2, 8, 128, 16, 129, 1)
+    check("e4m3_int8", [n, 0, 40, 7], [q, 0, 40, 0], 1, 8, 64, 16, head_scales=True)
+
+
+@pytest.mark.parametrize("q", [100, 520])  # dequantized by each CTA, and ahead
 @pytest.mark.parametrize("fmt", ["e5m2", "bf16"])
-def test_values_not_finite(fmt):
+def test_values_not_finite(fmt, q):
     """A value that is not finite reaches the rows that see it and no others."""
-    p = Paged(fmt, [100], 2, 64, 16)
+    p = Paged(fmt, [q], 2, 64, 16)
     b = p.table[0, 60 // 16]
     if fmt == "bf16":
         p.cache.v_cache.view(torch.bfloat16)[b, 60 % 16, 0, 5] = float("inf")
@@ -159,8 +176,7 @@ def test_values_not_finite(fmt):
     else:
         p.cache.v_cache[b, 60 % 16, 0, 5] = 0x7C  # inf
         p.cache.v_cache[b, 60 % 16, 0, 9] = 0x7F  # NaN
-    q = random_query(100, 4, 64)
-    out = prefill(p, q, np.array([0, 100]))
+    out = prefill(p, random_query(q, 4, 64), np.array([0, q]))
     good = torch.isfinite(out)
     assert good[:60].all() and good[:, 2:].all()
     assert not good[60:, :2, 5].any() and not good[60:, :2, 9].any()
@@ -182,19 +198,32 @@ def test_nan_where_no_row_looks(fmt):
     q = random_query(10, 4, 64)
     ref, tol = p.expect(q, [0, 10], 0.125, 100, 3)
     check_close(prefill(p, q, np.array([0, 10]), 100, 3), ref, tol)
+    p = Paged(fmt, [900], 2, 64, 16)  # and ahead: rows 300 on, a window of 150 behind 20 kept
+    for t in range(20, 151):
+        blk = p.table[0, t // 16]
+        p.cache.k_cache[blk, t % 16] = 0xFF
+        p.cache.v_cache[blk, t % 16] = 0xFF
+        if p.cache.k_meta is not None:
+            for m in (p.cache.k_meta, p.cache.v_meta):
+                m[blk, :, :, t % 16] = float("nan")
+    q = random_query(600, 4, 64)
+    ref, tol = p.expect(q, [0, 600], 0.125, 150, 20)
+    check_close(prefill(p, q, np.array([0, 600]), 150, 20), ref, tol)
 
 
-def test_rows_repeat_and_streams_and_graphs():
-    p = Paged("kvarn", [260, 1000], 2, 128, 16)
-    cu = np.array([0, 100, 103])
-    q = random_query(103, 8, 128)
+@pytest.mark.parametrize("lens,counts", [([260, 1000], [100, 3]), ([700, 800], [500, 300])])
+def test_rows_repeat_and_streams_and_graphs(lens, counts):
+    p = Paged("kvarn", lens, 2, 128, 16)
+    cu = offsets(counts)
+    rows, most = sum(counts), max(counts)
+    q = random_query(rows, 8, 128)
     one = prefill(p, q, cu)
     assert torch.equal(bits(prefill(p, q, cu)), bits(one))  # no order of sums varies
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    n = kvq.kvq_prefill_workspace_size(p.cache, 2, 8, 103, 100, p.max_len)
+    n = kvq.kvq_prefill_workspace_size(p.cache, 2, 8, rows, most, p.max_len)
     ws, out, cut = garbage(n), torch.empty_like(q), ints(cu)
-    call = lambda: kvq.kvq_paged_prefill(p.cache, q, out, cut, p.block_table, p.context_lens, 100, p.max_len,
+    call = lambda: kvq.kvq_paged_prefill(p.cache, q, out, cut, p.block_table, p.context_lens, most, p.max_len,
                                          p.d ** -0.5, 0, 0, ws)
     with torch.cuda.stream(s):
         call()
@@ -204,7 +233,7 @@ def test_rows_repeat_and_streams_and_graphs():
     with torch.cuda.graph(g, stream=s):
         call()
     for i in range(3):
-        q.copy_(random_query(103, 8, 128, seed=30 + i))
+        q.copy_(random_query(rows, 8, 128, seed=30 + i))
         out.fill_(7.0)
         g.replay()
         torch.cuda.synchronize()
