@@ -260,9 +260,12 @@ struct PrefillShape {
   size_t staged = 0;        // bytes of those, and of the flags behind them
   size_t workspace = 0;
 };
-// Dequantizing ahead pays where each key is read by this many row tiles on average,
-// and is done in at most this much workspace.
-constexpr int kStageTiles = 4;
+// Dequantizing ahead pays where each key is read by this many row tiles (of 256) on
+// average, fewer where dequantizing costs more, and is done in at most 16 GiB.
+// Measured ahead / not, 32 / 8 heads of 128: int8, 8 x 4,096 keys: 4 row tiles 165 /
+// 148 us, 8 280 / 290, 1 x 8,192 keys and 32 tiles 245 / 275; KVarN, 16 x 4,096 keys:
+// 2 tiles 224 / 227, 8 x 4,096: 4 tiles 187 / 222, 8 311 / 427; bf16 as int8.
+constexpr int64_t stage_tiles(int fmt) { return is_asym(fmt) ? 3 : 8; }
 constexpr int64_t kStageBytes = 16ll << 30;
 kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
                          int64_t total_q, int32_t max_query_len, int32_t max_context_len,
@@ -295,7 +298,7 @@ kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
     sh->workspace = sh->partial_rows * (c->head_dim + 2) * sizeof(float);
   }
   const int64_t len = (max_context_len + 127ll) / 128 * 128, rows = num_seqs * hkv * len;
-  if (sh->rows == 256 && total_q * g >= kStageTiles * 256ll * num_seqs && 2 * rows <= INT32_MAX &&
+  if (sh->rows == 256 && total_q * g >= stage_tiles(c->k_fmt) * 256 * num_seqs && 2 * rows <= INT32_MAX &&
       num_seqs * (len / 128) <= INT32_MAX && hkv <= 65535 && 2 * rows * c->head_dim * 2 <= kStageBytes) {
     sh->staged_len = static_cast<int>(len);
     sh->staged = (static_cast<size_t>(2 * rows) * c->head_dim * 2 + rows / 128 + 15) / 16 * 16;

@@ -77,16 +77,14 @@ struct Cfg {
 
 // Control words in shared memory.
 struct Ctrl {
-  unsigned long long q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done, o_full[2], drained;
+  unsigned long long q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], pv_done, o_full[2], drained;
   uint32_t tmem;
   int abort;
   int seq, tile, q0, q, n;  // this CTA's rows
-  int scan[20];  // a word per warp of the block
   int bad_lo, bad_hi;  // tiles with values that are not finite
 };
 
 static_assert(sizeof(Ctrl) <= 256, "control words");
-static_assert(Cfg<128, 2>::THREADS <= 32 * 20, "a scan word per warp");
 
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
@@ -101,9 +99,10 @@ __device__ __forceinline__ int2 seq_rows(const PrefillArgs& a, int s, bool& bad)
 }
 
 // The sequence and row tile that tile number `want` (of all sequences, ROWS
-// rows each) is: a scan of the sequences' tile counts by the whole block.
+// rows each) is: a scan of the sequences' tile counts by the whole block (scan: a
+// word per warp).
 template <int ROWS>
-__device__ void find_tile(const PrefillArgs& a, Ctrl* c, int want) {
+__device__ void find_tile(const PrefillArgs& a, Ctrl* c, int* scan, int want) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   if (tid == 0) c->seq = -1;
   int before = 0;  // tiles of the sequences before the chunk
@@ -127,12 +126,12 @@ __device__ void find_tile(const PrefillArgs& a, Ctrl* c, int want) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) c->scan[warp] = incl;
+    if (lane == 31) scan[warp] = incl;
     __syncthreads();
     int first = before, total = 0;
     for (int w = 0; w < warps; ++w) {
-      if (w < warp) first += c->scan[w];
-      total += c->scan[w];
+      if (w < warp) first += scan[w];
+      total += scan[w];
     }
     first += incl - v;
     if (first <= want && want < first + v) {
@@ -533,9 +532,10 @@ __device__ __forceinline__ float largest_score(uint32_t s_addr) {
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 // p = 2^(s * scale + off) over the scores, as 16-bit pairs in their first half;
-// returns the sum (before that rounding).
+// returns the sum (before that rounding).  The first 64 are handed over (half_bar,
+// if not 0) when they are there, so that their products run while the others are made.
 template <bool BF>
-__device__ __forceinline__ float probabilities(uint32_t s_addr, float scale, float off) {
+__device__ __forceinline__ float probabilities(uint32_t s_addr, float scale, float off, uint32_t half_bar, int lane) {
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
   for (int c0 = 0; c0 < kKeys; c0 += 64) {
@@ -554,6 +554,12 @@ __device__ __forceinline__ float probabilities(uint32_t s_addr, float scale, flo
       p[e / 2] = BF ? pack_bf162(x, y) : pack_half2(x, y);
     }
     tmem_st32(s_addr + c0 / 2, p);  // over scores that have been read
+    if (c0 == 0 && half_bar != 0) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(half_bar);
+    }
   }
   return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
@@ -756,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
   const int tile_id = a.tiles - 1 - blockIdx.x / a.num_kv_heads;  // later rows see more keys: first
   auto bar = [&](const void* p) { return base + static_cast<uint32_t>(static_cast<const uint8_t*>(p) - smem); };
 
-  find_tile<C::ROWS>(a, ctrl, tile_id);
+  find_tile<C::ROWS>(a, ctrl, reinterpret_cast<int*>(smem + C::META), tile_id);  // not in use yet
   __syncthreads();
   const int seq = ctrl->seq;
   if (seq < 0) return;  // the launch has room for more tiles than the batch has
@@ -779,6 +785,7 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
       mbar_init(bar(&ctrl->k_empty[i]), 1);
       mbar_init(bar(&ctrl->v_empty[i]), 1);
       mbar_init(bar(&ctrl->s_full[i]), 1);
+      mbar_init(bar(&ctrl->p_half[i]), 4);
       mbar_init(bar(&ctrl->p_full[i]), 4);
       mbar_init(bar(&ctrl->o_full[i]), 1);
     }
@@ -874,7 +881,9 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every p is 0
-        l += bf ? probabilities<true>(s_addr, scale, off) : probabilities<false>(s_addr, scale, off);
+        const uint32_t half_bar = NW == 2 ? bar(&ctrl->p_half[wg]) : 0u;
+        l += bf ? probabilities<true>(s_addr, scale, off, half_bar, lane)
+                : probabilities<false>(s_addr, scale, off, half_bar, lane);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -1088,10 +1097,10 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
         }
         tc_commit(leader, bar(&ctrl->s_full[buf]));
       };
-      auto values = [&](int w, int buf, int stage, bool add) {  // O_w += P V
+      auto values = [&](int w, int buf, int stage, bool add, int k0, int k1) {  // O_w += P V, keys 16 k0 .. 16 k1 - 1
         const uint64_t va = v_op + stage * (C::TILE >> 4);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
+        for (int k = k0; k < k1; ++k)
           mma_ts(leader, tm + C::O(0) + w * 128, tm + C::S(0) + buf * 128 + 8 * k, va + k * (2048 >> 4), pv_desc,
                  add || k > 0);
       };
@@ -1102,6 +1111,7 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
         tc_fence_after();
         for (int w = 0; w < halves; ++w) scores(w, w, 0);
         tc_commit(leader, bar(&ctrl->k_empty[0]));
+        if (NW == 2) ok = wait(&ctrl->v_full[0], 0) && (tiles == 1 || wait(&ctrl->k_full[1], 0));
       }
       for (int i = 0; ok && i < tiles; ++i) {
         const int st = i & 1, ns = (i + 1) & 1;
@@ -1116,28 +1126,31 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
           ok = wait(&ctrl->v_full[st], (i >> 1) & 1) && wait(&ctrl->p_full[st], (i >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          values(0, st, st, i > 0);
+          values(0, st, st, i > 0, 0, kKeys / 16);
           tc_commit(leader, bar(&ctrl->v_empty[st]));
           tc_commit(leader, bar(i + 1 < tiles ? &ctrl->pv_done : &ctrl->o_full[0]));
           continue;
         }
-        ok = wait(&ctrl->v_full[st], (i >> 1) & 1);
+        // this tile's V and the next one's K were waited for at the end of the last turn
         for (int w = 0; ok && w < halves; ++w) {
+          ok = wait(&ctrl->p_half[w], i & 1);
+          if (!ok) break;
+          tc_fence_after();
+          values(w, w, st, i > 0, 0, kKeys / 32);
           ok = wait(&ctrl->p_full[w], i & 1);
           if (!ok) break;
           tc_fence_after();
-          values(w, w, st, i > 0);
+          values(w, w, st, true, kKeys / 32, kKeys / 16);
           if (w == halves - 1) tc_commit(leader, bar(&ctrl->v_empty[st]));
           if (i + 1 < tiles) {
-            if (w == 0) ok = wait(&ctrl->k_full[ns], ((i + 1) >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
             scores(w, w, ns);
+            if (w == halves - 1) tc_commit(leader, bar(&ctrl->k_empty[ns]));
           } else {
             tc_commit(leader, bar(&ctrl->o_full[w]));
           }
         }
-        if (NW == 2 && ok && i + 1 < tiles) tc_commit(leader, bar(&ctrl->k_empty[ns]));
+        if (ok && i + 1 < tiles) ok = wait(&ctrl->v_full[ns], ((i + 1) >> 1) & 1);
+        if (ok && i + 2 < tiles) ok = wait(&ctrl->k_full[st], ((i + 2) >> 1) & 1);
       }
       if (!ok) {  // leave with nothing in flight
         tc_commit(leader, bar(&ctrl->drained));
@@ -1260,9 +1273,10 @@ __global__ void __launch_bounds__(2 * kProducers) stage_kernel(const __grid_cons
 template <int D>
 __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs a, int rows_per_tile) {
   __shared__ Ctrl ctrl;
+  __shared__ int scan[8];
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, h = blockIdx.x % a.num_kv_heads, tile_id = blockIdx.x / a.num_kv_heads;
-  if (rows_per_tile == 128) find_tile<128>(a, &ctrl, tile_id); else find_tile<256>(a, &ctrl, tile_id);
+  if (rows_per_tile == 128) find_tile<128>(a, &ctrl, scan, tile_id); else find_tile<256>(a, &ctrl, scan, tile_id);
   __syncthreads();
   if (ctrl.seq < 0) return;
   const int R0 = ctrl.tile * rows_per_tile, R1 = min(ctrl.q * a.gqa, R0 + rows_per_tile);
