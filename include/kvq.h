@@ -537,7 +537,12 @@ kvq_status kvq_decode_window(const kvq_cache_desc* cache, void* k_cache, void* v
  * window >= 0 (0: no limit), num_sinks >= 0.
  * workspace: device memory of >= kvq_prefill_workspace_size(...) bytes, 16-byte
  *   aligned (may be NULL when that is 0); its contents on entry do not matter.
- *   Two calls that overlap on the GPU must not share one.
+ *   Two calls that overlap on the GPU must not share one.  The size covers partial
+ *   results where few rows leave the keys to be split, and, for batches with some
+ *   hundred rows per sequence or more, the contexts dequantized to 16 bits (4 bytes x
+ *   num_seqs x max_context_len, rounded up to 128, x num_kv_heads x head_dim, up to
+ *   16 GiB: a tight max_context_len keeps it small).
+ * One to three launches on the stream; may be captured into a CUDA graph.
  * Arithmetic: 16-bit operands in the tensor cores, float32 sums and softmax.
  *   int8 and FP8 codes are exact in fp16; asymmetric rows are rounded to fp16
  *   once dequantized ((code * scale + zero_point) [* sigma]; past 65504 infinite);

@@ -6,10 +6,15 @@ too large for a multi-pass capture):
   python profile_case.py kvarn_131k num_seqs=1 ctx_lo=32768 ctx_hi=32768
 
 Arguments after the workload name override its generator settings (integers).
+
+  python profile_case.py operators prefill_long
+
+runs a case of perf/operators.py instead, through the library's calls.
 Everything goes through the library's public calls; nothing is checked here.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import sys
 
@@ -57,8 +62,25 @@ def run(name: str, repeats: int = 3, **overrides) -> None:
     print("device error bits:", kvq.kvq_get_device_error())
 
 
+def run_operator(name: str, repeats: int = 3) -> None:
+    kbuild.build()
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "perf", "operators.py")
+    spec = importlib.util.spec_from_file_location("perf_operators", path)
+    cases = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(cases)
+    cases.own = True
+    state = cases.prepare(next(c for c in cases.listed() if c["name"] == name), 1)
+    for _ in range(repeats):
+        cases.run(state)
+        torch.cuda.synchronize()
+    print(f"{name}: device error bits: {kvq.kvq_get_device_error()}")
+
+
 def main(argv=None) -> None:
     argv = sys.argv[1:] if argv is None else argv
+    if argv[0] == "operators":
+        run_operator(argv[1])
+        return
     kw = {}
     for a in argv[1:]:
         k, v = a.split("=", 1)

@@ -37,6 +37,7 @@
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "mbarrier.cuh"
 #include "quant_row.cuh"
 
 namespace kvq {

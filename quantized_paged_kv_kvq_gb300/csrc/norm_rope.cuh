@@ -18,7 +18,11 @@
 // on packed float32 pairs.  A warp takes kRopeRows row groups of one kind (queries,
 // keys or values) of one token, all loaded before any is worked on.  HBM-bound on
 // large batches: every row is read and written once, the table's 4r bytes per
-// token come from L2 after the first warp.
+// token come from L2 after the first warp.  16,384 tokens of 32 / 8 heads of 128
+// into an FP8 cache, 378 MB: 77 us, 72 % of the copy rate (99 us with a shuffle per
+// element for the partner and 8 elements a lane in a row; rows in two to eight
+// batches per warp, which spares loads of turns and weights: 74 to 82).  64 tokens
+// without a cache: 2.4 us.
 #pragma once
 
 #include "kvq_device.cuh"
