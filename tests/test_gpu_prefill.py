@@ -80,6 +80,16 @@ def test_more_tiles_than_the_device_holds_at_once():
     check("int8", lens, np.random.default_rng(4).integers(1, 4, 48), 8, 2, 64, 16)
 
 
+@pytest.mark.parametrize("count", [513, 1100])
+def test_many_sequences(count):
+    """More sequences than a CTA has threads: the row tiles are found over several chunks."""
+    rng = np.random.default_rng(count)
+    lens, new = rng.integers(0, 40, count), rng.integers(0, 4, count)
+    check("e5m2", lens, np.minimum(lens, new), 2, 1, 64, 16)
+    lens[count - 2], new[count - 2] = 300, 140  # one long chunk near the end
+    check("int8", lens, np.minimum(lens, new), 1, 2, 64, 16, 30, 3)
+
+
 def test_large_logits():
     """Keys whose logits span hundreds: the running maximum moves by more than any fixed range."""
     check("bf16", [400], [130], 1, 4, 128, 16, k_std=20.0)

@@ -154,3 +154,64 @@ def test_two_captured_steps_share_nothing():
             torch.cuda.synchronize()
             assert torch.equal(bits(a), bits(out)) and torch.equal(bits(b), bits(one))
             assert (a.double() - b.double()).abs().max() <= 4e-2
+
+
+def test_blocks_past_32_bits():
+    """The same tokens in the first blocks of a pool and in blocks beyond 4 GiB: same bits."""
+    bs, hkv, d, nb = 128, 8, 128, 34000  # 131,072 bytes a block and tensor: 4.46 GB each
+    cache = kvq.KVCache("int8", "int8", hkv, d, bs, nb, torch.empty((nb, bs, hkv, d), dtype=torch.uint8, device=DEV),
+                        torch.empty((nb, bs, hkv, d), dtype=torch.uint8, device=DEV), k_scale=0.04, v_scale=0.04)
+    n = 700
+    g = torch.Generator(DEV).manual_seed(1)
+    q, k, v = (torch.randn((n, h, d), device=DEV, generator=g).to(torch.bfloat16) for h in (32, hkv, hkv))
+    rope = kvq.Rope(None)
+    pos, query = ints(np.arange(n)), torch.empty_like(q)
+    pages = -(-n // bs)
+    found = []
+    for first in (0, nb - pages):
+        free = ints(np.arange(first, first + pages))
+        table, slots = torch.full((1, pages), -1, dtype=torch.int32, device=DEV), torch.empty(n, dtype=torch.int64, device=DEV)
+        lens, cu, rng = ints([0]), ints([0, 0]), ints([0, 0])
+        at = torch.empty(n, dtype=torch.int32, device=DEV)
+        kvq.kvq_plan_step(ints([0]), ints([n]), table, free, ints([0, pages]), bs, nb, slots, at, lens, cu, rng)
+        assert slots[0] == first * bs and torch.equal(at, pos)
+        kvq.kvq_norm_rope_write(rope, cache, q, k, v, pos, slots, query)
+        assert torch.equal(bits(query), bits(q))
+        outs = []
+        for rows in (n, 40, 1):  # dequantized ahead, by each CTA, and one token through the decode
+            sub, out = query[n - rows:].contiguous(), torch.empty((rows, 32, d), dtype=torch.bfloat16, device=DEV)
+            ws = garbage(kvq.kvq_prefill_workspace_size(cache, 1, 32, rows, rows, n))
+            outs.append(kvq.kvq_paged_prefill(cache, sub, out, ints([0, rows]), table, lens, rows, n, d ** -0.5, 300, 7, ws))
+        ws = garbage(kvq.kvq_decode_workspace_size(cache, 1, 32, n))
+        one = query[n - 1:].contiguous()
+        outs.append(kvq.kvq_decode_window(cache, one, torch.empty_like(one), table, lens, n, d ** -0.5, 300, 7, ws))
+        found.append([bits(o) for o in outs])
+    assert all(torch.equal(a, b) for a, b in zip(*found))
+    assert kvq.kvq_get_device_error() == 0
+
+
+def test_the_binding_refuses_wrong_tensors():
+    loop = Loop("int8", 0, 0)
+    loop.step([20, 1, 1, 1])
+    q = torch.zeros((SEQS, HQ, D), dtype=torch.bfloat16, device=DEV)
+    ws = garbage(1 << 22)
+    good = dict(query=q, out=torch.empty_like(q), block_table=loop.block_table, context_lens=loop.lens)
+    call = lambda **kw: kvq.kvq_decode_window(loop.cache, **{**good, **kw}, max_context_len=20, sm_scale=0.1, window=5,
+                                              workspace=ws)
+    call()
+    for kw in (dict(query=q.float()), dict(query=q.cpu()), dict(out=q[:, ::2]), dict(query=q[:, :, :64]),
+               dict(block_table=loop.block_table.long()), dict(block_table=loop.block_table[:, ::2]),
+               dict(context_lens=loop.lens[:2]), dict(new_key=q[:, :HKV])):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(kvq.KvqError):  # a head ratio above 8
+        big = torch.zeros((SEQS, 32, D), dtype=torch.bfloat16, device=DEV)
+        call(query=big, out=torch.empty_like(big))
+    rope = loop.rope
+    k = torch.zeros((3, HKV, D), dtype=torch.bfloat16, device=DEV)
+    for args in ((q[:3], k, ints([0, 1])), (q[:3], k[:2], ints([0, 1, 2])), (q[:3].transpose(0, 1), k, ints([0, 1, 2])),
+                 (q[:3], k, torch.zeros(3, dtype=torch.int64, device=DEV))):
+        with pytest.raises(ValueError):
+            kvq.kvq_norm_rope(rope, *args, torch.empty_like(q[:3]), torch.empty_like(k))
+    with pytest.raises(kvq.KvqError):  # an output over another input
+        kvq.kvq_norm_rope(rope, q[:3], k, ints([0, 1, 2]), torch.empty_like(q[:3]), q[:3, :HKV])
