@@ -140,8 +140,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:  # the current stream's handle (current_stream() would wrap it first, 3 us)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    if stream is None:
+        stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -359,37 +359,49 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _tensors(*specs) -> None:
-    """Each (name, tensor, dtype, shape): a contiguous CUDA tensor of the current device.
-    One pass of cheap comparisons: these calls take a few microseconds on the GPU, and
-    the checks run before each of them."""
-    dev = torch.cuda.current_device()
+# The calls below take a few microseconds on the GPU, and these checks run before each
+# of them: one device query per call, then plain comparisons.
+def _device_of(name: str, t: torch.Tensor) -> int:
+    """The current CUDA device, which t must be on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+    return dev
+
+
+def _tensors(dev: int, *specs) -> None:
+    """Each (name, tensor, dtype, shape): a contiguous tensor of CUDA device dev."""
     for name, t, dtype, shape in specs:
-        if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA "
                              f"device {dev}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _rows(name: str, t: torch.Tensor, shape) -> int:
+def _rows(dev: int, name: str, t: torch.Tensor, shape) -> int:
     """Checks bf16 [T, heads, D] rows with a free token stride; returns that stride."""
-    n, heads, d = shape
-    if t.get_device() != torch.cuda.current_device() or t.dtype is not torch.bfloat16 or t.shape != shape:
-        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on the current CUDA device, "
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on CUDA device {dev}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    n, heads, d = shape
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
-        if t.numel():
-            raise ValueError(f"{name}: heads and elements must be contiguous, got strides {t.stride()}")
+    if ((s2 != 1 and d > 1) or (s1 != d and heads > 1)) and t.numel():
+        raise ValueError(f"{name}: heads and elements must be contiguous, got strides {t.stride()}")
     # one token: any stride serves, and torch may report one that is too small
     return s0 if n > 1 else (heads * d + 7) // 8 * 8
 
 
-def _workspace(workspace: Optional[torch.Tensor]) -> int:
+def _workspace(dev: int, workspace: Optional[torch.Tensor]) -> int:
     if workspace is None:
         return 0
-    _need(workspace.get_device() == torch.cuda.current_device() and workspace.is_contiguous(),
+    _need(workspace.get_device() == dev and workspace.is_contiguous(),
           "workspace must be contiguous, on the current CUDA device")
     return workspace.numel() * workspace.element_size()
+
+
+def _raw_stream(dev: int, stream) -> int:
+    """A stream's handle (the current one's if None, without the wrapper that
+    torch.cuda.current_stream() makes in 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _address(t: Optional[torch.Tensor]):
@@ -409,7 +421,8 @@ def kvq_plan_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tabl
     (int32 [2]) the state after the step."""
     s, t, i32 = context_lens.numel(), slot_mapping.numel(), torch.int32
     width, free = block_table.shape[-1], free_blocks.numel()
-    _tensors(("context_lens", context_lens, i32, (s,)), ("new_lens", new_lens, i32, (s,)),
+    dev = _device_of("slot_mapping", slot_mapping)
+    _tensors(dev, ("context_lens", context_lens, i32, (s,)), ("new_lens", new_lens, i32, (s,)),
              ("block_table", block_table, i32, (s, width)), ("free_blocks", free_blocks, i32, (free,)),
              ("free_range", free_range, i32, (2,)), ("slot_mapping", slot_mapping, torch.int64, (t,)),
              ("positions", positions, i32, (t,)), ("context_lens_out", context_lens_out, i32, (s,)),
@@ -418,7 +431,7 @@ def kvq_plan_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tabl
         context_lens.data_ptr(), new_lens.data_ptr(), s, block_table.data_ptr(), width, block_size,
         num_blocks, free_blocks.data_ptr(), free, free_range.data_ptr(), slot_mapping.data_ptr(),
         positions.data_ptr(), t, context_lens_out.data_ptr(), cu_new.data_ptr(),
-        free_range_out.data_ptr(), _stream(stream))
+        free_range_out.data_ptr(), _raw_stream(dev, stream))
     _check(st, "kvq_plan_step")
 
 
@@ -439,14 +452,15 @@ def kvq_rope_table(table: torch.Tensor, base: float, scaling: Optional[RopeScali
     """table (fp32 [positions, rot_dim / 2, 2]) <- cos and sin of every position and pair."""
     _need(table.dim() == 3, "table must have shape (positions, rot_dim / 2, 2)")
     n, pairs = table.shape[:2]
-    _tensors(("table", table, torch.float32, (n, pairs, 2)))
+    dev = _device_of("table", table)
+    _tensors(dev, ("table", table, torch.float32, (n, pairs, 2)))
     sc = None
     if scaling is not None:
         sc = ctypes.byref(_RopeScaling(ROPE_KIND[scaling.kind], scaling.factor,
                                        scaling.original_len, scaling.low, scaling.high,
                                        scaling.amplitude))
     st = load_library().kvq_rope_table(table.data_ptr(), n, 2 * pairs, float(base), sc,
-                                       _stream(stream))
+                                       _raw_stream(dev, stream))
     _check(st, "kvq_rope_table")
     return table
 
@@ -463,16 +477,16 @@ class Rope:
     eps: float = 1e-6
     weight_offset: float = 0.0
 
-    def desc(self, head_dim: int) -> _RopeDesc:
+    def desc(self, head_dim: int, dev: int) -> _RopeDesc:
         rot, count, table = 0, 0, self.table
         if table is not None:
             _need(table.dim() == 3, "table must have shape (positions, rot_dim / 2, 2)")
             count, pairs = table.shape[:2]
             rot = 2 * pairs
-            _tensors(("table", table, torch.float32, (count, pairs, 2)))
+            _tensors(dev, ("table", table, torch.float32, (count, pairs, 2)))
         for name, w in (("q_weight", self.q_weight), ("k_weight", self.k_weight)):
             if w is not None:
-                _tensors((name, w, torch.bfloat16, (head_dim,)))
+                _tensors(dev, (name, w, torch.bfloat16, (head_dim,)))
         return _RopeDesc(head_dim, rot, self.interleaved, self.eps, self.weight_offset,
                          _address(self.q_weight), _address(self.k_weight), _address(table), count)
 
@@ -483,13 +497,15 @@ def kvq_norm_rope(rope: Rope, query: torch.Tensor, key: torch.Tensor, positions:
     (bf16, token strides free; an output may be its own input)."""
     t, hq, d = query.shape
     q, kv = (t, hq, d), (t, key.shape[1], d)
-    qs, ks = _rows("query", query, q), _rows("key", key, kv)
-    qos, kos = _rows("query_out", query_out, q), _rows("key_out", key_out, kv)
-    _tensors(("positions", positions, torch.int32, (t,)))
-    r = rope.desc(d)
+    dev = _device_of("query", query)
+    qs, ks = _rows(dev, "query", query, q), _rows(dev, "key", key, kv)
+    qos, kos = _rows(dev, "query_out", query_out, q), _rows(dev, "key_out", key_out, kv)
+    _tensors(dev, ("positions", positions, torch.int32, (t,)))
+    r = rope.desc(d, dev)
     st = load_library().kvq_norm_rope(ctypes.byref(r), query_out.data_ptr(), qos, key_out.data_ptr(),
                                       kos, query.data_ptr(), qs, key.data_ptr(), ks,
-                                      positions.data_ptr(), t, hq, kv[1], _stream(stream))
+                                      positions.data_ptr(), t, hq, kv[1],
+                                      _raw_stream(dev, stream))
     _check(st, "kvq_norm_rope")
 
 
@@ -501,14 +517,16 @@ def kvq_norm_rope_write(rope: Rope, cache: KVCache, query: torch.Tensor, key: to
     t, hq, _ = query.shape
     d = cache.head_dim
     q, kv = (t, hq, d), (t, cache.num_kv_heads, d)
-    qs, qos = _rows("query", query, q), _rows("query_out", query_out, q)
-    ks, vs = _rows("key", key, kv), _rows("value", value, kv)
-    _tensors(("positions", positions, torch.int32, (t,)), ("slot_mapping", slot_mapping, torch.int64, (t,)))
-    r, c = rope.desc(d), cache.desc()
+    dev = _device_of("query", query)
+    qs, qos = _rows(dev, "query", query, q), _rows(dev, "query_out", query_out, q)
+    ks, vs = _rows(dev, "key", key, kv), _rows(dev, "value", value, kv)
+    _tensors(dev, ("positions", positions, torch.int32, (t,)),
+             ("slot_mapping", slot_mapping, torch.int64, (t,)))
+    r, c = rope.desc(d, dev), cache.desc()
     st = load_library().kvq_norm_rope_write(
         ctypes.byref(r), ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(),
         query_out.data_ptr(), qos, query.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
-        positions.data_ptr(), slot_mapping.data_ptr(), t, hq, _stream(stream))
+        positions.data_ptr(), slot_mapping.data_ptr(), t, hq, _raw_stream(dev, stream))
     _check(st, "kvq_norm_rope_write")
     return query_out
 
@@ -523,20 +541,21 @@ def kvq_decode_window(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
     see the last `window` tokens of their context and its first num_sinks."""
     s, hq, _ = query.shape
     rows, width = (s, hq, cache.head_dim), block_table.shape[-1]
-    _tensors(("query", query, torch.bfloat16, rows), ("out", out, torch.bfloat16, rows),
+    dev = _device_of("query", query)
+    _tensors(dev, ("query", query, torch.bfloat16, rows), ("out", out, torch.bfloat16, rows),
              ("block_table", block_table, torch.int32, (s, width)),
              ("context_lens", context_lens, torch.int32, (s,)))
     _need((new_key is None) == (new_value is None), "new_key and new_value come together")
     ks = vs = 0
     if new_key is not None:
         kv = (s, cache.num_kv_heads, cache.head_dim)
-        ks, vs = _rows("new_key", new_key, kv), _rows("new_value", new_value, kv)
+        ks, vs = _rows(dev, "new_key", new_key, kv), _rows(dev, "new_value", new_value, kv)
     c = cache.desc()
     st = load_library().kvq_decode_window(
         ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), _address(new_key),
         _address(new_value), ks, vs, out.data_ptr(), query.data_ptr(), s, hq, block_table.data_ptr(),
         width, context_lens.data_ptr(), max_context_len, float(sm_scale), window, num_sinks, num_ctas,
-        _address(workspace), _workspace(workspace), _stream(stream))
+        _address(workspace), _workspace(dev, workspace), _raw_stream(dev, stream))
     _check(st, "kvq_decode_window")
     return out
 
@@ -562,7 +581,8 @@ def kvq_paged_prefill(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
     s = context_lens.numel()
     n, hq, _ = query.shape
     rows, width = (n, hq, cache.head_dim), block_table.shape[-1]
-    _tensors(("query", query, torch.bfloat16, rows), ("out", out, torch.bfloat16, rows),
+    dev = _device_of("query", query)
+    _tensors(dev, ("query", query, torch.bfloat16, rows), ("out", out, torch.bfloat16, rows),
              ("cu_query", cu_query, torch.int32, (s + 1,)),
              ("block_table", block_table, torch.int32, (s, width)),
              ("context_lens", context_lens, torch.int32, (s,)))
@@ -571,7 +591,7 @@ def kvq_paged_prefill(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
         ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), out.data_ptr(),
         query.data_ptr(), cu_query.data_ptr(), s, n, max_query_len, hq, block_table.data_ptr(), width,
         context_lens.data_ptr(), max_context_len, float(sm_scale), window, num_sinks,
-        _address(workspace), _workspace(workspace), _stream(stream))
+        _address(workspace), _workspace(dev, workspace), _raw_stream(dev, stream))
     _check(st, "kvq_paged_prefill")
     return out
 
