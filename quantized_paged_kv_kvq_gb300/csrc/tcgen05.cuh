@@ -58,12 +58,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       KVQ_W8(r, 0), KVQ_W8(r, 8), KVQ_W8(r, 16), KVQ_W8(r, 24)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t* r, uint32_t addr) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : KVQ_R8(r, 0), KVQ_R8(r, 8)
-      : "r"(addr));
-}
 // Waits for this warp's loads; the loaded registers pass through, so that no use
 // of them can be moved before it.
 #define KVQ_P8(r, i) \
@@ -76,13 +70,6 @@ __device__ __forceinline__ void tmem_waited32(uint32_t* r) {
   asm volatile("" : KVQ_P8(r, 0), KVQ_P8(r, 8), KVQ_P8(r, 16), KVQ_P8(r, 24));
 }
 #undef KVQ_P8
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          addr),
-      KVQ_W8(r, 0), KVQ_W8(r, 8)
-      : "memory");
-}
 #undef KVQ_R8
 #undef KVQ_W8
 

@@ -169,6 +169,6 @@ def test_prefill_shapes(lib):
 def test_binding_checks_before_the_call():
     """Tensors that are not on the GPU are refused by the binding itself."""
     if torch.cuda.is_available():
-        pytest.skip("the CPU container's check")
+        pytest.skip("needs a machine without a GPU")
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         kvq.kvq_rope_table(torch.empty(4, 8, 2), 10000.0)
