@@ -90,6 +90,17 @@ def test_many_sequences(count):
     check("int8", lens, np.minimum(lens, new), 1, 2, 64, 16, 30, 3)
 
 
+@pytest.mark.parametrize("count", [2, 63, 128, 129])
+def test_sequences_of_one_order(count):
+    """Equal, rising and falling lengths, rows of no tokens between: each row is its own sequence's."""
+    lens = np.full(count, 37)
+    check("int8", lens, np.ones(count, int), 1, 4, 64, 16)
+    lens = np.arange(count) * 3 % 200 + 1
+    new = np.minimum(np.arange(count) % 4, lens)
+    check("bf16", lens, new, 2, 2, 64, 16)
+    check("int4", lens[::-1].copy(), new[::-1].copy(), 1, 1, 128, 32, 40, 2)
+
+
 def test_large_logits():
     """Keys whose logits span hundreds: the running maximum moves by more than any fixed range."""
     check("bf16", [400], [130], 1, 4, 128, 16, k_std=20.0)
