@@ -283,7 +283,7 @@ kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
   const int sms = sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
   const int64_t g = num_q_heads / c->num_kv_heads, hkv = c->num_kv_heads;
-  sh->rows = max_query_len * g <= 128 ? 128 : 256;
+  sh->rows = max_query_len * g <= 64 ? 64 : max_query_len * g <= 128 ? 128 : 256;
   // no more than every sequence at its longest, nor than the rows there are with
   // a tile per sequence not full
   const int64_t longest = (max_query_len * g + sh->rows - 1) / sh->rows;

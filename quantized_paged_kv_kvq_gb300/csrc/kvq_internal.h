@@ -208,7 +208,7 @@ struct PrefillArgs {
   int max_context_len;
   int window;  // 0: every earlier token
   int sinks;
-  int rows_per_tile;  // 128 or 256
+  int rows_per_tile;  // 64, 128 or 256
   int tiles;      // row tiles the launch has room for
   int num_splits; // parts each row tile's keys are cut into
   float* ws_out;  // [splits, tiles, Hkv, rows, D] partial outputs

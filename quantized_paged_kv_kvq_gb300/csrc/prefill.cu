@@ -5,8 +5,9 @@
 // with a running maximum m over tiles of 128 keys and float32 sums: one pass over
 // the context, no score leaves the SM.
 //
-// Split: a CTA owns 128 or 256 rows (token, query head) of one sequence and
-// kv-head; row R of the sequence is query head R % G of new token R / G, so the
+// Split: a CTA owns 64, 128 or 256 rows (token, query head) of one sequence and
+// kv-head (the fewest that hold the longest chunk: 64 leave room for one more tile of
+// V on its way, and warps without rows sit out: 68 -> 57 us in the case below); row R of the sequence is query head R % G of new token R / G, so the
 // G heads that share keys fill a tile together.  Per 128 keys and 128 rows it
 // runs two tcgen05 products, S = Q K^T (operands in shared memory) and
 // O += P V (P in tensor memory, over S's own columns), S and O in tensor memory.
@@ -32,7 +33,7 @@
 //
 // Few rows over long contexts: the keys are cut into num_splits parts, whose
 // (m, sum, accumulators) a second kernel joins.  32 x 1..8 tokens on 256..4,096 keys:
-// 68 us, 2.1 TB/s: latency of the copies and of one CTA's start and end (7 us).
+// 57 us, 2.4 TB/s: latency of the copies and of one CTA's start and end (7 us).
 //
 // Measured and not kept: score buffers of 64 keys, two ahead (1.13 ms for 1.01); an
 // issuing warp per half (1.21); codes through registers instead of the queue (1.04);
@@ -57,10 +58,10 @@ constexpr int kProducers = 128;       // threads that load and dequantize K; as 
 constexpr int kSpin = 1 << 18;        // polls of an mbarrier before giving up (some seconds)
 constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is not raised: p <= 2^8
 
-template <int D_, int NW_, bool STAGED = false>  // head_dim, softmax warpgroups, keys dequantized ahead
+template <int D_, int ROWS_, bool STAGED = false>  // head_dim, rows, keys dequantized ahead
 struct Cfg {
-  static constexpr int D = D_, NW = NW_;
-  static constexpr int ROWS = 128 * NW;
+  static constexpr int D = D_, ROWS = ROWS_;
+  static constexpr int NW = ROWS == 256 ? 2 : 1;  // softmax warpgroups
   static constexpr int THREADS = 128 * NW + (STAGED ? 0 : 2 * kProducers) + 128;
   static constexpr int GROUPS = D / 64;              // 64-element column groups of an operand row
   static constexpr int GROUP_BYTES = 128 * 128;      // 128 rows of 128 bytes
@@ -68,10 +69,13 @@ struct Cfg {
   static constexpr int RAW = 128 * D;                // largest code tile that is dequantized
   // tiles that the producers' loads run ahead (slots of their queues); what shared
   // memory leaves room for
-  static constexpr int AHEAD_K = NW == 2 ? 1 : 2, AHEAD_V = 1;
-  // shared memory: queries, K and V stages, raw queue, raw metadata, control
+  static constexpr int AHEAD_K = NW == 2 ? 1 : 2, AHEAD_V = ROWS == 64 ? 2 : 1;
+  // shared memory: queries, K and V stages, raw queue, raw metadata, control.  With 64
+  // rows the products read 64 more of a group, which are what lies behind: rows of
+  // scores that no one reads.
   static constexpr int Q = 0;
-  static constexpr int K = Q + NW * TILE;
+  static constexpr int Q_GROUP = ROWS == 64 ? 64 * 128 : GROUP_BYTES;
+  static constexpr int K = Q + NW * GROUPS * Q_GROUP;
   static constexpr int V = K + 2 * TILE;
   static constexpr int RAWQ = V + 2 * TILE;
   static constexpr int META = RAWQ + (STAGED ? 0 : (AHEAD_K + AHEAD_V) * RAW);  // slots of K, then of V
@@ -118,7 +122,7 @@ __device__ __forceinline__ int2 seq_rows(const PrefillArgs& a, int s, bool& bad)
 // length (the launch starts from the last tile, so the longest come first; scan: two
 // words a sequence), more in their order (a scan; a word a warp): 32 x 1..8 tokens on
 // 256..4,096 keys, 256 CTAs on 152 SMs:
-// 93 us in their order, 68 so.
+// 93 us in their order, 68 so (of 128 rows each).
 constexpr int kOrdered = 128;
 static_assert(kOrdered * 8 <= 2 * 3 * kKeys * 2, "fits the metadata slots, which are not in use yet");
 template <int ROWS>
@@ -299,8 +303,8 @@ __device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, 
 }
 
 // Address of 16-byte chunk q of row `row` in an operand tile.
-__device__ __forceinline__ uint32_t chunk_addr(uint32_t tile, int row, int q) {
-  return tile + (q >> 3) * (128 * 128) + row * 128 + (((q & 7) ^ (row & 7)) << 4);
+__device__ __forceinline__ uint32_t chunk_addr(uint32_t tile, int row, int q, int group_bytes = 128 * 128) {
+  return tile + (q >> 3) * group_bytes + row * 128 + (((q & 7) ^ (row & 7)) << 4);
 }
 
 // One of the two caches, as the producers read it.
@@ -657,14 +661,14 @@ struct RowMap {
 // of an operand tile, by a warp: copied as they are, a row being D/8 lanes of 16
 // bytes, then turned (sign), rotated for KVarN and rounded to fp16 a row per
 // thread.
-template <int D>
+template <int D, int GROUP>
 __device__ __forceinline__ void load_queries(const PrefillArgs& a, uint32_t tile, uint32_t signs, int row0, int R,
                                              int R1, const RowMap& map, float turn, bool bf, int lane) {
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   const int sub = lane % LPR, grp = lane / LPR;
 #pragma unroll 4
   for (int d = grp; d < 32; d += RPI)
-    cp_async_or_zero<16>(chunk_addr(tile, row0 + d, sub), a.query + map(R + d < R1 ? d : 0) * D + sub * 8, R + d < R1);
+    cp_async_or_zero<16>(chunk_addr(tile, row0 + d, sub, GROUP), a.query + map(R + d < R1 ? d : 0) * D + sub * 8, R + d < R1);
   cp_async_commit();
   cp_async_wait<0>();
   __syncwarp();
@@ -673,7 +677,7 @@ __device__ __forceinline__ void load_queries(const PrefillArgs& a, uint32_t tile
     float x[D];
 #pragma unroll
     for (int q = 0; q < D / 8; ++q) {
-      const uint4 w = ldsv4(chunk_addr(tile, row0 + lane, q)), m = ldsv4(signs + 16 * q);
+      const uint4 w = ldsv4(chunk_addr(tile, row0 + lane, q, GROUP)), m = ldsv4(signs + 16 * q);
       const uint32_t o[4] = {w.x ^ m.x, w.y ^ m.y, w.z ^ m.z, w.w ^ m.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -689,12 +693,12 @@ __device__ __forceinline__ void load_queries(const PrefillArgs& a, uint32_t tile
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = pack_half2(x[8 * q + 2 * e] * f, x[8 * q + 2 * e + 1] * f);
       nf = track_not_finite<false>(nf, o);
-      sts128(chunk_addr(tile, row0 + lane, q), o[0], o[1], o[2], o[3]);
+      sts128(chunk_addr(tile, row0 + lane, q, GROUP), o[0], o[1], o[2], o[3]);
     }
   } else {
 #pragma unroll 2
     for (int q = 0; q < D / 8; ++q) {
-      const uint32_t at = chunk_addr(tile, row0 + lane, q);
+      const uint32_t at = chunk_addr(tile, row0 + lane, q, GROUP);
       const uint4 w = ldsv4(at);
       uint32_t o[4] = {w.x, w.y, w.z, w.w};
       if (!bf || turn != 1.f) {
@@ -781,10 +785,11 @@ __device__ __forceinline__ void result_columns(uint32_t (&o)[32], uint32_t addr,
   }
 }
 
-template <int D, int NW, bool STAGED>
-__global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
+template <int D, int ROWS, bool STAGED>
+__global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap map_staged) {
-  using C = Cfg<D, NW, STAGED>;
+  using C = Cfg<D, ROWS, STAGED>;
+  constexpr int NW = C::NW;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzled tiles: 1024-byte aligned
   uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
@@ -809,18 +814,22 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
   const int i1 = static_cast<int>(static_cast<long long>(span.tiles) * (split + 1) / a.num_splits);
   const int nk = i1 - i0;
   const int nw = (NW == 2 && R1 - R0 > 128) ? 2 : 1;  // row halves in use
+  // warps with rows, of all and of each half (the others of a half only wait for the end)
+  const int row_warps = (R1 - R0 + 31) / 32;
+  auto half_warps = [&](int w) { return max(min(row_warps - 4 * w, 4), 1); };
   const bool bf = a.k_fmt == BF16;
 
   if (tid == 0) {
-    mbar_init(bar(&ctrl->q_full), 4 * nw);
+    mbar_init(bar(&ctrl->q_full), row_warps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(&ctrl->k_full[i]), STAGED ? 1 : kProducers / 32);
       mbar_init(bar(&ctrl->v_full[i]), STAGED ? 1 : kProducers / 32);
       mbar_init(bar(&ctrl->k_empty[i]), 1);
       mbar_init(bar(&ctrl->v_empty[i]), 1);
       mbar_init(bar(&ctrl->s_full[i]), 1);
-      mbar_init(bar(&ctrl->p_half[i]), 4);
-      mbar_init(bar(&ctrl->p_full[i]), 4);
+      const int arrivals = half_warps(NW == 2 ? i : 0);  // one warpgroup has both buffers
+      mbar_init(bar(&ctrl->p_half[i]), arrivals);
+      mbar_init(bar(&ctrl->p_full[i]), arrivals);
       mbar_init(bar(&ctrl->o_full[i]), 1);
     }
     mbar_init(bar(&ctrl->pv_done), 1);
@@ -867,12 +876,12 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
     const float turn = scale < 0.f ? -1.f : scale > 0.f ? 1.f : 0.f;
     scale = scale == 0.f ? 1.f : fabsf(scale);
     float m = -INFINITY, l = 0.f;
-    const bool active = wg < nw && nk > 0;
+    const bool has_rows = warp < row_warps, active = has_rows && nk > 0;
     const RowMap map(a, ctrl->q0, h, min(R0 + 32 * warp, R1 - 1));
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_first = tmem + C::S(wg) + lane_base, o_addr = tmem + C::O(wg) + lane_base;
     if (active) {
-      load_queries<D>(a, base + C::Q + wg * C::TILE, base + C::SIGNS, 32 * (warp & 3), R0 + 32 * warp, R1, map, turn, bf,
+      load_queries<D, C::Q_GROUP>(a, base + C::Q + wg * C::TILE, base + C::SIGNS, 32 * (warp & 3), R0 + 32 * warp, R1, map, turn, bf,
                       lane);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -931,7 +940,7 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
       if (!done) give_up();
     }
     const bool partial = a.num_splits > 1;
-    if (wg < nw && done && !*abort) {
+    if (has_rows && done && !*abort) {
       tc_fence_after();
       const float vs = a.v_head_scale != nullptr ? a.v_head_scale[h] : a.v_scale;
       const float mul = partial || l != l ? 1.f : l > 0.f ? vs / l : 0.f;
@@ -1126,8 +1135,9 @@ __global__ void __launch_bounds__(Cfg<D, NW, STAGED>::THREADS, 1)
         const uint64_t qa = q_op + w * (C::TILE >> 4), ka = k_op + stage * (C::TILE >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const int o = ((k >> 2) * C::GROUP_BYTES + (k & 3) * 32) >> 4;
-          mma_ss(leader, tm + C::S(0) + buf * 128, qa + o, ka + o, qk_desc, k > 0);
+          const int in_row = (k & 3) * 32;
+          mma_ss(leader, tm + C::S(0) + buf * 128, qa + (((k >> 2) * C::Q_GROUP + in_row) >> 4),
+                 ka + (((k >> 2) * C::GROUP_BYTES + in_row) >> 4), qk_desc, k > 0);
         }
         tc_commit(leader, bar(&ctrl->s_full[buf]));
       };
@@ -1310,7 +1320,9 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs a, 
   __shared__ __align__(8) int scan[2 * kOrdered];
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, h = blockIdx.x % a.num_kv_heads, tile_id = blockIdx.x / a.num_kv_heads;
-  if (rows_per_tile == 128) find_tile<128>(a, &ctrl, scan, tile_id); else find_tile<256>(a, &ctrl, scan, tile_id);
+  if (rows_per_tile == 64) find_tile<64>(a, &ctrl, scan, tile_id);
+  else if (rows_per_tile == 128) find_tile<128>(a, &ctrl, scan, tile_id);
+  else find_tile<256>(a, &ctrl, scan, tile_id);
   __syncthreads();
   if (ctrl.seq < 0) return;
   const int R0 = ctrl.tile * rows_per_tile, R1 = min(ctrl.q * a.gqa, R0 + rows_per_tile);
@@ -1351,16 +1363,16 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs a, 
   }
 }
 
-template <int D, int NW, bool STAGED>
+template <int D, int ROWS, bool STAGED>
 cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
-  using C = Cfg<D, NW, STAGED>;
+  using C = Cfg<D, ROWS, STAGED>;
   static std::atomic<unsigned long long> attr_done{0};  // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
-    e = cudaFuncSetAttribute(prefill_kernel<D, NW, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(prefill_kernel<D, ROWS, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
   }
@@ -1382,7 +1394,7 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   const dim3 grid(static_cast<unsigned>(a.tiles) * a.num_kv_heads, a.num_splits, 1);
-  prefill_kernel<D, NW, STAGED><<<grid, C::THREADS, C::SMEM, st>>>(a, map);
+  prefill_kernel<D, ROWS, STAGED><<<grid, C::THREADS, C::SMEM, st>>>(a, map);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.num_splits == 1) return e;
   prefill_join_kernel<D><<<grid.x, 256, 0, st>>>(a, C::ROWS);
@@ -1391,8 +1403,9 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_d(const PrefillArgs& a, cudaStream_t st) {
-  if (a.rows_per_tile == 128) return launch_t<D, 1, false>(a, st);
-  return a.staged != nullptr ? launch_t<D, 2, true>(a, st) : launch_t<D, 2, false>(a, st);
+  if (a.rows_per_tile == 64) return launch_t<D, 64, false>(a, st);
+  if (a.rows_per_tile == 128) return launch_t<D, 128, false>(a, st);
+  return a.staged != nullptr ? launch_t<D, 256, true>(a, st) : launch_t<D, 256, false>(a, st);
 }
 
 }  // namespace
