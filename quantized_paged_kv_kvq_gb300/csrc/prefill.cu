@@ -33,12 +33,17 @@
 //
 // Few rows over long contexts: the keys are cut into num_splits parts, whose
 // (m, sum, accumulators) a second kernel joins.  32 x 1..8 tokens on 256..4,096 keys:
-// 57 us, 2.4 TB/s: latency of the copies and of one CTA's start and end (7 us).
+// 57 us, 2.4 TB/s.  A tile takes 2,650 cycles, the softmax of the one warp with rows
+// 2,050 of them and the producers as much (a third converting, half issuing copies);
+// a CTA's start and end 14,000 (7 us).
 //
 // Measured and not kept: score buffers of 64 keys, two ahead (1.13 ms for 1.01); an
 // issuing warp per half (1.21); codes through registers instead of the queue (1.04);
 // scores held in 128 registers (0.85 ms for 0.85, 0.48 for 0.35 with masks and KVarN);
-// fully unrolled softmax and conversions (2.1 ms: instruction fetch).
+// fully unrolled softmax and conversions (2.1 ms: instruction fetch).  With few rows:
+// up to 32 rows in four copies, each warp a quarter of a tile's keys (63 us for 57: the
+// producers bound it, and the copies have to be joined); keys cut into parts for two or
+// four waves of CTAs (91 for 68, with 128 rows a tile).
 #include <atomic>
 
 #include "kvq_device.cuh"

@@ -90,6 +90,15 @@ def test_many_sequences(count):
     check("int8", lens, np.minimum(lens, new), 1, 2, 64, 16, 30, 3)
 
 
+@pytest.mark.parametrize("fmt", sorted(FORMATS))
+@pytest.mark.parametrize("g,q", [(1, 64), (8, 8), (8, 9), (5, 13), (3, 21), (4, 1)])
+def test_few_rows(fmt, g, q):
+    """63, 64, 65 and fewer rows of the longest chunk, on contexts of one tile and of several."""
+    check(fmt, [q, 128, 700, 1300], [q, 1, q, q // 2], 1, g, 128, 16)
+    check(fmt, [2000 + q], [q], 2, g, 64, 8)  # cut into parts
+    check(fmt, [900, 385], [q, q], 1, g, 128, 32, 200, 40)
+
+
 @pytest.mark.parametrize("count", [2, 63, 128, 129])
 def test_sequences_of_one_order(count):
     """Equal, rising and falling lengths, rows of no tokens between: each row is its own sequence's."""
