@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanArgs a) {
   // the usable part of the free list
   const int f0 = a.free_range[0], f1 = a.free_range[1];
   const int first = min(max(f0, 0), a.free_capacity);
-  const int avail = max(min(f1, a.free_capacity) - first, 0);
+  const int avail = max(min(f1, a.free_capacity), first) - first;  // no difference that could wrap: f1 is any int
   unsigned err = (f0 != first || f1 > a.free_capacity || f1 < f0) ? 128u : 0u;  // KVQ_DEVERR_FREE_BLOCKS
 
   const long long t0 = (static_cast<long long>(blockIdx.x) * kThreads + tid) * kRun;  // this thread's tokens

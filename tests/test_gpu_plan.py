@@ -144,3 +144,20 @@ def test_replayed_from_a_graph_and_on_another_stream():
         g.replay()
         st.check()
     assert kvq.kvq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("rng", [(2, -2 ** 31), (2, -2 ** 31 + 1), (7, -2 ** 31 + 6), (2, 1), (2, -1), (-5, -3),
+                                 (-2 ** 31, -2 ** 31), (2 ** 31 - 1, -2 ** 31), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_ranges_that_end_before_they_begin_hold_nothing(rng):
+    """However far the end lies before the beginning: no entry of the list is taken."""
+    st = Step([20, 0], [30, 20], 16, 50)
+    st.free_range.copy_(ints(rng))
+    st.call()
+    first = min(max(rng[0], 0), len(st.free))
+    assert kvq.kvq_get_device_error() == kvq.DEVERR_FREE_BLOCKS
+    assert st.out["range"].tolist() == [first, first]
+    table, slots = st.block_table.tolist(), st.out["slots"].tolist()
+    assert table[0][2:4] == [-1, -1] and table[1][:2] == [-1, -1]
+    assert table[0][:2] == st.table[0, :2].tolist()
+    assert all(x >= 0 for x in slots[:12]) and slots[12:50] == [-1] * 38  # the held page's 12 free places
+    assert st.out["cu"].tolist() == [0, 30, 50] and st.out["lens"].tolist() == [50, 20]
