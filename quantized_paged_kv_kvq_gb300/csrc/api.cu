@@ -267,9 +267,9 @@ struct PrefillShape {
 // 2 tiles 224 / 227, 8 x 4,096: 4 tiles 187 / 222, 8 311 / 427; bf16 as int8.
 constexpr int64_t stage_tiles(int fmt) { return is_asym(fmt) ? 3 : 8; }
 constexpr int64_t kStageBytes = 16ll << 30;
-kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
-                         int64_t total_q, int32_t max_query_len, int32_t max_context_len,
-                         PrefillShape* sh) {
+// What can be said of a batch's sizes without a device.
+kvq_status check_prefill(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
+                         int64_t total_q, int32_t max_query_len, int32_t max_context_len) {
   kvq_status st = check_cache(c);
   if (st != KVQ_OK) return st;
   if (num_seqs < 0 || num_q_heads < 1 || total_q < 0 || max_query_len < 0 || max_context_len < 0)
@@ -279,6 +279,12 @@ kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
   if (total_q > INT32_MAX || max_context_len > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->block_size) * c->num_kv_heads * c->head_dim * 2 > INT32_MAX)
     return KVQ_ERR_UNSUPPORTED;  // a block's bytes fit 31 bits
+  return KVQ_OK;
+}
+// The launch of a batch that check_prefill has passed.
+kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
+                         int64_t total_q, int32_t max_query_len, int32_t max_context_len,
+                         PrefillShape* sh) {
   if (num_seqs == 0 || total_q == 0 || max_query_len == 0) return KVQ_OK;
   const int sms = sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
@@ -837,9 +843,10 @@ kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t num_s
                                       int32_t num_q_heads, int64_t total_q, int32_t max_query_len,
                                       int32_t max_context_len, size_t* bytes) {
   if (bytes == nullptr) return KVQ_ERR_INVALID_ARGUMENT;
+  kvq_status st = check_prefill(cache, num_seqs, num_q_heads, total_q, max_query_len, max_context_len);
+  if (st != KVQ_OK) return st;
   PrefillShape sh;
-  kvq_status st = prefill_shape(cache, num_seqs, num_q_heads, total_q, max_query_len,
-                                max_context_len, &sh);
+  st = prefill_shape(cache, num_seqs, num_q_heads, total_q, max_query_len, max_context_len, &sh);
   if (st != KVQ_OK) return st;
   *bytes = sh.workspace;
   return KVQ_OK;
@@ -853,9 +860,7 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
                              int32_t max_context_len, float sm_scale, int32_t window,
                              int32_t num_sinks, void* workspace, size_t workspace_bytes,
                              kvq_stream_t stream) {
-  PrefillShape sh;
-  kvq_status st = prefill_shape(cache, num_seqs, num_q_heads, total_q, max_query_len,
-                                max_context_len, &sh);
+  kvq_status st = check_prefill(cache, num_seqs, num_q_heads, total_q, max_query_len, max_context_len);
   if (st != KVQ_OK) return st;
   if (window < 0 || num_sinks < 0 || !isfinite(sm_scale)) return KVQ_ERR_INVALID_ARGUMENT;
   if (num_seqs == 0 || total_q == 0 || max_query_len == 0) return KVQ_OK;
@@ -868,6 +873,9 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
   if (overlap({out, rows}, {query, rows})) return KVQ_ERR_INVALID_ARGUMENT;
   if (max_blocks_per_seq < ceil_div(max_context_len, cache->block_size))
     return KVQ_ERR_INVALID_ARGUMENT;
+  PrefillShape sh;  // asks for the device's SMs: after all that the host can refuse by itself
+  st = prefill_shape(cache, num_seqs, num_q_heads, total_q, max_query_len, max_context_len, &sh);
+  if (st != KVQ_OK) return st;
   if (sh.workspace > 0 && (workspace == nullptr || workspace_bytes < sh.workspace))
     return KVQ_ERR_WORKSPACE;
   if (sh.workspace > 0 && !aligned(workspace, 16)) return KVQ_ERR_INVALID_ARGUMENT;

@@ -278,3 +278,26 @@ def test_matches_the_decode_for_single_tokens():
     ref, tol = p.expect(q, [0, 1, 2, 3], p.d ** -0.5)
     check_close(out, ref, tol)
     check_close(prefill(p, q, np.array([0, 1, 2, 3])), ref, tol)
+
+
+@pytest.mark.parametrize("lens,counts", [([3000], [2]), ([700], [600])])  # keys cut into parts; dequantized ahead
+def test_workspaces_that_do_not_serve_are_refused(lens, counts):
+    p = Paged("int8", lens, 2, 64, 16)
+    cu = offsets(counts)
+    rows, most = sum(counts), max(counts)
+    q = random_query(rows, 8, 64)
+    out = torch.full_like(q, 7.0)
+    n = kvq.kvq_prefill_workspace_size(p.cache, 1, 8, rows, most, p.max_len)
+    assert n > 0
+    ws = torch.zeros(n + 64, dtype=torch.uint8, device=DEV)
+    call = lambda w: kvq.kvq_paged_prefill(p.cache, q, out, ints(cu), p.block_table, p.context_lens, most, p.max_len,
+                                           0.125, 0, 0, w)
+    for bad, status in ((None, 3), (ws[:0], 3), (ws[:16], 3), (ws[8:n + 8], 1), (ws[4:n + 4], 1)):
+        with pytest.raises(kvq.KvqError) as e:
+            call(bad)
+        assert e.value.status == status
+    torch.cuda.synchronize()
+    assert (out == 7).all() and not ws.any()
+    ref, tol = p.expect(q, cu, 0.125)
+    check_close(call(ws[:n]), ref, tol)
+    assert not ws[n:].any() and kvq.kvq_get_device_error() == 0

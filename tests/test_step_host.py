@@ -166,6 +166,21 @@ def test_prefill_shapes(lib):
     assert prefill(lib, s=0, kc=None) == 0 and prefill(lib, total=0, q=None) == 0 and prefill(lib, mq=0, cu=None) == 0
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(w=-1), 1), (dict(sinks=-1), 1), (dict(sm=float("inf")), 1), (dict(sm=float("nan")), 1),
+    (dict(kc=None), 1), (dict(vc=None), 1), (dict(out=None), 1), (dict(q=None), 1), (dict(cu=None), 1),
+    (dict(bt=None), 1), (dict(cl=None), 1),
+    (dict(kc=at(0) + 8), 1), (dict(vc=at(8) + 4), 1), (dict(out=at(16) + 8), 1), (dict(q=at(24) + 2), 1),
+    (dict(cu=at(32) + 2), 1), (dict(bt=at(33) + 1), 1), (dict(cl=at(34) + 2), 1),
+    # 20 rows of 32 heads of 128: the output over the queries, whole or by 16 bytes at either end
+    (dict(out=at(24)), 1), (dict(out=at(24) + 20 * 32 * 128 * 2 - 16), 1), (dict(out=at(24) - 20 * 32 * 128 * 2 + 16), 1),
+    (dict(mb=63), 1), (dict(mb=-1), 1), (dict(s=-1), 1), (dict(total=-1), 1), (dict(mq=-1), 1), (dict(mc=-1), 1),
+    (dict(hq=30), 1), (dict(hq=128), 2), (dict(total=1 << 31), 2), (dict(mc=(1 << 30) + 1), 2)])
+def test_prefill(lib, kw, status):
+    """Refused on the host, before the device is asked for anything."""
+    assert prefill(lib, **kw) == status
+
+
 def test_binding_checks_before_the_call():
     """Tensors that are not on the GPU are refused by the binding itself."""
     if torch.cuda.is_available():
