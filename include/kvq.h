@@ -537,11 +537,18 @@ kvq_status kvq_decode_window(const kvq_cache_desc* cache, void* k_cache, void* v
  * window >= 0 (0: no limit), num_sinks >= 0.
  * workspace: device memory of >= kvq_prefill_workspace_size(...) bytes, 16-byte
  *   aligned (may be NULL when that is 0); its contents on entry do not matter.
- *   Two calls that overlap on the GPU must not share one.  The size covers partial
- *   results where few rows leave the keys to be split, and, for batches with some
- *   hundred rows per sequence or more, the contexts dequantized to 16 bits (4 bytes x
- *   num_seqs x max_context_len, rounded up to 128, x num_kv_heads x head_dim, up to
- *   16 GiB: a tight max_context_len keeps it small).
+ *   Two calls that overlap on the GPU must not share one.
+ *   The size is for every batch of at most num_seqs sequences, total_q rows in all,
+ *   max_query_len rows and max_context_len keys a sequence, with this cache and
+ *   num_q_heads on the current device: asked for once with a server's limits, the
+ *   buffer serves each of its steps (a call itself refuses only a buffer that is too
+ *   small for its own batch, and a smaller batch can need more than a larger one).
+ *   It covers partial results where few rows leave the keys to be split (at most one
+ *   tile of 64, 128 or 256 rows per SM, 5 to 20 MB for head_dim 128), and, where
+ *   total_q allows some hundred rows a sequence or more, the contexts of that many
+ *   sequences dequantized to 16 bits (4 bytes x sequences x max_context_len, rounded up
+ *   to 128, x num_kv_heads x head_dim, up to 16 GiB: a tight max_context_len keeps it
+ *   small).
  * One to three launches on the stream; may be captured into a CUDA graph.
  * Arithmetic: 16-bit operands in the tensor cores, float32 sums and softmax.
  *   int8 and FP8 codes are exact in fp16; asymmetric rows are rounded to fp16

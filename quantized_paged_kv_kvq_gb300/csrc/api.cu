@@ -312,6 +312,35 @@ kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
   }
   return KVQ_OK;
 }
+// A workspace for every batch of at most these sizes, of which the smaller ones can
+// need more: fewer row tiles leave more parts to cut the keys into, and fewer
+// sequences have more row tiles each, which is when keys are dequantized ahead.
+kvq_status prefill_workspace(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
+                             int64_t total_q, int32_t max_query_len, int32_t max_context_len,
+                             size_t* bytes) {
+  PrefillShape sh;
+  kvq_status st = prefill_shape(c, num_seqs, num_q_heads, total_q, max_query_len, max_context_len, &sh);
+  *bytes = 0;
+  if (st != KVQ_OK || sh.tiles == 0) return st;
+  const int64_t sms = sm_count(), g = num_q_heads / c->num_kv_heads, hkv = c->num_kv_heads, d = c->head_dim;
+  // Partial results: splits * tiles * hkv <= SMs (splits > 1 is a floor of their
+  // quotient), of no more rows a tile than these sizes'; and no more splits or rows
+  // than there can be.
+  const int64_t parts = std::min<int64_t>((max_context_len + 255) / 256, 64);
+  if (parts > 1 && 2 * hkv <= sms) {
+    const int64_t longest = (max_query_len * g + sh.rows - 1) / sh.rows;
+    const int64_t ctas = std::min(std::min(num_seqs * longest, sms) * hkv * parts, sms);
+    *bytes = static_cast<size_t>(ctas) * sh.rows * (d + 2) * sizeof(float);
+  }
+  // Contexts dequantized ahead: of as many sequences as the rows are enough for.
+  if (sh.rows == 256 && hkv <= 65535) {
+    const int64_t len = (max_context_len + 127ll) / 128 * 128;
+    const int64_t seqs = std::min<int64_t>(num_seqs, total_q * g / (stage_tiles(c->k_fmt) * 256));
+    const int64_t rows = std::min(std::min<int64_t>(seqs * hkv * len, INT32_MAX / 2), kStageBytes / (4 * d));
+    *bytes += (static_cast<size_t>(2 * rows) * d * 2 + rows / 128 + 15) / 16 * 16;
+  }
+  return KVQ_OK;
+}
 
 }  // namespace
 
@@ -845,10 +874,10 @@ kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t num_s
   if (bytes == nullptr) return KVQ_ERR_INVALID_ARGUMENT;
   kvq_status st = check_prefill(cache, num_seqs, num_q_heads, total_q, max_query_len, max_context_len);
   if (st != KVQ_OK) return st;
-  PrefillShape sh;
-  st = prefill_shape(cache, num_seqs, num_q_heads, total_q, max_query_len, max_context_len, &sh);
+  size_t n = 0;
+  st = prefill_workspace(cache, num_seqs, num_q_heads, total_q, max_query_len, max_context_len, &n);
   if (st != KVQ_OK) return st;
-  *bytes = sh.workspace;
+  *bytes = n;
   return KVQ_OK;
 }
 

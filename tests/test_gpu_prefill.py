@@ -301,3 +301,44 @@ def test_workspaces_that_do_not_serve_are_refused(lens, counts):
     ref, tol = p.expect(q, cu, 0.125)
     check_close(call(ws[:n]), ref, tol)
     assert not ws[n:].any() and kvq.kvq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "kvarn", "bf16"])
+@pytest.mark.parametrize("hkv,g,d", [(8, 4, 128), (1, 1, 64), (2, 8, 128), (16, 1, 64), (3, 5, 64), (96, 1, 64)])
+def test_a_workspace_for_limits_serves_every_batch_within_them(fmt, hkv, g, d):
+    """The size never grows when a limit shrinks."""
+    kf, vf, kvarn = FORMATS[fmt]
+    cache = kvq.alloc_kv_cache(kf, vf, 2, 16, hkv, d, 0.1, 0.1, kvarn, device=DEV)
+    size = lambda s, t, q, c: kvq.kvq_prefill_workspace_size(cache, s, hkv * g, t, q, c)
+    rng = np.random.default_rng(hkv * g)
+    for _ in range(300):
+        s, q, c = (int(np.exp(rng.uniform(0, np.log(hi)))) for hi in (300, 9000, 140000))
+        t = int(rng.integers(q, s * q + 1))
+        most = size(s, t, q, c)
+        for _ in range(8):
+            s2, q2, c2 = (int(rng.integers(1, x + 1)) if rng.random() < 0.6 else x for x in (s, q, c))
+            assert size(s2, min(t, s2 * q2), q2, c2) <= most
+            assert size(s2, int(rng.integers(0, t + 1)), q2, c2) <= most
+
+
+@pytest.mark.parametrize("fmt", ["int8", "kvarn"])
+def test_one_workspace_for_every_step_of_a_server(fmt):
+    """A buffer of the largest step's size serves smaller steps, whose keys are cut into
+    parts or dequantized ahead where the largest step's are not."""
+    p = Paged(fmt, [1300, 700, 64, 900] + [300] * 60, 8, 64, 16)
+    n, most, g = len(p.lens), 600, 4
+    counts = np.full(n, 30)
+    counts[0] = most
+    ws = garbage(kvq.kvq_prefill_workspace_size(p.cache, n, 8 * g, int(counts.sum()), most, p.max_len))
+    for seqs, new in ((range(n), counts), ([0], [1]), ([0], [most]), ([1, 3], [40, 8]), ([2], [64]), (range(4), [1] * 4)):
+        seqs = list(seqs)
+        cu = offsets(np.asarray(new))
+        q = random_query(int(cu[-1]), 8 * g, 64)
+        ids = ints(seqs, torch.int64)
+        out = kvq.kvq_paged_prefill(p.cache, q, torch.empty_like(q), ints(cu), p.block_table[ids].contiguous(),
+                                    p.context_lens[ids].contiguous(), int(max(new)), p.max_len, 0.125, 0, 0, ws)
+        own = garbage(kvq.kvq_prefill_workspace_size(p.cache, len(seqs), 8 * g, int(cu[-1]), int(max(new)), p.max_len))
+        ref = kvq.kvq_paged_prefill(p.cache, q, torch.empty_like(q), ints(cu), p.block_table[ids].contiguous(),
+                                    p.context_lens[ids].contiguous(), int(max(new)), p.max_len, 0.125, 0, 0, own)
+        assert torch.equal(bits(out), bits(ref))
+    assert kvq.kvq_get_device_error() == 0
