@@ -419,7 +419,8 @@ typedef enum {
 
 typedef struct {
   int32_t kind;        /* kvq_rope_kind */
-  double factor;       /* > 0 (kinds other than NONE) */
+  double factor;       /* > 0 (kinds other than NONE); no pair may turn more than 2^24
+                          times a position (a factor below 2^-24 or so) */
   double original_len; /* > 0 (YARN, BANDS) */
   double low, high;    /* turns within original_len: 0 < low < high (YARN, BANDS) */
   double amplitude;    /* multiplies cos and sin (1 for most; YARN's is 0.1 ln(factor) + 1) */
@@ -432,8 +433,9 @@ typedef struct {
  * table: device fp32 [num_positions, rot_dim / 2, 2], 16-byte aligned.
  * rot_dim: even, 2..256.  base > 1.  scaling: NULL for KVQ_ROPE_NONE with
  * amplitude 1.
- * The angle is reduced to a part of a turn in 64-bit integers, so entries are
- * within 3e-7 of amplitude 1 at every position.  num_positions == 0 is a no-op.
+ * The angle is reduced to a part of a turn in 64-bit integers, from turns per position
+ * that the host makes to 2^-65 of a turn, so entries are within 3e-7 of amplitude 1 at
+ * every position.  num_positions < 2^31; 0 is a no-op.
  */
 kvq_status kvq_rope_table(float* table, int64_t num_positions, int32_t rot_dim, double base,
                           const kvq_rope_scaling* scaling, kvq_stream_t stream);

@@ -11,6 +11,7 @@
 #include "../../include/kvq.h"
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "rope_turns.h"
 
 using namespace kvq;
 
@@ -183,39 +184,6 @@ kvq_status decode_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q
   }
   *NC = nc;
   return KVQ_OK;
-}
-
-// The turns (of 2^64) per position of every pair of a rotation; see
-// kvq_rope_kind for the formulas.
-void rope_turns(int rot_dim, double base, const kvq_rope_scaling& sc, RopeTurns* turns) {
-  const double two_pi = 6.283185307179586476925;
-  if (sc.kind == KVQ_ROPE_NTK) base *= pow(sc.factor, rot_dim / (rot_dim - 2.0));
-  double from = 0.0, to = 0.0;  // YARN's ramp
-  if (sc.kind == KVQ_ROPE_YARN) {
-    auto pair_of = [&](double n) {
-      return rot_dim * log(sc.original_len / (two_pi * n)) / (2.0 * log(base));
-    };
-    from = fmax(floor(pair_of(sc.high)), 0.0);
-    to = fmin(ceil(pair_of(sc.low)), rot_dim - 1.0);
-  }
-  for (int i = 0; i < kMaxRopePairs; ++i) {
-    turns->t[i] = 0;
-    if (i >= rot_dim / 2) continue;
-    double theta = pow(base, -2.0 * i / rot_dim);
-    if (sc.kind == KVQ_ROPE_LINEAR) theta /= sc.factor;
-    if (sc.kind == KVQ_ROPE_YARN) {
-      const double g = fmin(fmax((i - from) / fmax(to - from, 0.001), 0.0), 1.0);
-      theta = theta / sc.factor * g + theta * (1.0 - g);
-    }
-    if (sc.kind == KVQ_ROPE_BANDS) {
-      const double n = sc.original_len * theta / two_pi;
-      const double h = fmin(fmax((n - sc.low) / (sc.high - sc.low), 0.0), 1.0);
-      theta = theta / sc.factor * (1.0 - h) + theta * h;
-    }
-    double part = theta / two_pi;
-    part -= floor(part);  // whole turns change nothing
-    turns->t[i] = static_cast<unsigned long long>(ldexp(part, 64));  // part <= 1 - 2^-53: fits
-  }
 }
 
 // Checks shared by the norm and rotation calls; fills what they share of *a.
@@ -771,7 +739,7 @@ kvq_status kvq_rope_table(float* table, int64_t num_positions, int32_t rot_dim, 
         isfinite(sc.high)))
     return KVQ_ERR_INVALID_ARGUMENT;
   RopeTurns turns;
-  rope_turns(rot_dim, base, sc, &turns);
+  if (!rope_turns(rot_dim, base, sc, &turns)) return KVQ_ERR_INVALID_ARGUMENT;
   if (num_positions == 0) return KVQ_OK;
   if (!table || !aligned(table, 16)) return KVQ_ERR_INVALID_ARGUMENT;
   const int sms = sm_count();

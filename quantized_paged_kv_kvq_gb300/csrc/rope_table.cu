@@ -22,11 +22,12 @@ namespace {
 constexpr int kRun = 8;        // positions per thread and step
 constexpr int kThreads = 256;
 
-// (cos, sin) of `turn` / 2^64 turns.  The 32 bits kept of the part beyond a quarter
-// turn leave 2^-33 turns, 7e-10 radians.
+// (cos, sin) of `turn` / 2^64 turns.  The part beyond a quarter turn is rounded to 32
+// bits of a turn: off by 2^-33 turns, 7e-10 radians, at most.
 __device__ __forceinline__ float2 cos_sin_turn(unsigned long long turn) {
   const unsigned q = static_cast<unsigned>((turn + (1ull << 61)) >> 62);  // nearest quarter
-  const int rest = static_cast<int>((turn - (static_cast<unsigned long long>(q) << 62)) >> 32);
+  const long long beyond = static_cast<long long>(turn - (static_cast<unsigned long long>(q) << 62));  // |.| <= 2^61
+  const int rest = static_cast<int>((beyond + (1ll << 31)) >> 32);
   float s, c;
   sincospif(static_cast<float>(rest) * 0x1p-31f, &s, &c);  // pi * (2 * turns), |.| <= pi / 4
   const float x = (q & 1) ? s : c, y = (q & 1) ? c : s;

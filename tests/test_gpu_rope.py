@@ -1,4 +1,7 @@
 """kvq_rope_table, kvq_norm_rope and kvq_norm_rope_write."""
+import math
+from decimal import Decimal, getcontext
+
 import numpy as np
 import pytest
 import torch
@@ -165,3 +168,34 @@ def test_no_tokens_and_no_heads():
     qo, none = torch.empty((3, 4, 64), dtype=torch.bfloat16, device=DEV), torch.empty((3, 0, 64), dtype=torch.bfloat16, device=DEV)
     kvq.kvq_norm_rope(rope, q, none, ints([1, 2, 3]), qo, none)
     check_rotated(rope, q, None, ints([1, 2, 3]), qo)
+
+
+def exact_rotation(p, base, i, rot):
+    """cos and sin of p * base^(-2i/rot), from decimals of 60 digits."""
+    getcontext().prec = 60
+    turn = Decimal("6.283185307179586476925286766559005768394338798750211641949889184615632812572417997256")
+    angle = Decimal(p) * (Decimal(base).ln() * (-2 * i) / rot).exp()
+    x = float(angle - turn * int(angle / turn))  # rounded by 4e-16
+    return math.cos(x), math.sin(x)
+
+
+@pytest.mark.parametrize("base", [1.298, 1.175, 10000.0])
+def test_table_at_the_last_positions(base):
+    """Every pair up to the last position that the call takes."""
+    n = (1 << 31) - 1  # 34 GB
+    table = torch.empty((n, 2, 2), device=DEV)
+    kvq.kvq_rope_table(table, base)
+    pos = [n - 1, n - 2, n - 12345, (1 << 30) + 7, 1 << 24] + list(range(n - 300, n - 100))
+    got = table[ints(pos, torch.int64)].cpu().numpy()
+    ref = np.array([[exact_rotation(p, base, i, 4) for i in range(2)] for p in pos])
+    assert np.abs(got - ref).max() <= 3e-7
+
+
+def test_table_at_far_positions_of_every_pair():
+    n = 1 << 24  # 8.6 GB
+    table = torch.empty((n, 64, 2), device=DEV)
+    kvq.kvq_rope_table(table, 1e6)
+    pos = [n - 1, n - 12345, 8388607, 5000001]
+    got = table[ints(pos, torch.int64)].cpu().numpy()
+    ref = np.array([[exact_rotation(p, 1e6, i, 128) for i in range(64)] for p in pos])
+    assert np.abs(got - ref).max() <= 3e-7

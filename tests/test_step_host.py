@@ -187,3 +187,8 @@ def test_binding_checks_before_the_call():
         pytest.skip("needs a machine without a GPU")
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         kvq.kvq_rope_table(torch.empty(4, 8, 2), 10000.0)
+
+
+def test_rope_table_factors_without_a_fraction_to_keep(lib):
+    assert table(lib, scaling=(1, 1e-9, 1.0, 1.0, 2.0, 1.0)) == 1  # 1.6e8 turns a position
+    assert table(lib, n=0, scaling=(1, 1e-6, 1.0, 1.0, 2.0, 1.0)) == 0
