@@ -553,8 +553,9 @@ kvq_status kvq_decode_window(const kvq_cache_desc* cache, void* k_cache, void* v
  *   small).
  * One to three launches on the stream; may be captured into a CUDA graph.
  * Arithmetic: 16-bit operands in the tensor cores, float32 sums and softmax.
- *   int8 and FP8 codes are exact in fp16; asymmetric rows are rounded to fp16
- *   once dequantized ((code * scale + zero_point) [* sigma]; past 65504 infinite);
+ *   int8 and FP8 codes are exact in fp16; asymmetric rows are rounded once to fp16
+ *   when they are dequantized ((code * scale + zero_point) [* sigma] past 65504 is
+ *   infinite; only the result counts, not the product on the way);
  *   the query is rounded to fp16 as in kvq_paged_decode (KVQ_DEVERR_QUERY_RANGE);
  *   probabilities are rounded to fp16.  The 16-bit cache uses bf16 throughout.
  *   A value (V) that is not finite makes the rows that see it not finite; rows

@@ -215,19 +215,53 @@ __device__ __forceinline__ Span row_span(const PrefillArgs& a, int n, int q, int
 }
 __device__ __forceinline__ int tile_key(const Span& s, int i) { return kKeys * (i < s.kept ? i : i + s.skip); }
 
+// A row's fields, each an fp16 value twice, as dequantize16 takes them.  Rotated rows:
+// scale and zero point times the deviation, in float32 (products of 11 bits each: exact).
+template <bool KVARN>
+struct RowFields {
+  uint32_t s, z;
+  __device__ __forceinline__ RowFields(uint32_t scale, uint32_t zero, uint32_t) : s(scale), z(zero) {}
+};
+template <>
+struct RowFields<true> {
+  float s, z;
+  __device__ __forceinline__ RowFields(uint32_t scale, uint32_t zero, uint32_t deviation) {
+    const float g = __half2float(__ushort_as_half(static_cast<uint16_t>(deviation)));
+    s = __half2float(__ushort_as_half(static_cast<uint16_t>(scale))) * g;
+    z = __half2float(__ushort_as_half(static_cast<uint16_t>(zero))) * g;
+  }
+};
+
 // 16 bytes of codes as 16-bit operands: 16 (8-bit codes) or 32 (int4) fp16
-// values, in order.  s, z: fp16 pairs of the row's scale and zero point, and g of
-// its deviation (rotated rows).
+// values, in order.  Asymmetric rows are rounded once, to fp16: code * scale + zero
+// point by a fused fp16 operation, rotated rows (code * (scale * deviation) + zero point *
+// deviation) in float32, where code * scale may pass fp16's range on the way.
 template <int F, bool KVARN>
-__device__ __forceinline__ void dequantize16(const uint4& raw, uint32_t s, uint32_t z, uint32_t g,
+__device__ __forceinline__ void dequantize16(const uint4& raw, const RowFields<KVARN>& row,
                                              uint32_t (&o)[F == INT4A ? 16 : 8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   constexpr uint32_t K64 = 0x64646464u;
-  auto affine = [&](uint32_t c) {  // fp16(c * s + z), then fp16(. * deviation)
-    const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&s),
-                              *reinterpret_cast<const __half2*>(&z));
-    const __half2 y = KVARN ? __hmul2(x, *reinterpret_cast<const __half2*>(&g)) : x;
-    return *reinterpret_cast<const uint32_t*>(&y);
+  auto affine2 = [&](uint32_t c, uint32_t* p) {  // four codes, a byte each
+    if constexpr (KVARN) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(prmt(c, 0x4B000000u, 0x7440u + e));  // 2^23 + code
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        float u, v;
+        add2(u, v, x[e], x[e + 1], -8388608.f, -8388608.f);
+        fma2(u, v, u, v, row.s, row.s, row.z, row.z);
+        p[e / 2] = pack_half2(u, v);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t h = hsub2_u32(prmt(c, K64, e ? 0x4342u : 0x4140u), 0x64006400u);
+        const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&row.s),
+                                  *reinterpret_cast<const __half2*>(&row.z));
+        p[e] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    }
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -242,15 +276,11 @@ __device__ __forceinline__ void dequantize16(const uint4& raw, uint32_t s, uint3
       o[2 * i] = prmt(w[i], 0u, 0x1404);
       o[2 * i + 1] = prmt(w[i], 0u, 0x3424);
     } else if constexpr (F == UINT8A) {
-      o[2 * i] = affine(hsub2_u32(prmt(w[i], K64, 0x4140), 0x64006400u));
-      o[2 * i + 1] = affine(hsub2_u32(prmt(w[i], K64, 0x4342), 0x64006400u));
+      affine2(w[i], o + 2 * i);
     } else {  // INT4A: element 2i in the low nibble of byte i
       const uint32_t lo = w[i] & 0x0F0F0F0Fu, hi = (w[i] >> 4) & 0x0F0F0F0Fu;
-      const uint32_t a = prmt(lo, hi, 0x5140), b = prmt(lo, hi, 0x7362);
-      o[4 * i] = affine(hsub2_u32(prmt(a, K64, 0x4140), 0x64006400u));
-      o[4 * i + 1] = affine(hsub2_u32(prmt(a, K64, 0x4342), 0x64006400u));
-      o[4 * i + 2] = affine(hsub2_u32(prmt(b, K64, 0x4140), 0x64006400u));
-      o[4 * i + 3] = affine(hsub2_u32(prmt(b, K64, 0x4342), 0x64006400u));
+      affine2(prmt(lo, hi, 0x5140), o + 4 * i);
+      affine2(prmt(lo, hi, 0x7362), o + 4 * i + 2);
     }
   }
 }
@@ -480,7 +510,7 @@ struct Producer {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         uint32_t o[4 * P::OUT];
-        dequantize16<F, KVARN>(w[u], sc[u], zp[u], sg[u], o);
+        dequantize16<F, KVARN>(w[u], {sc[u], zp[u], sg[u]}, o);
         if constexpr (IS_V && is_asym(F)) {  // |code * s + z| g is at most this
           float top = fmaf(half_of_pair(sc[u]), static_cast<float>(asym_levels(F)), half_of_pair(zp[u]));
           if (KVARN) top *= half_of_pair(sg[u]);
@@ -752,8 +782,11 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
           v = e4m3x2_to_f16x2(row[d]) & 0xFFFFu;
         } else if (s.fields > 0) {
           const int c = s.fmt == INT4A ? (row[d / 2] >> (4 * (d & 1))) & 15 : row[d];
-          __half x = __hfma(__int2half_rn(c), sc, zp);
-          if (s.fields == 3) x = __hmul(x, sg);
+          __half x = __hfma(__int2half_rn(c), sc, zp);  // as dequantize16
+          if (s.fields == 3) {
+            const float g = __half2float(sg);
+            x = __float2half_rn(fmaf(static_cast<float>(c), __half2float(sc) * g, __half2float(zp) * g));
+          }
           v = __half_as_ushort(x);
         } else {
           return;
@@ -1249,7 +1282,7 @@ __device__ __forceinline__ bool stage_tile(const PrefillArgs& a, const Source& s
           f[k] = x | x << 16;
         }
       }
-      dequantize16<F, KVARN>(w, f[0], f[1], f[2], o);
+      dequantize16<F, KVARN>(w, {f[0], f[1], f[2]}, o);
     }
     if constexpr (IS_V && F != INT8) {
       nf = track_not_finite<F == BF16>(0u, o);

@@ -342,3 +342,19 @@ def test_one_workspace_for_every_step_of_a_server(fmt):
                                     p.context_lens[ids].contiguous(), int(max(new)), p.max_len, 0.125, 0, 0, own)
         assert torch.equal(bits(out), bits(ref))
     assert kvq.kvq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("q", [3, 100, 700])  # keys cut into parts, by each CTA, and ahead
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_rotated_rows_whose_deviation_brings_them_into_range(which, q):
+    """code * scale + zero point past 65,504, times a small deviation: some hundred at most."""
+    p = Paged("kvarn", [q + 700], 2, 64, 16, seed=q)
+    meta = getattr(p.cache, which + "_meta")
+    for t in (5, 400, 640):  # seen by every row
+        b, off = p.table[0, t // 16], t % 16
+        meta[b, 0, :, off] = torch.tensor([6000.0 if which == "k" else 400.0, 30000.0, 1e-4], dtype=torch.float16, device=DEV)
+    cu = np.array([0, q])
+    x = random_query(q, 8, 64)
+    ref, tol = p.expect(x, cu, 0.125)
+    check_close(prefill(p, x, cu), ref, tol)
+    assert kvq.kvq_get_device_error() == 0
