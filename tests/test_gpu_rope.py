@@ -199,3 +199,31 @@ def test_table_at_far_positions_of_every_pair():
     got = table[ints(pos, torch.int64)].cpu().numpy()
     ref = np.array([[exact_rotation(p, 1e6, i, 128) for i in range(64)] for p in pos])
     assert np.abs(got - ref).max() <= 3e-7
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3_int8", "e5m2"])
+@pytest.mark.parametrize("which", ["k", "v", "kv"])
+@pytest.mark.parametrize("d,interleaved", [(128, False), (64, True)])
+def test_write_with_head_scales(fmt, which, d, interleaved):
+    """Each tensor with its own scales per kv-head, or with its one scale: the two calls' codes."""
+    kf, vf, _ = FORMATS[fmt]
+    t, hq, hkv = 45, 12, 6
+    q, k, v = packed(t, hq, hkv, d, seed=d)
+    rope = make_rope(d, d, interleaved, True)
+    pos, slots = ints(np.arange(t) * 7 % 500), ints(np.random.default_rng(1).permutation(64)[:t], torch.int64)
+    a, b = (kvq.alloc_kv_cache(kf, vf, 4, 16, hkv, d, 0.04, 0.05, device=DEV, fill=0x5A) for _ in range(2))
+    for c in (a, b):
+        if "k" in which:
+            c.k_head_scales = torch.linspace(0.02, 0.09, hkv, device=DEV)
+        if "v" in which:
+            c.v_head_scales = torch.linspace(0.11, 0.03, hkv, device=DEV)
+    qo, ko = torch.empty((t, hq, d), dtype=torch.bfloat16, device=DEV), torch.empty((t, hkv, d), dtype=torch.bfloat16, device=DEV)
+    kvq.kvq_norm_rope(rope, q, k, pos, qo, ko)
+    kvq.kvq_write_cache(a, ko, v, slots)
+    kvq.kvq_norm_rope_write(rope, b, q, k, v, pos, slots, torch.empty_like(qo))
+    assert torch.equal(a.k_cache, b.k_cache) and torch.equal(a.v_cache, b.v_cache)
+    plain = kvq.alloc_kv_cache(kf, vf, 4, 16, hkv, d, 0.04, 0.05, device=DEV, fill=0x5A)
+    kvq.kvq_norm_rope_write(rope, plain, q, k, v, pos, slots, torch.empty_like(qo))
+    assert torch.equal(plain.k_cache, b.k_cache) == ("k" not in which)
+    assert torch.equal(plain.v_cache, b.v_cache) == ("v" not in which)
+    assert kvq.kvq_get_device_error() == 0
