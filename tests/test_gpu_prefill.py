@@ -358,3 +358,100 @@ def test_rotated_rows_whose_deviation_brings_them_into_range(which, q):
     ref, tol = p.expect(x, cu, 0.125)
     check_close(prefill(p, x, cu), ref, tol)
     assert kvq.kvq_get_device_error() == 0
+
+
+NOT_FINITE = {"parts": (1500, 3, 1498), "by_each_cta": (100, 100, 60), "ahead": (1100, 1100, 60)}  # keys, rows, the key
+
+
+@pytest.mark.parametrize("way", sorted(NOT_FINITE))
+@pytest.mark.parametrize("fmt", ["uint8", "int4", "kvarn", "e4m3", "e5m2", "bf16"])
+def test_one_value_row_not_finite(fmt, way, monkeypatch):
+    """Rows that see it are not finite in the elements that its dequantized row is not
+    (rotated rows: in all); everything else is what it is without it."""
+    n, rows, key = NOT_FINITE[way]
+    monkeypatch.setitem(FORMATS, "e4m3", ("fp8_e4m3", "fp8_e4m3", False))
+    p = Paged(fmt, [n], 2, 64, 16)
+    cu = np.array([0, rows])
+    q = random_query(rows, 8, 64)
+    b, off = p.table[0, key // 16], key % 16
+    clean = prefill(p, q, cu)
+    bad = torch.zeros(64, dtype=torch.bool, device=DEV)
+    if p.cache.v_meta is not None:
+        code = p.cache.v_cache[b, off, 0]
+        if fmt == "int4":
+            code = torch.stack((code & 15, code >> 4), -1).flatten()
+        scale = 5000.0 if fmt == "int4" else 300.0
+        p.cache.v_meta[b, 0, :2, off] = torch.tensor([scale, 0.0], dtype=torch.float16, device=DEV)
+        bad = torch.isinf((code.double() * scale).half())
+        if fmt == "kvarn":
+            p.cache.v_meta[b, 0, 2, off] = 1.0
+            bad = torch.full_like(bad, bool(bad.any()))
+    elif fmt == "e4m3":
+        bad[[5, 63]] = True
+        p.cache.v_cache[b, off, 0, 5], p.cache.v_cache[b, off, 0, 63] = 0x7F, 0xFF  # its NaN
+    else:
+        bad[[5, 9, 40]] = True
+        t = {"e5m2": torch.float8_e5m2, "bf16": torch.bfloat16}[fmt]
+        values = torch.tensor([float("inf"), float("nan"), -float("inf")]).to(t).view(torch.uint8).to(DEV)
+        row = p.cache.v_cache[b, off, 0].view(64, -1)
+        row[[5, 9, 40]] = values.view(3, -1)
+    assert bad.any()
+    out = prefill(p, q, cu)
+    assert kvq.kvq_get_device_error() == 0
+    first = key - (n - rows)  # the first row that sees the key
+    assert torch.equal(bits(out[:first]), bits(clean[:first])) and torch.equal(bits(out[:, 4:]), bits(clean[:, 4:]))
+    finite = torch.isfinite(out[first:, :4])
+    assert (finite == ~bad).all()
+    if not bad.all():  # the other elements against the oracle, where they are finite
+        good = (~bad).cpu().numpy()
+        with np.errstate(all="ignore"):
+            ref, tol = p.expect(q, cu, 0.125)
+        # within the derived bound; check_close's mean limit of 2e-3 is for values of size one
+        # (of outputs near 10 the rounding to bf16 alone is off by 10 * 2^-10 = 1e-2 on average)
+        err = np.abs(out[first:, :4][..., ~bad].double().cpu().numpy() - ref[first:, :4][..., good])
+        assert (err <= tol[first:, :4][..., good]).all()
+    # a NaN among the row's fields: all of the row
+    if p.cache.v_meta is not None:
+        for field in range(p.cache.v_meta.shape[2]):
+            keep = p.cache.v_meta[b, 0, field, off].clone()
+            p.cache.v_meta[b, 0, field, off] = float("nan")
+            out = prefill(p, q, cu)
+            assert torch.equal(bits(out[:first]), bits(clean[:first])) and torch.equal(bits(out[:, 4:]), bits(clean[:, 4:]))
+            assert not torch.isfinite(out[first:, :4]).any()
+            p.cache.v_meta[b, 0, field, off] = keep
+
+
+@pytest.mark.parametrize("way", sorted(NOT_FINITE))
+@pytest.mark.parametrize("fmt", ["uint8", "kvarn", "e5m2", "bf16"])
+def test_one_key_row_not_finite(fmt, way):
+    """Rows that see a key that is NaN are NaN, and no others."""
+    n, rows, key = NOT_FINITE[way]
+    p = Paged(fmt, [n], 2, 64, 16)
+    cu = np.array([0, rows])
+    q = random_query(rows, 8, 64)
+    b, off = p.table[0, key // 16], key % 16
+    clean = prefill(p, q, cu)
+    if p.cache.k_meta is not None:
+        p.cache.k_meta[b, 0, 1, off] = float("nan")
+    else:
+        p.cache.k_cache[b, off, 0] = 0x7F if fmt == "e5m2" else 0xFF
+    out = prefill(p, q, cu)
+    first = key - (n - rows)
+    assert torch.equal(bits(out[:first]), bits(clean[:first])) and torch.equal(bits(out[:, 4:]), bits(clean[:, 4:]))
+    assert torch.isnan(out[first:, :4]).all()
+    assert kvq.kvq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("way", sorted(NOT_FINITE))
+def test_large_finite_values(way):
+    """Rows near the end of fp16's range, whose bound passes it although no value does."""
+    n, rows, key = NOT_FINITE[way]
+    p = Paged("uint8", [n], 2, 64, 16)
+    b, off = p.table[0, key // 16], key % 16
+    p.cache.v_meta[b, 0, :2, off] = torch.tensor([200.0, -30000.0], dtype=torch.float16, device=DEV)
+    cu = np.array([0, rows])
+    q = random_query(rows, 8, 64)
+    ref, tol = p.expect(q, cu, 0.125)
+    out = prefill(p, q, cu)
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert (err <= tol).all() and kvq.kvq_get_device_error() == 0
