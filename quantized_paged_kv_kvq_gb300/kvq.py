@@ -152,6 +152,8 @@ class KVCache:
     k_cache / v_cache: uint8 [num_blocks, block_size, num_kv_heads, row_bytes]
     k_meta / v_meta:   fp16 [num_blocks, num_kv_heads, F, block_size] (asymmetric formats)
     signs:             int8 [head_dim] of +-1 (KVarN rotation) or None
+
+    The tensors may hold more blocks than num_blocks.
     """
     k_fmt: str
     v_fmt: str
@@ -390,6 +392,32 @@ def _rows(dev: int, name: str, t: torch.Tensor, shape) -> int:
     return s0 if n > 1 else (heads * d + 7) // 8 * 8
 
 
+def _cache_desc(dev: int, cache: KVCache) -> _CacheDesc:
+    """The cache's description, once its tensors are what it says: the kernels write and
+    read through them, and see nothing but addresses."""
+    c, rot = cache, cache.varnorm_rotate
+    blocks, bs, hkv = c.num_blocks, c.block_size, c.num_kv_heads
+    specs = [("k_cache", c.k_cache, torch.uint8, (bs, hkv, row_bytes(c.k_fmt, c.head_dim))),
+             ("v_cache", c.v_cache, torch.uint8, (bs, hkv, row_bytes(c.v_fmt, c.head_dim)))]
+    for name, fmt, meta in (("k_meta", c.k_fmt, c.k_meta), ("v_meta", c.v_fmt, c.v_meta)):
+        fields = meta_fields(fmt, rot)
+        if fields:
+            _need(meta is not None, f"{name} is missing: {fmt} rows have {fields} fields")
+            specs.append((name, meta, torch.float16, (hkv, fields, bs)))
+    for name, t, dtype, shape in specs:
+        if (t.dtype is not dtype or t.dim() != 4 or t.shape[0] < blocks or t.shape[1:] != shape
+                or t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(blocks, *shape)} on CUDA device {dev}, "
+                             f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    if rot and c.signs is not None:
+        _tensors(dev, ("signs", c.signs, torch.int8, (c.head_dim,)))
+    if c.k_head_scales is not None:
+        _tensors(dev, ("k_head_scales", c.k_head_scales, torch.float32, (hkv,)))
+    if c.v_head_scales is not None:
+        _tensors(dev, ("v_head_scales", c.v_head_scales, torch.float32, (hkv,)))
+    return c.desc()
+
+
 def _workspace(dev: int, workspace: Optional[torch.Tensor]) -> int:
     if workspace is None:
         return 0
@@ -522,7 +550,7 @@ def kvq_norm_rope_write(rope: Rope, cache: KVCache, query: torch.Tensor, key: to
     ks, vs = _rows(dev, "key", key, kv), _rows(dev, "value", value, kv)
     _tensors(dev, ("positions", positions, torch.int32, (t,)),
              ("slot_mapping", slot_mapping, torch.int64, (t,)))
-    r, c = rope.desc(d, dev), cache.desc()
+    r, c = rope.desc(d, dev), _cache_desc(dev, cache)
     st = load_library().kvq_norm_rope_write(
         ctypes.byref(r), ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(),
         query_out.data_ptr(), qos, query.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
@@ -550,7 +578,7 @@ def kvq_decode_window(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
     if new_key is not None:
         kv = (s, cache.num_kv_heads, cache.head_dim)
         ks, vs = _rows(dev, "new_key", new_key, kv), _rows(dev, "new_value", new_value, kv)
-    c = cache.desc()
+    c = _cache_desc(dev, cache)
     st = load_library().kvq_decode_window(
         ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), _address(new_key),
         _address(new_value), ks, vs, out.data_ptr(), query.data_ptr(), s, hq, block_table.data_ptr(),
@@ -586,7 +614,7 @@ def kvq_paged_prefill(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
              ("cu_query", cu_query, torch.int32, (s + 1,)),
              ("block_table", block_table, torch.int32, (s, width)),
              ("context_lens", context_lens, torch.int32, (s,)))
-    c = cache.desc()
+    c = _cache_desc(dev, cache)
     st = load_library().kvq_paged_prefill(
         ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), out.data_ptr(),
         query.data_ptr(), cu_query.data_ptr(), s, n, max_query_len, hq, block_table.data_ptr(), width,

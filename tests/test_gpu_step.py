@@ -2,6 +2,8 @@
 and store its tokens, attend to the cache; prompts first, then single tokens, then a
 request that ends and one that joins.  Every token's key and value are kept on the side
 and the whole attention is compared with the definition on them."""
+from dataclasses import replace
+
 import numpy as np
 import pytest
 import torch
@@ -215,3 +217,31 @@ def test_the_binding_refuses_wrong_tensors():
             kvq.kvq_norm_rope(rope, *args, torch.empty_like(q[:3]), torch.empty_like(k))
     with pytest.raises(kvq.KvqError):  # an output over another input
         kvq.kvq_norm_rope(rope, q[:3], k, ints([0, 1, 2]), torch.empty_like(q[:3]), q[:3, :HKV])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "kvarn"])
+def test_the_binding_refuses_caches_that_do_not_fit(fmt):
+    """A cache with a tensor elsewhere, of another type or too small reaches no kernel."""
+    loop = Loop(fmt, 0, 0)
+    loop.step([20, 1, 1, 1])
+    q = torch.zeros((SEQS, HQ, D), dtype=torch.bfloat16, device=DEV)
+    kv = torch.zeros((SEQS, HKV, D), dtype=torch.bfloat16, device=DEV)
+    out, ws, pos = torch.empty_like(q), garbage(1 << 22), ints([0, 1, 2, 3])
+    calls = (lambda c: kvq.kvq_decode_window(c, q, out, loop.block_table, loop.lens, 20, 0.1, 5, workspace=ws),
+             lambda c: kvq.kvq_paged_prefill(c, q, out, ints([0, 1, 2, 3, 4]), loop.block_table, loop.lens, 1, 20, 0.1, workspace=ws),
+             lambda c: kvq.kvq_norm_rope_write(loop.rope, c, q, kv, kv, pos, ints([0, 1, 2, 3], torch.int64), out))
+    for call in calls:
+        call(loop.cache)
+    torch.cuda.synchronize()
+    bad = [dict(k_cache=loop.cache.k_cache.cpu()), dict(v_cache=loop.cache.v_cache.float()),
+           dict(k_cache=loop.cache.k_cache[:1]), dict(num_blocks=loop.cache.num_blocks + 1),
+           dict(v_cache=loop.cache.v_cache.transpose(1, 2))]
+    if loop.cache.k_meta is not None:
+        bad += [dict(k_meta=None), dict(v_meta=loop.cache.v_meta.float()), dict(signs=loop.cache.signs.cpu())]
+    for kw in bad:
+        for call in calls:
+            with pytest.raises(ValueError):
+                call(replace(loop.cache, **kw))
+    for call in calls:
+        call(loop.cache)
+    assert kvq.kvq_get_device_error() == 0

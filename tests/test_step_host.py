@@ -192,3 +192,44 @@ def test_binding_checks_before_the_call():
 def test_rope_table_factors_without_a_fraction_to_keep(lib):
     assert table(lib, scaling=(1, 1e-9, 1.0, 1.0, 2.0, 1.0)) == 1  # 1.6e8 turns a position
     assert table(lib, n=0, scaling=(1, 1e-6, 1.0, 1.0, 2.0, 1.0)) == 0
+
+
+CACHE_FORMATS = [("int8", "fp8_e4m3", False), ("int4_asym", "uint8_asym", True), ("uint8_asym", "uint8_asym", False), ("bf16", "bf16", False)]
+
+
+def host_cache(kf, vf, kvarn):
+    signs = torch.ones(64, dtype=torch.int8) if kvarn else None
+    c = kvq.alloc_kv_cache(kf, vf, 3, 16, 2, 64, 0.1, 0.1, kvarn, signs, device="cpu")
+    if not kf.endswith("asym") and kf != "bf16":
+        c.k_head_scales, c.v_head_scales = torch.ones(2), torch.ones(2)
+    return c
+
+
+@pytest.mark.parametrize("kf,vf,kvarn", CACHE_FORMATS)
+def test_caches_whose_tensors_do_not_fit_are_refused(kf, vf, kvarn):
+    """The check that the binding makes before a cache's addresses leave it (here of CPU
+    tensors, which are those of device -1)."""
+    kvq._cache_desc(-1, host_cache(kf, vf, kvarn))
+    more = host_cache(kf, vf, kvarn)
+    more.num_blocks = 2  # tensors with a block more than it is told of
+    kvq._cache_desc(-1, more)
+    wrong = {}
+    for name in ("k_cache", "v_cache", "k_meta", "v_meta", "signs", "k_head_scales", "v_head_scales"):
+        t = getattr(host_cache(kf, vf, kvarn), name)
+        if t is None:
+            continue
+        wrong[name] = [t.double(), t[..., :-1], t[:1], torch.stack((t, t), -1)[..., 0], t.unsqueeze(0)]
+        if name.endswith("meta"):
+            wrong[name] += [None, t[:, :, :1].contiguous(), t[:, :1].contiguous()]
+    for name, values in wrong.items():
+        for x in values:
+            c = host_cache(kf, vf, kvarn)
+            setattr(c, name, x)
+            with pytest.raises(ValueError, match=name):
+                kvq._cache_desc(-1, c)
+        with pytest.raises(ValueError, match="k_cache"):  # on another device than the call's
+            kvq._cache_desc(0, host_cache(kf, vf, kvarn))
+    c = host_cache(kf, vf, kvarn)
+    c.num_blocks = 4  # more blocks than its tensors hold
+    with pytest.raises(ValueError, match="k_cache"):
+        kvq._cache_desc(-1, c)
