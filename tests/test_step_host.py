@@ -1,5 +1,7 @@
 """The serving-step entry points refuse bad arguments on the host, without a GPU."""
 import ctypes
+import importlib.util
+import sys
 
 import pytest
 import torch
@@ -233,3 +235,30 @@ def test_caches_whose_tensors_do_not_fit_are_refused(kf, vf, kvarn):
     c.num_blocks = 4  # more blocks than its tensors hold
     with pytest.raises(ValueError, match="k_cache"):
         kvq._cache_desc(-1, c)
+
+
+def test_the_binding_does_without_torchs_shortcuts(monkeypatch):
+    """A torch without its private device and stream queries: the public ones serve."""
+    class Stream:
+        def __init__(self, dev):
+            self.cuda_stream = 100 + dev
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 5)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location("kvq_without_shortcuts", kvq.__file__)
+    other = importlib.util.module_from_spec(spec)
+    monkeypatch.setitem(sys.modules, spec.name, other)
+    spec.loader.exec_module(other)
+
+    class OnDevice:
+        def __init__(self, dev):
+            self.dev = self.device = dev
+
+        def get_device(self):
+            return self.dev
+    assert other._device_of("x", OnDevice(5)) == 5 and other._raw_stream(5, None) == 105
+    assert other._raw_stream(5, Stream(7)) == 107
+    for dev in (4, -1):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            other._device_of("x", OnDevice(dev))
