@@ -378,6 +378,13 @@ def _device_of(name: str, t: torch.Tensor) -> int:
     return dev
 
 
+def _int32(**values) -> None:
+    """Refuses numbers that the C call's 32-bit arguments do not hold (ctypes would cut them)."""
+    for name, v in values.items():
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError(f"{name} must fit 32 bits, got {v}")
+
+
 def _tensors(dev: int, *specs) -> None:
     """Each (name, tensor, dtype, shape): a contiguous tensor of CUDA device dev."""
     for name, t, dtype, shape in specs:
@@ -455,6 +462,7 @@ def kvq_plan_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tabl
     (int32 [2]) the state after the step."""
     s, t, i32 = context_lens.numel(), slot_mapping.numel(), torch.int32
     width, free = block_table.shape[-1], free_blocks.numel()
+    _int32(block_size=block_size, num_blocks=num_blocks, free_blocks=free)
     dev = _device_of("slot_mapping", slot_mapping)
     _tensors(dev, ("context_lens", context_lens, i32, (s,)), ("new_lens", new_lens, i32, (s,)),
              ("block_table", block_table, i32, (s, width)), ("free_blocks", free_blocks, i32, (free,)),
@@ -575,6 +583,7 @@ def kvq_decode_window(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
     see the last `window` tokens of their context and its first num_sinks."""
     s, hq, _ = query.shape
     rows, width = (s, hq, cache.head_dim), block_table.shape[-1]
+    _int32(max_context_len=max_context_len, window=window, num_sinks=num_sinks, num_ctas=num_ctas)
     dev = _device_of("query", query)
     _tensors(dev, ("query", query, torch.bfloat16, rows), ("out", out, torch.bfloat16, rows),
              ("block_table", block_table, torch.int32, (s, width)),
@@ -596,6 +605,7 @@ def kvq_decode_window(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
 
 def kvq_prefill_workspace_size(cache: KVCache, num_seqs: int, num_q_heads: int, total_q: int,
                                max_query_len: int, max_context_len: int) -> int:
+    _int32(num_seqs=num_seqs, num_q_heads=num_q_heads, max_query_len=max_query_len, max_context_len=max_context_len)
     n = ctypes.c_size_t(0)
     c = cache.desc()
     _check(load_library().kvq_prefill_workspace_size(ctypes.byref(c), num_seqs, num_q_heads,
@@ -615,6 +625,7 @@ def kvq_paged_prefill(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
     s = context_lens.numel()
     n, hq, _ = query.shape
     rows, width = (n, hq, cache.head_dim), block_table.shape[-1]
+    _int32(max_query_len=max_query_len, max_context_len=max_context_len, window=window, num_sinks=num_sinks)
     dev = _device_of("query", query)
     _tensors(dev, ("query", query, torch.bfloat16, rows), ("out", out, torch.bfloat16, rows),
              ("cu_query", cu_query, torch.int32, (s + 1,)),

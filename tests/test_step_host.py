@@ -262,3 +262,24 @@ def test_the_binding_does_without_torchs_shortcuts(monkeypatch):
     for dev in (4, -1):
         with pytest.raises(ValueError, match="current CUDA device"):
             other._device_of("x", OnDevice(dev))
+
+
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 5, 1 << 40, -(1 << 31) - 1, -(1 << 32) + 7])
+def test_numbers_beyond_32_bits_are_refused(value):
+    """ctypes cuts them: a window of 2^32 + 5 would be one of 5."""
+    c, i32 = host_cache("int8", "int8", False), torch.int32
+    q, table, lens = torch.zeros((2, 4, 64), dtype=torch.bfloat16), torch.zeros((2, 3), dtype=i32), torch.zeros(2, dtype=i32)
+    cu, slots, two = torch.zeros(3, dtype=i32), torch.zeros(4, dtype=torch.int64), torch.zeros(2, dtype=i32)
+    decode = dict(max_context_len=9, window=4, num_sinks=0, num_ctas=0)
+    prefill = dict(max_query_len=1, max_context_len=9, window=4, num_sinks=0)
+    size = dict(num_seqs=2, num_q_heads=4, max_query_len=1, max_context_len=9)
+    plan = dict(block_size=16, num_blocks=3)
+    for good, call in (
+            (decode, lambda **kw: kvq.kvq_decode_window(c, q, q, table, lens, sm_scale=0.1, **kw)),
+            (prefill, lambda **kw: kvq.kvq_paged_prefill(c, q, q, cu, table, lens, sm_scale=0.1, **kw)),
+            (size, lambda **kw: kvq.kvq_prefill_workspace_size(c, total_q=2, **kw)),
+            (plan, lambda **kw: kvq.kvq_plan_step(lens, lens, table, lens, two, slot_mapping=slots, positions=slots.int(),
+                                                  context_lens_out=lens, cu_new=cu, free_range_out=two, **kw))):
+        for name in good:
+            with pytest.raises(ValueError, match=f"{name} must fit 32 bits"):
+                call(**{**good, name: value})
