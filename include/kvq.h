@@ -592,15 +592,18 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
 #define KVQ_DEVERR_POSITION 512u    /* a position outside the rotation table */
 
 /*
- * kvq_debug_arm_wait_timeout -- test hook for the decode kernel's bounded
- * pipeline waits (every mbarrier wait gives up after a number of polls, sets
- * KVQ_DEVERR_TIMEOUT and makes its CTA stop loading, publish nothing and
- * return once no copy it issued is in flight).  It applies to the next decode
- * launch of the process (kvq_paged_decode*, kvq_decode_append) and then
- * disarms itself: that launch polls each wait at most `polls` times (>= 1),
+ * kvq_debug_arm_wait_timeout -- test hook for the bounded pipeline waits of the
+ * decode and of the chunk attention (every mbarrier wait gives up after a number
+ * of polls, sets KVQ_DEVERR_TIMEOUT and makes its CTA stop loading, publish nothing
+ * and return once no copy or matrix product it issued is in flight).  It applies to
+ * the next launch of the process of either kind (kvq_paged_decode*,
+ * kvq_decode_append, kvq_decode_mixed, kvq_decode_window; kvq_paged_prefill) and
+ * then disarms itself: that launch polls each wait at most `polls` times (>= 1),
  * and CTA `cta` of the first kv-head group never issues the loads of the
- * `tile`-th tile of its range (-1: every load is issued), so that the waits
- * for that tile run out with nothing in flight.  The launch's output is then
+ * `tile`-th tile of its range (chunk attention: CTA `cta` of the first part of the
+ * keys waits for what nothing signals in place of the K of its `tile`-th tile of 128
+ * keys; -1: no tile), so that the waits for that tile run out with nothing in
+ * flight.  The launch's output is then
  * invalid.  For tests of the failure path only; a caller never needs it.
  */
 kvq_status kvq_debug_arm_wait_timeout(int32_t polls, int32_t cta, int32_t tile);

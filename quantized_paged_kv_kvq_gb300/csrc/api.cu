@@ -143,14 +143,28 @@ size_t workspace_bytes_for(int num_seqs, int hq, int hkv, int d, int nc) {
 }
 
 // Test hook of the bounded pipeline waits (kvq_debug_arm_wait_timeout): armed
-// for the next decode launch of the process only.
+// for the next decode or chunk-attention launch of the process only.
 std::atomic<int> g_wait_hook_armed{0};
 std::atomic<int> g_wait_hook_polls{0};
 std::atomic<int> g_wait_hook_cta{-1};
 std::atomic<int> g_wait_hook_tile{-1};
 
-// Polls of an mbarrier before a decode CTA gives up (the kernel's default).
+// Polls of an mbarrier before a decode CTA gives up (the kernel's default), and before
+// one of the chunk attention does (some seconds).
 constexpr int kDefaultSpinLimit = 1 << 22;
+constexpr int kPrefillSpinLimit = 1 << 18;
+// What a launch gets of the hook, and its default.
+template <class Args>
+void bound_waits(Args* a, int spin_limit) {
+  a->spin_limit = spin_limit;
+  a->withhold_cta = -1;
+  a->withhold_tile = -1;
+  if (g_wait_hook_armed.exchange(0) != 0) {
+    a->spin_limit = g_wait_hook_polls.load();
+    a->withhold_cta = g_wait_hook_cta.load();
+    a->withhold_tile = g_wait_hook_tile.load();
+  }
+}
 
 // Nonzero 64-bit tag, different for every decode call of the process, so that
 // the completion tags never need clearing between calls.
@@ -514,14 +528,7 @@ kvq_status decode_call(const kvq_cache_desc* classes, int32_t num_classes,
   volatile float one = 1.0f;  // 1/scale, one IEEE float32 division, as kvq_write_cache
   a.k_inv = scaled(cache->k_fmt) ? one / cache->k_scale : 1.0f;
   a.v_inv = scaled(cache->v_fmt) ? one / cache->v_scale : 1.0f;
-  a.spin_limit = kDefaultSpinLimit;
-  a.withhold_cta = -1;
-  a.withhold_tile = -1;
-  if (g_wait_hook_armed.exchange(0) != 0) {
-    a.spin_limit = g_wait_hook_polls.load();
-    a.withhold_cta = g_wait_hook_cta.load();
-    a.withhold_tile = g_wait_hook_tile.load();
-  }
+  bound_waits(&a, kDefaultSpinLimit);
   // A launch recorded into a CUDA graph is replayed with the same call tag, so
   // a replay would find the tags and claims its predecessor left: while the
   // stream is capturing, the call first clears them (a memset node that runs
@@ -917,6 +924,7 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
   a.staged_bad = ws + static_cast<size_t>(2) * num_seqs * cache->num_kv_heads * sh.staged_len * cache->head_dim * 2;
   a.ws_out = reinterpret_cast<float*>(ws + sh.staged);
   a.ws_ml = a.ws_out + sh.partial_rows * cache->head_dim;
+  bound_waits(&a, kPrefillSpinLimit);
   const cudaError_t e = launch_prefill(a, cache->head_dim, stream);
   if (e == cudaErrorNotSupported) return KVQ_ERR_UNSUPPORTED;
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

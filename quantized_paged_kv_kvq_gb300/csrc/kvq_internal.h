@@ -219,6 +219,11 @@ struct PrefillArgs {
   uint16_t* staged;
   uint8_t* staged_bad;
   int staged_len;  // a multiple of 128
+  // Bounded waits, as in DecodeArgs: polls of an mbarrier, and the test hook: CTA
+  // (withhold_cta, 0) waits for what nothing signals in place of K tile withhold_tile.
+  int spin_limit;
+  int withhold_cta;
+  int withhold_tile;
 };
 cudaError_t launch_prefill(const PrefillArgs& a, int head_dim, cudaStream_t st);
 

@@ -60,7 +60,7 @@ namespace {
 
 constexpr int kKeys = 128;            // keys per tile
 constexpr int kProducers = 128;       // threads that load and dequantize K; as many for V
-constexpr int kSpin = 1 << 18;        // polls of an mbarrier before giving up (some seconds)
+constexpr int kDrain = 1 << 18;       // polls for what is in flight at a CTA's end (some seconds)
 constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is not raised: p <= 2^8
 
 template <int D_, int ROWS_, bool STAGED = false>  // head_dim, rows, keys dequantized ahead
@@ -833,6 +833,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
   uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + C::CTRL);
   volatile int* abort = &ctrl->abort;
+  const int spin = a.spin_limit;  // polls of an mbarrier before giving up
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7;
   constexpr int kIssuer = C::THREADS / 32 - 4;  // the warp that issues the products
   const int h = blockIdx.x % a.num_kv_heads;
@@ -931,7 +932,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
         // each way for either: its warps may be a tile apart.
         const int buf = NW == 2 ? wg : i & 1;
         const uint32_t s_addr = NW == 2 ? s_first : s_first + buf * 128;
-        if (!__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->s_full[buf]), (NW == 2 ? i : i >> 1) & 1, kSpin, abort))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->s_full[buf]), (NW == 2 ? i : i >> 1) & 1, spin, abort))) {
           give_up();
           break;
         }
@@ -953,7 +954,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
           if (i > 0) {
             // The products so far are done: with two warpgroups S of this tile was issued
             // behind them; else they are waited for.
-            if (NW == 1 && !__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->pv_done), (i - 1) & 1, kSpin, abort))) {
+            if (NW == 1 && !__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->pv_done), (i - 1) & 1, spin, abort))) {
               give_up();
               break;
             }
@@ -971,14 +972,16 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(&ctrl->p_full[buf]));
       }
     }
-    // ---- the row's result
-    bool done = true;
-    if (active && !*abort) {
-      done = __all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->o_full[wg]), 0, kSpin, abort));
+    // ---- the row's result.  The lanes of a warp decide together whether to go on: the
+    // flag may be set between two lanes' looks at it.
+    auto aborted = [&]() { return __any_sync(0xffffffffu, *abort != 0); };
+    bool done = !aborted();
+    if (active && done) {
+      done = __all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->o_full[wg]), 0, spin, abort));
       if (!done) give_up();
     }
     const bool partial = a.num_splits > 1;
-    if (has_rows && done && !*abort) {
+    if (has_rows && done) {
       tc_fence_after();
       const float vs = a.v_head_scale != nullptr ? a.v_head_scale[h] : a.v_scale;
       const float mul = partial || l != l ? 1.f : l > 0.f ? vs / l : 0.f;
@@ -1077,7 +1080,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
       const int slot0 = is_v ? C::AHEAD_K : 0;
       auto wait_empty = [&](int i) {  // the operand stage of tile i: its last reader is done
         if (i < 2) return true;
-        const bool ok = mbar_wait_or_abort(bar(empty + (i & 1)), ((i >> 1) + 1) & 1, kSpin, abort);
+        const bool ok = mbar_wait_or_abort(bar(empty + (i & 1)), ((i >> 1) + 1) & 1, spin, abort);
         if (__all_sync(0xffffffffu, ok)) return true;
         give_up();
         return false;
@@ -1134,7 +1137,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
         for (; ok && issued < 2 * nk; ++issued) {
           const int i = issued >> 1, st = i & 1;
           const bool is_v = issued & 1;
-          if (i >= 2) ok = mbar_wait_or_abort(bar(is_v ? &ctrl->v_empty[st] : &ctrl->k_empty[st]), ((i >> 1) + 1) & 1, kSpin, abort);
+          if (i >= 2) ok = mbar_wait_or_abort(bar(is_v ? &ctrl->v_empty[st] : &ctrl->k_empty[st]), ((i >> 1) + 1) & 1, spin, abort);
           if (!ok) break;
           const uint32_t full = bar(is_v ? &ctrl->v_full[st] : &ctrl->k_full[st]);
           const uint32_t dst = base + (is_v ? C::V : C::K) + st * C::TILE;
@@ -1148,11 +1151,10 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
                 "l"(reinterpret_cast<uint64_t>(&map_staged)), "r"(64 * g), "r"(y), "r"(full)
                 : "memory");
         }
-        if (!ok) {
-          give_up();
-          for (int t = max(issued - 4, 0); t < issued; ++t)  // leave with no copy in flight
-            mbar_wait(bar((t & 1) ? &ctrl->v_full[t >> 1 & 1] : &ctrl->k_full[t >> 1 & 1]), (t >> 2) & 1, kSpin);
-        }
+        if (!ok) give_up();
+        // Leave with no copy in flight, whoever gave up: the last of each stage is there.
+        for (int t = max(issued - 4, 0); t < issued; ++t)
+          mbar_wait(bar((t & 1) ? &ctrl->v_full[t >> 1 & 1] : &ctrl->k_full[t >> 1 & 1]), (t >> 2) & 1, kDrain);
       }
       __syncwarp();
     }
@@ -1165,9 +1167,14 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
       const uint64_t q_op = smem_desc(base + C::Q, 16), k_op = smem_desc(base + C::K, 16);
       const uint64_t v_op = smem_desc(base + C::V, C::GROUP_BYTES);
       auto wait = [&](const void* b, uint32_t parity) {
-        if (__all_sync(0xffffffffu, mbar_wait_or_abort(bar(b), parity, kSpin, abort))) return true;
+        if (__all_sync(0xffffffffu, mbar_wait_or_abort(bar(b), parity, spin, abort))) return true;
         give_up();
         return false;
+      };
+      // test hook: in place of this K tile (-1: none) the products wait for what nothing signals
+      const int withheld = static_cast<int>(blockIdx.x) == a.withhold_cta && blockIdx.y == 0 ? a.withhold_tile : -1;
+      auto k_there = [&](int i) {
+        return i == withheld ? wait(&ctrl->drained, 0) : wait(&ctrl->k_full[i & 1], (i >> 1) & 1);
       };
       auto scores = [&](int w, int buf, int stage) {  // S = Q_w K^T
         const uint64_t qa = q_op + w * (C::TILE >> 4), ka = k_op + stage * (C::TILE >> 4);
@@ -1188,18 +1195,18 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
       };
       // Products run in the order of their issue, so scores that overwrite
       // probabilities only need to be issued behind the products that read them.
-      bool ok = wait(&ctrl->q_full, 0) && wait(&ctrl->k_full[0], 0);
+      bool ok = wait(&ctrl->q_full, 0) && k_there(0);
       if (ok) {
         tc_fence_after();
         for (int w = 0; w < halves; ++w) scores(w, w, 0);
         tc_commit(leader, bar(&ctrl->k_empty[0]));
-        if (NW == 2) ok = wait(&ctrl->v_full[0], 0) && (tiles == 1 || wait(&ctrl->k_full[1], 0));
+        if (NW == 2) ok = wait(&ctrl->v_full[0], 0) && (tiles == 1 || k_there(1));
       }
       for (int i = 0; ok && i < tiles; ++i) {
         const int st = i & 1, ns = (i + 1) & 1;
         if (NW == 1) {  // the next tile's scores, into the other buffer, ahead of this one's probabilities
           if (i + 1 < tiles) {
-            ok = wait(&ctrl->k_full[ns], ((i + 1) >> 1) & 1);
+            ok = k_there(i + 1);
             if (!ok) break;
             tc_fence_after();
             scores(0, ns, ns);
@@ -1232,12 +1239,11 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
           }
         }
         if (ok && i + 1 < tiles) ok = wait(&ctrl->v_full[ns], ((i + 1) >> 1) & 1);
-        if (ok && i + 2 < tiles) ok = wait(&ctrl->k_full[st], ((i + 2) >> 1) & 1);
+        if (ok && i + 2 < tiles) ok = k_there(i + 2);
       }
-      if (!ok) {  // leave with nothing in flight
-        tc_commit(leader, bar(&ctrl->drained));
-        mbar_wait(bar(&ctrl->drained), 0, kSpin);
-      }
+      // Leave with no product in flight, whoever gave up.
+      tc_commit(leader, bar(&ctrl->drained));
+      mbar_wait(bar(&ctrl->drained), 0, kDrain);
       __syncwarp();
     }
   }

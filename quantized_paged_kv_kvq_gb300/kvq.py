@@ -675,9 +675,10 @@ def kvq_calibrate_head_scales(x: torch.Tensor, qmax: float, out: torch.Tensor, s
 
 
 def kvq_debug_arm_wait_timeout(polls: int, cta: int, tile: int) -> None:
-    """Test hook: the next decode launch polls each pipeline wait at most `polls`
-    times, and CTA `cta` (first kv-head group) never loads its range's tile
-    `tile`, so that a wait runs out (KVQ_DEVERR_TIMEOUT); one launch only."""
+    """Test hook: the next decode or chunk-attention launch polls each pipeline wait at
+    most `polls` times, and CTA `cta` (first kv-head group; first part of the keys) never
+    gets its range's tile `tile`, so that a wait runs out (KVQ_DEVERR_TIMEOUT); one
+    launch only."""
     _check(load_library().kvq_debug_arm_wait_timeout(polls, cta, tile),
            "kvq_debug_arm_wait_timeout")
 
