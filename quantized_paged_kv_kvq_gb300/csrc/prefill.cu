@@ -953,8 +953,12 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
           l *= f;
           if (i > 0) {
             // The products so far are done: with two warpgroups S of this tile was issued
-            // behind them; else they are waited for.
-            if (NW == 1 && !__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->pv_done), (i - 1) & 1, spin, abort))) {
+            // behind them; else the next tile's was, whose barrier this warp follows phase by
+            // phase (a wait sees no more than a phase's parity), and behind the last but
+            // one tile's a commit of their own.
+            const bool last = i + 1 == nk;
+            if (NW == 1 && !__all_sync(0xffffffffu, mbar_wait_or_abort(bar(last ? &ctrl->pv_done : &ctrl->s_full[(i + 1) & 1]),
+                                                                       last ? 0 : ((i + 1) >> 1) & 1, spin, abort))) {
               give_up();
               break;
             }
@@ -1217,7 +1221,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
           tc_fence_after();
           values(0, st, st, i > 0, 0, kKeys / 16);
           tc_commit(leader, bar(&ctrl->v_empty[st]));
-          tc_commit(leader, bar(i + 1 < tiles ? &ctrl->pv_done : &ctrl->o_full[0]));
+          if (i + 2 >= tiles) tc_commit(leader, bar(i + 1 < tiles ? &ctrl->pv_done : &ctrl->o_full[0]));
           continue;
         }
         // this tile's V and the next one's K were waited for at the end of the last turn

@@ -455,3 +455,37 @@ def test_large_finite_values(way):
     out = prefill(p, q, cu)
     err = np.abs(out.double().cpu().numpy() - ref)
     assert (err <= tol).all() and kvq.kvq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("seqs", [1, 40])  # keys cut into parts, and a CTA for all of them
+@pytest.mark.parametrize("rows", [1, 2, 16, 30])
+@pytest.mark.parametrize("n", [129, 256, 700, 1281])
+def test_a_new_maximum_in_every_tile_of_few_rows(n, rows, seqs):
+    """The accumulators are scaled in every tile, the second and the last among them, when
+    the products before are done."""
+    p = Paged("bf16", [n] * seqs, 2, 64, 16)
+    g = torch.Generator(DEV).manual_seed(n)
+    k = torch.ones((n, 2, 64), device=DEV) * torch.linspace(-8, 8, n, device=DEV)[:, None, None]
+    v = torch.randn((n, 2, 64), device=DEV, generator=g).to(torch.bfloat16)
+    q = torch.ones((rows * seqs, 8, 64), dtype=torch.bfloat16, device=DEV)
+    cu = np.arange(seqs + 1) * rows
+    for keys, sm in ((k, 1.0), (k.flip(0), -1.0), (k, 0.125)):
+        for s in range(seqs):
+            slots = ints([p.table[s, t // 16] * 16 + t % 16 for t in range(n)], torch.int64)
+            kvq.kvq_write_cache(p.cache, keys.to(torch.bfloat16).contiguous(), v, slots)
+        out = prefill(p, q, cu, sm=sm)
+        each = bits(out).view(seqs, rows, 8, 64)
+        assert (each == each[:1]).all()  # the sequences are alike
+        ref, tol = expected_of_the_first(p, q[:rows], sm)
+        check_close(out[:rows], ref, tol)
+    assert kvq.kvq_get_device_error() == 0
+
+
+def expected_of_the_first(p, q, sm):
+    """The oracle's result for p's first sequence."""
+    lens, table = p.lens, p.table
+    p.lens, p.table = lens[:1], table[:1]
+    try:
+        return p.expect(q, [0, q.shape[0]], sm)
+    finally:
+        p.lens, p.table = lens, table
