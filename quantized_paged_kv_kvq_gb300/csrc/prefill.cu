@@ -62,6 +62,11 @@ constexpr int kKeys = 128;            // keys per tile
 constexpr int kProducers = 128;       // threads that load and dequantize K; as many for V
 constexpr int kDrain = 1 << 18;       // polls for what is in flight at a CTA's end (some seconds)
 constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is not raised: p <= 2^8
+// Probabilities are made 2^7 times as large, sums and accumulators with them, so that
+// as 16-bit operands they end at 2^15 and reach down to 2^-32 of the maximum's: fp16
+// alone would drop what is below 2^-25, and 131,072 such keys weigh 0.4 % of one that
+// dominates (often a first token whose own value is next to nothing).
+constexpr float kLift = 7.0f;
 
 template <int D_, int ROWS_, bool STAGED = false>  // head_dim, rows, keys dequantized ahead
 struct Cfg {
@@ -604,8 +609,9 @@ __device__ __forceinline__ float largest_score(uint32_t s_addr) {
   }
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
-// p = 2^(s * scale + off) over the scores, as 16-bit pairs in their first half;
-// returns the sum (before that rounding).  The first 64 are handed over (half_bar,
+// p = 2^(s * scale + off) over the scores, as 16-bit pairs in their first half (what
+// the product takes); returns the sum, in float32 and before that rounding, whose errors
+// (2^-11 of each p, or 2^-8 in bf16) do not add up in one direction.  The first 64 are handed over (half_bar,
 // if not 0) when they are there, so that their products run while the others are made.
 template <bool BF>
 __device__ __forceinline__ float probabilities(uint32_t s_addr, float scale, float off, uint32_t half_bar, int lane) {
@@ -966,7 +972,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
             scale_columns(o_addr, D, f);
           }
         }
-        const float off = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every p is 0
+        const float off = m == -INFINITY ? 0.f : kLift - m;  // a row that has seen nothing: every p is 0
         const uint32_t half_bar = NW == 2 ? bar(&ctrl->p_half[wg]) : 0u;
         l += bf ? probabilities<true>(s_addr, scale, off, half_bar, lane)
                 : probabilities<false>(s_addr, scale, off, half_bar, lane);

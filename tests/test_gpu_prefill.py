@@ -489,3 +489,30 @@ def expected_of_the_first(p, q, sm):
         return p.expect(q, [0, q.shape[0]], sm)
     finally:
         p.lens, p.table = lens, table
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e5m2", "uint8", "bf16"])
+@pytest.mark.parametrize("rows,g,seqs", [(2, 1, 1), (40, 2, 1), (300, 1, 1), (600, 4, 1),  # keys cut into parts
+                                         (2, 1, 100), (40, 2, 100), (100, 2, 100), (600, 4, 10)])  # not; 64 to 256 rows
+def test_many_light_keys_beside_a_heavy_one(fmt, rows, g, seqs):
+    """One key that dominates, its value zero, and 131,071 of 2^-25.4 its weight: what
+    they weigh together is the output."""
+    n, d, weight = 131072, 64, 2.0 ** -25.4
+    k, v = torch.zeros((n, 1, d), device=DEV), torch.full((n, 1, d), 100.0, device=DEV)
+    k[0], v[0] = 1.0, 0.0
+    p = Paged(fmt, [n], 1, d, 128)
+    if fmt == "int8":
+        p.cache.k_scale, p.cache.v_scale = 1.0, 1.0
+    slots = ints(p.table[0, np.arange(n) // 128] * 128 + np.arange(n) % 128, torch.int64)
+    kvq.kvq_write_cache(p.cache, k.to(torch.bfloat16), v.to(torch.bfloat16), slots)
+    p.lens = p.lens.repeat(seqs)  # sequences of the same pages
+    p.block_table, p.context_lens = p.block_table.repeat(seqs, 1), p.context_lens.repeat(seqs)
+    q = torch.ones((rows * seqs, g, d), dtype=torch.bfloat16, device=DEV)
+    out = prefill(p, q, np.arange(seqs + 1) * rows, sm=float(-np.log(weight) / d)).double().cpu().numpy()
+    light = np.tile(np.arange(n - rows, n), seqs)[:, None, None] * weight
+    value = 96.0 if fmt == "e5m2" else 100.0  # as the format holds it
+    ref = np.broadcast_to(light / (1 + light) * value, out.shape)
+    # a probability of 2^(7 - 25.4) in fp16 is off by 2^-25, 2^-6.6 of it, the same in every
+    # key (bf16: 2^-8); a logit of 17.6 by 2^-22; the output by 2^-8
+    assert np.abs(out / ref - 1).max() <= (2.0 ** -8 if fmt == "bf16" else 2.0 ** -6.6) + 2.0 ** -8 + 1e-4
+    assert kvq.kvq_get_device_error() == 0
