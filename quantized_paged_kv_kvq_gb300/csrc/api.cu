@@ -244,9 +244,10 @@ struct PrefillShape {
 };
 // Dequantizing ahead pays where each key is read by this many row tiles (of 256) on
 // average, fewer where dequantizing costs more, and is done in at most 16 GiB.
-// Measured ahead / not, 32 / 8 heads of 128: int8, 8 x 4,096 keys: 4 row tiles 165 /
-// 148 us, 8 280 / 290, 1 x 8,192 keys and 32 tiles 245 / 275; KVarN, 16 x 4,096 keys:
-// 2 tiles 224 / 227, 8 x 4,096: 4 tiles 187 / 222, 8 311 / 427; bf16 as int8.
+// Measured ahead / not, 32 / 8 heads of 128: int8, 8 x 4,096 keys: 4 row tiles 160 /
+// 138 us, 8 257 / 257, 1 x 8,192 keys and 32 tiles 193 / 217; KVarN, 16 x 4,096 keys:
+// 2 tiles 223 / 222, 8 x 4,096: 4 tiles 182 / 210, 8 289 / 389; int4 4 tiles 165 / 177;
+// bf16 as int8.
 constexpr int64_t stage_tiles(int fmt) { return is_asym(fmt) ? 3 : 8; }
 constexpr int64_t kStageBytes = 16ll << 30;
 // What can be said of a batch's sizes without a device.

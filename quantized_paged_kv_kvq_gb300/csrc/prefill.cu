@@ -27,13 +27,13 @@
 // more than the products hide (the schedulers issue 0.6 instructions a cycle, a third
 // of them for it).  Then stage_kernel writes the operands to memory once, by whole
 // tiles, and one thread per CTA loads them by TMA: 2 x 4,096 tokens on 10,000 keys of
-// int8, 32 / 8 heads of 128, 1.18 TFLOP: 0.79 ms, 1,490 TFLOP/s, 78 % of the measured
+// int8, 32 / 8 heads of 128, 1.18 TFLOP: 0.79 to 0.80 ms, 1,490 TFLOP/s, 78 % of the measured
 // matrix rate, against 1.01 ms (30 us of it the staging; the tensor pipe is 69 % busy).
 // What is left is the chain of a row's tile: scores, softmax (1,500 cycles), products.
 //
 // Few rows over long contexts: the keys are cut into num_splits parts, whose
 // (m, sum, accumulators) a second kernel joins.  32 x 1..8 tokens on 256..4,096 keys:
-// 57 us, 2.4 TB/s.  A tile takes 2,650 cycles, the softmax of the one warp with rows
+// 57 us, 2.4 TB/s (int8; bf16 73, int4 78, uint8 84, KVarN 96: rows made in float32).  A tile takes 2,650 cycles, the softmax of the one warp with rows
 // 2,050 of them and the producers as much (a third converting, half issuing copies);
 // a CTA's start and end 14,000 (7 us).
 //
@@ -43,7 +43,9 @@
 // fully unrolled softmax and conversions (2.1 ms: instruction fetch).  With few rows:
 // up to 32 rows in four copies, each warp a quarter of a tile's keys (63 us for 57: the
 // producers bound it, and the copies have to be joined); keys cut into parts for two or
-// four waves of CTAs (91 for 68, with 128 rows a tile).
+// four waves of CTAs (with 128 rows a tile: 91 us for 68 with 32 sequences, 47 and 51 for
+// 32 with 2, 45 and 59 for 43 with 8; 52 and 65 for 61 with 12, whose 96 CTAs leave a
+// third of the SMs idle).
 #include <atomic>
 
 #include "kvq_device.cuh"
@@ -130,9 +132,10 @@ __device__ __forceinline__ int2 seq_rows(const PrefillArgs& a, int s, bool& bad)
 // The sequence and row tile that tile number `want` (of all sequences, ROWS
 // rows each) is, found by the whole block.  Up to kOrdered sequences count by rising
 // length (the launch starts from the last tile, so the longest come first; scan: two
-// words a sequence), more in their order (a scan; a word a warp): 32 x 1..8 tokens on
-// 256..4,096 keys, 256 CTAs on 152 SMs:
-// 93 us in their order, 68 so (of 128 rows each).
+// words a sequence, which is what the metadata slots hold), more in their order (a scan;
+// a word a warp): 32 x 1..8 tokens on 256..4,096 keys, 256 CTAs on 152 SMs: 93 us in
+// their order, 68 so (of 128 rows each).  Of many sequences the order matters less: 128
+// such take 206 us, 129 in their order 227.
 constexpr int kOrdered = 128;
 static_assert(kOrdered * 8 <= 2 * 3 * kKeys * 2, "fits the metadata slots, which are not in use yet");
 template <int ROWS>
