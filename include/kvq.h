@@ -188,7 +188,10 @@ kvq_status kvq_decode_workspace_size(const kvq_cache_desc* cache, int32_t num_se
  *   enter the tensor cores as exact fp16 code values; the query is rounded to
  *   fp16, which is exact for bf16 values of magnitude 2^-14 .. 65504: smaller
  *   ones lose bits, larger ones overflow and set KVQ_DEVERR_QUERY_RANGE; the
- *   16-bit cache keeps the bf16 query).
+ *   16-bit cache keeps the bf16 query).  Probabilities enter them in 16 bits too, below
+ *   2^-25 of the largest as 0 (symmetric formats: 4,096 such keys weigh 1.2e-4); of
+ *   asymmetric formats times the row's scale, by a power of two that keeps the product
+ *   in range whatever the scale is.
  */
 kvq_status kvq_paged_decode(const kvq_cache_desc* cache, const void* k_cache,
                             const void* v_cache, void* out, const void* query,

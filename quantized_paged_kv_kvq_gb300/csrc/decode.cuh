@@ -26,7 +26,8 @@
 //    permuted to match) and tokens are assigned to mma rows so that, with the
 //    swizzle, every 16-byte load of a quarter-warp hits distinct banks.
 //  * online softmax in the log2 domain; the running maximum is raised (with
-//    a reduction) only when a logit exceeds it by more than 8, so P <= 2^8;
+//    a reduction) only when a logit exceeds it by more than 8, so P <= 2^8 (with
+//    asymmetric V when P times a row's scale, which is the operand, passes 2^15);
 //    scales, zero points and sigma are folded in after the k-sum (K) or into
 //    the probabilities (V).
 //  * a sequence split between ranges is merged (log-sum-exp) by the last CTA
@@ -1381,14 +1382,10 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
     // ---- online softmax (log2 domain), lazy rescale: the running maximum m is
     // only raised (with a reduction over the tile) when some logit exceeds it
     // by more than 8, so probabilities stay <= 2^8 and most tiles skip it
-    float mx0 = fmaxf(sl[0], sl[2]), mx1 = fmaxf(sl[1], sl[3]);
-    if (__any_sync(0xffffffffu, (mx0 > m0 + 8.0f) || (mx1 > m1 + 8.0f))) {
-#pragma unroll
-      for (int o = 4; o <= 16; o <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-      }
-      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+    float pr[4];
+    auto raise = [&](float n0, float n1) {  // to the maxima n, or where they are already
+      n0 = fmaxf(m0, n0);
+      n1 = fmaxf(m1, n1);
       const float al0 = fast_exp2(m0 - n0), al1 = fast_exp2(m1 - n1);
       m0 = n0;
       m1 = n1;
@@ -1398,21 +1395,58 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
         Oa[2 * d] *= al0; Oa[2 * d + 1] *= al0;
         Ob[2 * d] *= al1; Ob[2 * d + 1] *= al1;
       }
-    }
-    float pr[4];
-    pr[0] = fast_exp2(sl[0] - m0);
-    pr[1] = fast_exp2(sl[1] - m1);
-    pr[2] = fast_exp2(sl[2] - m0);
-    pr[3] = fast_exp2(sl[3] - m1);
-    l0 += pr[0] + pr[2];
-    l1 += pr[1] + pr[3];
+    };
+    auto probabilities = [&]() {
+      pr[0] = fast_exp2(sl[0] - m0);
+      pr[1] = fast_exp2(sl[1] - m1);
+      pr[2] = fast_exp2(sl[2] - m0);
+      pr[3] = fast_exp2(sl[3] - m1);
+    };
+    float mx0, mx1;
+    auto tile_max = [](float x) {
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      return x;
+    };
     if constexpr (is_asym(VF)) {
+      // The operand is p times the row's scale, in fp16, whatever the scale's size: m is
+      // the maximum less the lift that brings the largest operand of the tile that
+      // raises it to 2^10..2^11, and it is raised when one passes 2^15.  (With p <= 2^8
+      // alone, scales of 0.02 lost every p below 2^-19, and the zero points' sum, which
+      // is float32, did not: 32,768 keys of 2^-20 beside one that dominates moved a
+      // UINT8 output by 0.07 and a KVarN one by 0.64; and scales above 256 overflowed.)
       if (!ok0) vs0 = vz0 = 0.f;
       if (!ok1) vs1 = vz1 = 0.f;
+      float px[4];
+      auto products = [&]() {
+        probabilities();
+        px[0] = pr[0] * vs0; px[1] = pr[1] * vs0;
+        px[2] = pr[2] * vs1; px[3] = pr[3] * vs1;
+      };
+      products();
+      const float most = fmaxf(fmaxf(fabsf(px[0]), fabsf(px[1])), fmaxf(fabsf(px[2]), fabsf(px[3])));
+      if (__any_sync(0xffffffffu, !(most <= 32768.0f))) {  // the first tile's too: m is -inf
+        mx0 = tile_max(fmaxf(sl[0], sl[2]));
+        mx1 = tile_max(fmaxf(sl[1], sl[3]));
+        // 2^lift times the largest scale is in [2^10, 2^11)
+        const float vm = fminf(fmaxf(tile_max(fmaxf(fabsf(vs0), fabsf(vs1))), 0x1p-30f), 0x1p33f);
+        const float lift = static_cast<float>(137 - (__float_as_int(vm) >> 23));
+        raise(mx0 - lift, mx1 - lift);
+        products();
+      }
+      l0 += pr[0] + pr[2];
+      l1 += pr[1] + pr[3];
       z0 += pr[0] * vz0 + pr[2] * vz1;
       z1 += pr[1] * vz0 + pr[3] * vz1;
-      pr[0] *= vs0; pr[1] *= vs0;
-      pr[2] *= vs1; pr[3] *= vs1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) pr[u] = px[u];
+    } else {
+      mx0 = fmaxf(sl[0], sl[2]);
+      mx1 = fmaxf(sl[1], sl[3]);
+      if (__any_sync(0xffffffffu, (mx0 > m0 + 8.0f) || (mx1 > m1 + 8.0f))) raise(tile_max(mx0), tile_max(mx1));
+      probabilities();
+      l0 += pr[0] + pr[2];
+      l1 += pr[1] + pr[3];
     }
     // ---- P^T operand: lane (g, c) needs head g at its 4 V tokens
     const uint32_t x0 = pack_op2<VF == BF16>(pr[0], pr[2]);  // head 2c, rows (g, g+8)
