@@ -19,6 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvq.so")
 
 FMT = {"int8": 1, "fp8_e4m3": 2, "fp8_e5m2": 3, "int4_asym": 4, "uint8_asym": 5, "bf16": 6}
+ASYM = ("int4_asym", "uint8_asym")
 FLAG_VARNORM_ROTATE = 1
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARGUMENT", 2: "KVQ_ERR_UNSUPPORTED",
           3: "KVQ_ERR_WORKSPACE", 4: "KVQ_ERR_CUDA"}
@@ -187,7 +188,7 @@ def row_bytes(fmt: str, head_dim: int) -> int:
 
 
 def meta_fields(fmt: str, varnorm_rotate: bool) -> int:
-    if fmt in ("int4_asym", "uint8_asym"):
+    if fmt in ASYM:
         return 3 if varnorm_rotate else 2
     return 0
 
@@ -406,25 +407,30 @@ def _rows(dev: int, name: str, t: torch.Tensor, shape) -> int:
     return s0 if n > 1 else (heads * d + 7) // 8 * 8
 
 
+def _pool(dev: int, name: str, t: torch.Tensor, dtype, blocks: int, a: int, b: int, c: int) -> None:
+    """Checks a cache's contiguous tensor [blocks or more, a, b, c] of CUDA device dev."""
+    shape = t.shape
+    if (t.dtype is not dtype or len(shape) != 4 or shape[0] < blocks or shape != (shape[0], a, b, c)
+            or t.get_device() != dev or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(blocks, a, b, c)} on CUDA device {dev}, "
+                         f"got {t.dtype} {tuple(shape)} with strides {t.stride()} on {t.device}")
+
+
 def _cache_desc(dev: int, cache: KVCache) -> _CacheDesc:
     """The cache's description, once its tensors are what it says: the kernels write and
     read through them, and see nothing but addresses."""
     c, rot = cache, cache.varnorm_rotate
-    blocks, bs, hkv = c.num_blocks, c.block_size, c.num_kv_heads
-    specs = [("k_cache", c.k_cache, torch.uint8, (bs, hkv, row_bytes(c.k_fmt, c.head_dim))),
-             ("v_cache", c.v_cache, torch.uint8, (bs, hkv, row_bytes(c.v_fmt, c.head_dim)))]
-    for name, fmt, meta in (("k_meta", c.k_fmt, c.k_meta), ("v_meta", c.v_fmt, c.v_meta)):
-        fields = meta_fields(fmt, rot)
-        if fields:
-            _need(meta is not None, f"{name} is missing: {fmt} rows have {fields} fields")
-            specs.append((name, meta, torch.float16, (hkv, fields, bs)))
-    for name, t, dtype, shape in specs:
-        if (t.dtype is not dtype or t.dim() != 4 or t.shape[0] < blocks or t.shape[1:] != shape
-                or t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(blocks, *shape)} on CUDA device {dev}, "
-                             f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    blocks, bs, hkv, d = c.num_blocks, c.block_size, c.num_kv_heads, c.head_dim
+    _pool(dev, "k_cache", c.k_cache, torch.uint8, blocks, bs, hkv, row_bytes(c.k_fmt, d))
+    _pool(dev, "v_cache", c.v_cache, torch.uint8, blocks, bs, hkv, row_bytes(c.v_fmt, d))
+    if c.k_fmt in ASYM:
+        _need(c.k_meta is not None, "k_meta is missing: rows of this format have fields")
+        _pool(dev, "k_meta", c.k_meta, torch.float16, blocks, hkv, 3 if rot else 2, bs)
+    if c.v_fmt in ASYM:
+        _need(c.v_meta is not None, "v_meta is missing: rows of this format have fields")
+        _pool(dev, "v_meta", c.v_meta, torch.float16, blocks, hkv, 3 if rot else 2, bs)
     if rot and c.signs is not None:
-        _tensors(dev, ("signs", c.signs, torch.int8, (c.head_dim,)))
+        _tensors(dev, ("signs", c.signs, torch.int8, (d,)))
     if c.k_head_scales is not None:
         _tensors(dev, ("k_head_scales", c.k_head_scales, torch.float32, (hkv,)))
     if c.v_head_scales is not None:
