@@ -1417,14 +1417,17 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
       // UINT8 output by 0.07 and a KVarN one by 0.64; and scales above 256 overflowed.)
       if (!ok0) vs0 = vz0 = 0.f;
       if (!ok1) vs1 = vz1 = 0.f;
-      float px[4];
+      float px[4], sum0, sum1;
       auto products = [&]() {
         probabilities();
+        sum0 = pr[0] + pr[2];
+        sum1 = pr[1] + pr[3];
         px[0] = pr[0] * vs0; px[1] = pr[1] * vs0;
         px[2] = pr[2] * vs1; px[3] = pr[3] * vs1;
       };
       products();
-      const float most = fmaxf(fmaxf(fabsf(px[0]), fabsf(px[1])), fmaxf(fabsf(px[2]), fabsf(px[3])));
+      // (rows whose scale is 0 raise it by the probabilities alone, from 2^63 on)
+      const float most = max3f(max3f(fabsf(px[0]), fabsf(px[1]), fabsf(px[2])), fabsf(px[3]), fmaxf(sum0, sum1) * 0x1p-48f);
       if (__any_sync(0xffffffffu, !(most <= 32768.0f))) {  // the first tile's too: m is -inf
         mx0 = tile_max(fmaxf(sl[0], sl[2]));
         mx1 = tile_max(fmaxf(sl[1], sl[3]));
@@ -1434,8 +1437,8 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
         raise(mx0 - lift, mx1 - lift);
         products();
       }
-      l0 += pr[0] + pr[2];
-      l1 += pr[1] + pr[3];
+      l0 += sum0;
+      l1 += sum1;
       z0 += pr[0] * vz0 + pr[2] * vz1;
       z1 += pr[1] * vz0 + pr[3] * vz1;
 #pragma unroll

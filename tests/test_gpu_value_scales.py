@@ -74,13 +74,20 @@ def test_scales_behind_a_maximum_that_lags(fmt, scale, rise, ctas):
     check(decodes(p, q, sm, ctas), ref, tol)
 
 
+@pytest.mark.parametrize("ctas", [1, 3])
+@pytest.mark.parametrize("step", [0.0, 1.0, 30.0, 100.0, -30.0])
 @pytest.mark.parametrize("fmt", ["int4", "uint8", "kvarn"])
-def test_rows_without_a_scale(fmt):
-    """Scales of zero: the rows are their zero points."""
-    n, d = 70, 64
+def test_rows_without_a_scale(fmt, step, ctas):
+    """Scales of zero: the rows are their zero points.  Logits that move by 2^step from
+    tile to tile, by more than float32's range in all."""
+    n, d = 300, 64
     p = Paged(fmt, [n], 2, d, 16, seed=5)
-    for m in (p.cache.v_meta,):
-        m[:, :, 0] = 0.0
-    q = torch.randn((1, 8, d), device=DEV, generator=torch.Generator(DEV).manual_seed(2)).to(torch.bfloat16)
-    ref, tol = p.expect(q, [0, 1], 0.125)
-    check(decodes(p, q, 0.125, 0), ref, tol)
+    k = (torch.arange(n, device=DEV) // 16 / 20.0)[:, None, None].expand(n, 2, d)  # 0 .. 0.9 by 0.05 a tile
+    store(p, k, torch.randn((n, 2, d), device=DEV, generator=torch.Generator(DEV).manual_seed(1)))
+    p.cache.v_meta[:, :, 0] = 0.0
+    q = torch.ones((1, 8, d), dtype=torch.bfloat16, device=DEV)
+    sm = float(step * np.log(2) / (0.05 * d))
+    # the oracle's bound holds for sm >= 0 (its logits' part is sm * 2u * |q| |k|): a
+    # negative one is the other sign of the queries, the same logits exactly
+    ref, tol = p.expect(q if sm >= 0 else -q, [0, 1], abs(sm))
+    check(decodes(p, q, sm, ctas), ref, tol)
