@@ -62,6 +62,10 @@ typedef enum {
   KVQ_FMT_BF16 = 6,       /* the bf16 value itself, no scale (PR #4893 item 1's
                              --kv-cache-dtype auto: the unquantized 16-bit cache);
                              K and V both, no per-head scales, no rotation      */
+  KVQ_FMT_INT8_BLOCK = 7, /* int8, symmetric, one fp32 scale per page and kv-head, made
+                             as the page is written (no calibration)            */
+  KVQ_FMT_E4M3_BLOCK = 8, /* OCP E4M3FN byte, one fp32 scale per page and kv-head;
+                             with a block format K and V both have one          */
 } kvq_format;
 
 /* KVarN pre-quantization (both tensors; asymmetric formats only): per
@@ -84,6 +88,11 @@ typedef enum {
  *   KVQ_FLAG_VARNORM_ROTATE.  16-byte aligned.
  *   Dequantization: x = (code * scale + zero_point) [* sigma, then the
  *   inverse rotation].
+ * Page scales (block formats): k_meta, v_meta: fp32 [num_blocks, P], P =
+ *   num_kv_heads rounded up to a multiple of 4; entry (b, h) is the scale of block b
+ *   and kv-head h, x = code_value * scale; the padding is never used.  16-byte
+ *   aligned.  Written by kvq_write_cache and kvq_decode_append, which read them too
+ *   where they continue a page; a page that is begun needs no initial value.
  * Per-tensor scales (symmetric formats): x = code_value * k_scale (v_scale).
  * Per-kv-head scales (symmetric formats, optional): k_head_scales /
  *   v_head_scales, device fp32 [num_kv_heads], 4-byte aligned, each > 0; when
@@ -132,7 +141,20 @@ typedef struct {
  *          code = clamp(rint((x - z) * (1.0f / s)), 0, L), L = 15 or 255.
  *   With KVQ_FLAG_VARNORM_ROTATE the ASYM step runs on the normalised,
  *   rotated row (see kvq_hadamard for the transform's definition).
- * Slots that are not written are left untouched.  num_tokens == 0 is a no-op.
+ *   BLOCK: pages fill from the front.  The tokens of a page are consecutive in a
+ *          call, skipped ones between them aside (31 in a row at most); with m the largest finite |x| of their rows (per kv-head), need = 0
+ *          for m = 0, else max(m / qmax, 2^-126), qmax = 127 or 448.  Where they reach
+ *          offset 0 the page is begun: scale = need.  Else it goes on behind the rows
+ *          in front of them: scale = old * 2^k with the least k >= 0 that makes
+ *          it >= need (old 0: need), and for k > 0 the codes in front become code * 2^-k,
+ *          rounded to nearest even (e4m3: exact above its subnormals).  Codes are
+ *          those of INT8 / E4M3 with inv = 1.0f / scale (0 for scale 0): an infinity
+ *          becomes the largest code, a NaN 0 or E4M3's NaN.  Rows behind them keep
+ *          their codes, under the new scale.  Tokens of one page further apart in a
+ *          call, or two that name one slot: which of them set a scale or land is
+ *          unspecified, in that page.
+ * Slots that are not written are left untouched (but for codes in front of a block
+ * format's rows, as above).  num_tokens == 0 is a no-op.
  */
 kvq_status kvq_write_cache(const kvq_cache_desc* cache, void* k_cache, void* v_cache,
                            const void* key, const void* value, int64_t key_stride,
@@ -190,8 +212,8 @@ kvq_status kvq_decode_workspace_size(const kvq_cache_desc* cache, int32_t num_se
  *   ones lose bits, larger ones overflow and set KVQ_DEVERR_QUERY_RANGE; the
  *   16-bit cache keeps the bf16 query).  Probabilities enter them in 16 bits too, below
  *   2^-25 of the largest as 0 (symmetric formats: 4,096 such keys weigh 1.2e-4); of
- *   asymmetric formats times the row's scale, by a power of two that keeps the product
- *   in range whatever the scale is.
+ *   asymmetric and block formats times the row's or page's scale, by a power of two that keeps
+ *   the product in range whatever the scale is (a page's: from 2^-100 on).
  */
 kvq_status kvq_paged_decode(const kvq_cache_desc* cache, const void* k_cache,
                             const void* v_cache, void* out, const void* query,
@@ -240,6 +262,8 @@ kvq_status kvq_paged_decode_ex(const kvq_cache_desc* cache, const void* k_cache,
  * The token at position n-1 must be written by this call alone: another call
  *   (or kernel) that writes the same slots or reads them while this one runs
  *   races with it.
+ * Block formats take two launches, the store and the attention: a row may change the
+ *   scale and the codes of its page, which other CTAs read.
  * The caches are written, so k_cache / v_cache (and the metadata in `cache`)
  *   must be writable.  Other arguments, the workspace and its size are those
  *   of kvq_paged_decode_ex (num_ctas included).
@@ -268,6 +292,7 @@ kvq_status kvq_decode_append(const kvq_cache_desc* cache, void* k_cache, void* v
  *   block_table holds block ids of that class's pool, and max_blocks_per_seq
  *   must cover max_context_len at the smallest page size.  A class id outside
  *   [0, num_classes) sets KVQ_DEVERR_CLASS_RANGE and reads class 0.
+ * Block formats: KVQ_ERR_UNSUPPORTED.
  * Writes go through kvq_write_cache with each class's description, codes and
  *   slots (slot = block * class block_size + offset).
  * new_key, new_value, key_stride, value_stride: as in kvq_decode_append (the
@@ -490,6 +515,8 @@ kvq_status kvq_norm_rope(const kvq_rope_desc* rope, void* query_out, int64_t que
  * value: device bf16 [num_tokens, num_kv_heads, head_dim], as key.
  * Other arguments as in kvq_norm_rope; a position outside the table writes
  *   nothing of the token.  rope->head_dim must be the cache's.
+ * Block formats: KVQ_ERR_UNSUPPORTED (a page's scale takes all of its rows: kvq_norm_rope,
+ *   then kvq_write_cache).
  */
 kvq_status kvq_norm_rope_write(const kvq_rope_desc* rope, const kvq_cache_desc* cache, void* k_cache,
                                void* v_cache, void* query_out, int64_t query_out_stride,
@@ -576,6 +603,60 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
                              int32_t num_sinks, void* workspace, size_t workspace_bytes,
                              kvq_stream_t stream);
 
+/*
+ * kvq_prompt_attention -- attention of whole prompts whose queries, keys and values are
+ * at hand in 16 bits: causal, heads in groups, sequences packed.  None of the source
+ * pages has a counterpart: it is a prompt's first pass, before (or beside) the cache write,
+ * on the values as they are and without a look-up of pages.
+ *
+ * query: device bf16 [total_tokens, num_q_heads, head_dim], key, value: device bf16
+ *   [total_tokens, num_kv_heads, head_dim], out as query; heads and elements
+ *   contiguous, tokens the given strides (elements) apart: each >= its heads * head_dim,
+ *   a multiple of 8, at most 2^31.  All 16-byte aligned.  (Slices of one projection.)
+ *   out may overlap none of the others.
+ *   q-head h reads kv-head h / (num_q_heads / num_kv_heads); the ratio must be an
+ *   integer <= 8.  head_dim 64 or 128.
+ * cu_seqlens: device int32 [num_seqs + 1], non-decreasing: sequence s has tokens
+ *   cu_seqlens[s] .. cu_seqlens[s+1]-1, at positions 0, 1, ...  The token at position p
+ *   sees position t of its sequence when t <= p and (window == 0 or t > p - window or
+ *   t < num_sinks).  Rows of out outside [cu_seqlens[0], cu_seqlens[num_seqs]) are left
+ *   as they were.  Offsets outside [0, total_tokens], decreasing ones, and a sequence of
+ *   more than max_len tokens (its first max_len are taken) are cut and set
+ *   KVQ_DEVERR_TOKENS.
+ * total_tokens <= 2^30.  window >= 0 (0: no limit), num_sinks >= 0.
+ * One launch, no workspace; may be captured into a CUDA graph.
+ * Arithmetic: bf16 operands in the tensor cores (probabilities rounded to bf16), float32
+ *   sums and softmax.  A value that is not finite makes the rows that see it not
+ *   finite; keys and values that a row does not see (later ones, other sequences')
+ *   do not touch it, whatever they are.
+ */
+kvq_status kvq_prompt_attention(void* out, int64_t out_stride, const void* query, int64_t query_stride,
+                                const void* key, int64_t key_stride, const void* value,
+                                int64_t value_stride, const int32_t* cu_seqlens, int32_t num_seqs,
+                                int64_t total_tokens, int32_t max_len, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim, float sm_scale, int32_t window,
+                                int32_t num_sinks, kvq_stream_t stream);
+
+/*
+ * kvq_read_cache -- rows of the cache dequantized to bf16, every format: the inverse of
+ * kvq_write_cache up to the quantization (to move a request to a cache of another format or
+ * off the GPU, or to attend to it densely).
+ *
+ * slot_mapping: device int64 [num_tokens], as in kvq_write_cache: token t's key and
+ *   value come from slot slot_mapping[t], slot < 0 leaves its output rows as they
+ *   were; a slot past the cache sets KVQ_DEVERR_SLOT_RANGE and does the same.  A slot may be
+ *   named any number of times.
+ * key_out, value_out: device bf16 [num_tokens, num_kv_heads, head_dim]; heads and
+ *   elements contiguous, tokens the given strides (elements) apart: >= num_kv_heads *
+ *   head_dim, a multiple of 8.  16-byte aligned, not overlapping.
+ * Computed in float32 (the dequantization above; KVarN's inverse rotation included),
+ *   rounded once.
+ */
+kvq_status kvq_read_cache(const kvq_cache_desc* cache, const void* k_cache, const void* v_cache,
+                          void* key_out, void* value_out, int64_t key_out_stride,
+                          int64_t value_out_stride, const int64_t* slot_mapping, int64_t num_tokens,
+                          kvq_stream_t stream);
+
 /* Device error word bits. */
 #define KVQ_DEVERR_SLOT_RANGE 1u  /* a slot id past num_blocks*block_size */
 #define KVQ_DEVERR_BLOCK_RANGE 2u /* a block-table entry outside [0, num_blocks) */
@@ -596,14 +677,14 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
 
 /*
  * kvq_debug_arm_wait_timeout -- test hook for the bounded pipeline waits of the
- * decode and of the chunk attention (every mbarrier wait gives up after a number
+ * decode, the chunk attention and the prompt attention (every mbarrier wait gives up after a number
  * of polls, sets KVQ_DEVERR_TIMEOUT and makes its CTA stop loading, publish nothing
  * and return once no copy or matrix product it issued is in flight).  It applies to
  * the next launch of the process of either kind (kvq_paged_decode*,
- * kvq_decode_append, kvq_decode_mixed, kvq_decode_window; kvq_paged_prefill) and
- * then disarms itself: that launch polls each wait at most `polls` times (>= 1),
+ * kvq_decode_append, kvq_decode_mixed, kvq_decode_window; kvq_paged_prefill;
+ * kvq_prompt_attention) and then disarms itself: that launch polls each wait at most `polls` times (>= 1),
  * and CTA `cta` of the first kv-head group never issues the loads of the
- * `tile`-th tile of its range (chunk attention: CTA `cta` of the first part of the
+ * `tile`-th tile of its range (chunk and prompt attention: CTA `cta` of the first part of the
  * keys waits for what nothing signals in place of the K of its `tile`-th tile of 128
  * keys; -1: no tile), so that the waits for that tile run out with nothing in
  * flight.  The launch's output is then

@@ -21,17 +21,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-bool valid_fmt(int f) { return f >= KVQ_FMT_INT8 && f <= KVQ_FMT_BF16; }
+bool valid_fmt(int f) { return f >= KVQ_FMT_INT8 && f <= KVQ_FMT_E4M3_BLOCK; }
 
 // Families that share a kernel: per-tensor-scaled 8-bit codes, per-row
-// asymmetric codes (optionally KVarN), and the 16-bit cache (K and V both).
+// asymmetric codes (optionally KVarN), 8-bit codes scaled per page and kv-head, and the
+// 16-bit cache (K and V both).
 bool pairing_ok(int kf, int vf, bool kvarn) {
   if ((kf == KVQ_FMT_BF16) != (vf == KVQ_FMT_BF16)) return false;
+  if (is_block(kf) != is_block(vf)) return false;
   const bool ak = is_asym(kf), av = is_asym(vf);
   if (kvarn) return ak && av;
   return ak == av;
 }
-bool scaled(int f) { return !is_asym(f) && f != KVQ_FMT_BF16; }
+bool scaled(int f) { return !is_asym(f) && !is_block(f) && f != KVQ_FMT_BF16; }
+bool has_meta(int f) { return is_asym(f) || is_block(f); }
 
 // A power of two from 8 to 128: a 16-token tile lies in one block, or in two
 // consecutive entries of the block table (8-token pages).
@@ -86,9 +89,9 @@ kvq_status check_cache(const kvq_cache_desc* c) {
     return KVQ_ERR_INVALID_ARGUMENT;
   if (scaled(c->v_fmt) && !(c->v_scale > 0.0f && isfinite(c->v_scale)))
     return KVQ_ERR_INVALID_ARGUMENT;
-  if (is_asym(c->k_fmt) && (c->k_meta == nullptr || !aligned(c->k_meta, 16)))
+  if (has_meta(c->k_fmt) && (c->k_meta == nullptr || !aligned(c->k_meta, 16)))
     return KVQ_ERR_INVALID_ARGUMENT;
-  if (is_asym(c->v_fmt) && (c->v_meta == nullptr || !aligned(c->v_meta, 16)))
+  if (has_meta(c->v_fmt) && (c->v_meta == nullptr || !aligned(c->v_meta, 16)))
     return KVQ_ERR_INVALID_ARGUMENT;
   if (kvarn && c->signs != nullptr && !aligned(c->signs, 16)) return KVQ_ERR_INVALID_ARGUMENT;
   // per-kv-head scales: scaled symmetric formats only
@@ -259,6 +262,7 @@ kvq_status check_prefill(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
     return KVQ_ERR_INVALID_ARGUMENT;
   if (num_q_heads % c->num_kv_heads) return KVQ_ERR_INVALID_ARGUMENT;
   if (num_q_heads / c->num_kv_heads > 8) return KVQ_ERR_UNSUPPORTED;
+  if (is_block(c->k_fmt)) return KVQ_ERR_UNSUPPORTED;
   if (total_q > INT32_MAX || max_context_len > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->block_size) * c->num_kv_heads * c->head_dim * 2 > INT32_MAX)
     return KVQ_ERR_UNSUPPORTED;  // a block's bytes fit 31 bits
@@ -359,6 +363,9 @@ kvq_status kvq_write_cache(const kvq_cache_desc* cache, void* k_cache, void* v_c
     return KVQ_ERR_INVALID_ARGUMENT;
   if (num_tokens > (1LL << 31) * 8) return KVQ_ERR_UNSUPPORTED;
   const bool kvarn = (cache->flags & KVQ_FLAG_VARNORM_ROTATE) != 0;
+  const bool block = is_block(cache->k_fmt);
+  const int sms = block ? sm_count() : 0;
+  if (block && sms <= 0) return KVQ_ERR_CUDA;
   WriteArgs a;
   a.key = static_cast<const uint16_t*>(key);
   a.value = static_cast<const uint16_t*>(value);
@@ -383,7 +390,8 @@ kvq_status kvq_write_cache(const kvq_cache_desc* cache, void* k_cache, void* v_c
   a.signs = cache->signs;
   a.cR = rotation_scale(cache->head_dim);
   const cudaError_t e =
-      launch_write(a, cache->head_dim, cache->k_fmt, cache->v_fmt, kvarn, stream);
+      block ? launch_write_block(a, AppendSlots{}, cache->head_dim, cache->k_fmt, cache->v_fmt, stream, sms)
+            : launch_write(a, cache->head_dim, cache->k_fmt, cache->v_fmt, kvarn, stream);
   if (e == cudaErrorNotSupported) return KVQ_ERR_UNSUPPORTED;
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
@@ -425,6 +433,7 @@ kvq_status check_classes(const kvq_cache_desc* classes, int32_t num_classes,
   if (classes == nullptr || k_caches == nullptr || v_caches == nullptr || seq_class == nullptr)
     return KVQ_ERR_INVALID_ARGUMENT;
   if (num_classes < 1 || num_classes > kMaxPageClasses) return KVQ_ERR_UNSUPPORTED;
+  if (is_block(classes[0].k_fmt)) return KVQ_ERR_UNSUPPORTED;  // one pool: a scale belongs to a page
   const kvq_cache_desc& c0 = classes[0];
   for (int c = 0; c < num_classes; ++c) {
     const kvq_cache_desc& x = classes[c];
@@ -548,6 +557,27 @@ kvq_status decode_call(const kvq_cache_desc* classes, int32_t num_classes,
   }
   cudaError_t e = cudaErrorNotSupported;
   const int kf = cache->k_fmt, vf = cache->v_fmt;
+  if (append && is_block(kf)) {  // the new rows first: one may change its page's scale and codes
+    const int sms = sm_count();
+    if (sms <= 0) return KVQ_ERR_CUDA;
+    WriteArgs w = {};
+    w.key = a.new_key;
+    w.value = a.new_value;
+    w.key_stride = a.new_key_stride;
+    w.value_stride = a.new_value_stride;
+    w.num_tokens = num_seqs;
+    w.k_cache = a.k_cache_w[0];
+    w.v_cache = a.v_cache_w[0];
+    w.k_meta = a.k_meta_w[0];
+    w.v_meta = a.v_meta_w[0];
+    w.num_kv_heads = cache->num_kv_heads;
+    w.block_size = cache->block_size;
+    w.block_shift = a.block_shift[0];
+    w.num_blocks = cache->num_blocks;
+    e = launch_write_block(w, AppendSlots{block_table, context_lens, max_blocks_per_seq, max_context_len},
+                           cache->head_dim, kf, vf, stream, sms);
+    if (e != cudaSuccess) return e == cudaErrorNotSupported ? KVQ_ERR_UNSUPPORTED : KVQ_ERR_CUDA;
+  }
 #define KVQ_UNIT_LAUNCHER(U) launch_##U,
   static const DecodeLauncher launchers[] = {KVQ_DECODE_UNITS(KVQ_UNIT_LAUNCHER)};
 #undef KVQ_UNIT_LAUNCHER
@@ -569,8 +599,8 @@ kvq_status append_rows(const kvq_cache_desc* cache, int32_t num_seqs, const void
     const int64_t row = static_cast<int64_t>(cache->num_kv_heads) * cache->head_dim;
     if (key_stride < row || value_stride < row || key_stride % 8 || value_stride % 8)
       return KVQ_ERR_INVALID_ARGUMENT;
-    if (!write_supported(cache->k_fmt, cache->v_fmt,
-                         (cache->flags & KVQ_FLAG_VARNORM_ROTATE) != 0))
+    if (!is_block(cache->k_fmt) &&
+        !write_supported(cache->k_fmt, cache->v_fmt, (cache->flags & KVQ_FLAG_VARNORM_ROTATE) != 0))
       return KVQ_ERR_UNSUPPORTED;
   }
   app->key = new_key;
@@ -802,6 +832,7 @@ kvq_status kvq_norm_rope_write(const kvq_rope_desc* rope, const kvq_cache_desc* 
   st = check_rope(rope, positions, num_tokens, num_q_heads, cache->num_kv_heads, &a);
   if (st != KVQ_OK) return st;
   if (rope->head_dim != cache->head_dim) return KVQ_ERR_INVALID_ARGUMENT;
+  if (is_block(cache->k_fmt)) return KVQ_ERR_UNSUPPORTED;  // kvq_norm_rope, then kvq_write_cache
   if (num_tokens == 0) return KVQ_OK;
   const int64_t d = cache->head_dim, row = cache->num_kv_heads * d;
   if (!k_cache || !v_cache || !slot_mapping || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
@@ -931,6 +962,100 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
+kvq_status kvq_prompt_attention(void* out, int64_t out_stride, const void* query, int64_t query_stride,
+                                const void* key, int64_t key_stride, const void* value,
+                                int64_t value_stride, const int32_t* cu_seqlens, int32_t num_seqs,
+                                int64_t total_tokens, int32_t max_len, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim, float sm_scale, int32_t window,
+                                int32_t num_sinks, kvq_stream_t stream) {
+  if (num_seqs < 0 || total_tokens < 0 || max_len < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
+      head_dim < 1 || window < 0 || num_sinks < 0 || !isfinite(sm_scale))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_q_heads % num_kv_heads) return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_q_heads / num_kv_heads > 8 || (head_dim != 64 && head_dim != 128)) return KVQ_ERR_UNSUPPORTED;
+  if (total_tokens > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || total_tokens == 0 || max_len == 0) return KVQ_OK;
+  const int64_t d = head_dim;
+  const Rows rows[] = {{query, query_stride, num_q_heads * d}, {key, key_stride, num_kv_heads * d},
+                       {value, value_stride, num_kv_heads * d}, {out, out_stride, num_q_heads * d}};
+  for (const Rows& r : rows)
+    if (!rows_ok(r) || r.stride > (1ll << 31)) return KVQ_ERR_INVALID_ARGUMENT;
+  if (!cu_seqlens || !aligned(cu_seqlens, 4)) return KVQ_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < 3; ++i)  // other CTAs read what one writes: not in place
+    if (rows_meet(rows[3], rows[i], total_tokens)) return KVQ_ERR_INVALID_ARGUMENT;
+  const int sms = sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  PromptArgs a = {};
+  a.query = static_cast<const uint16_t*>(query);
+  a.key = static_cast<const uint16_t*>(key);
+  a.value = static_cast<const uint16_t*>(value);
+  a.out = static_cast<uint16_t*>(out);
+  a.query_stride = query_stride;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.out_stride = out_stride;
+  a.cu_seqlens = cu_seqlens;
+  a.num_seqs = num_seqs;
+  a.total = total_tokens;
+  a.max_len = static_cast<int>(std::min<int64_t>(max_len, total_tokens));
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.gqa = num_q_heads / num_kv_heads;
+  a.sm_scale_log2 = sm_scale * kLog2e;
+  a.window = std::min(window, 1 << 30);  // prompts are no longer
+  a.sinks = std::min(num_sinks, 1 << 30);
+  bound_waits(&a, kPrefillSpinLimit);
+  const cudaError_t e = launch_prompt(a, head_dim, stream, sms);
+  if (e == cudaErrorNotSupported) return KVQ_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_read_cache(const kvq_cache_desc* cache, const void* k_cache, const void* v_cache,
+                          void* key_out, void* value_out, int64_t key_out_stride,
+                          int64_t value_out_stride, const int64_t* slot_mapping, int64_t num_tokens,
+                          kvq_stream_t stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (num_tokens < 0) return KVQ_ERR_INVALID_ARGUMENT;
+  if (num_tokens == 0) return KVQ_OK;
+  if (!k_cache || !v_cache || !slot_mapping || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(slot_mapping, 8))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  const int64_t row = static_cast<int64_t>(cache->num_kv_heads) * cache->head_dim;
+  if (num_tokens > (1LL << 31) * 8 || row > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+  const Rows rows[] = {{key_out, key_out_stride, row}, {value_out, value_out_stride, row}};
+  if (!rows_ok(rows[0]) || !rows_ok(rows[1]) || rows_meet(rows[0], rows[1], num_tokens))
+    return KVQ_ERR_INVALID_ARGUMENT;
+  const int sms = sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  ReadArgs a = {};
+  a.codes[0] = static_cast<const uint8_t*>(k_cache);
+  a.codes[1] = static_cast<const uint8_t*>(v_cache);
+  a.meta[0] = cache->k_meta;
+  a.meta[1] = cache->v_meta;
+  a.head_scale[0] = cache->k_head_scales;
+  a.head_scale[1] = cache->v_head_scales;
+  a.scale[0] = cache->k_scale;
+  a.scale[1] = cache->v_scale;
+  a.fmt[0] = cache->k_fmt;
+  a.fmt[1] = cache->v_fmt;
+  a.out[0] = static_cast<uint16_t*>(key_out);
+  a.out[1] = static_cast<uint16_t*>(value_out);
+  a.out_stride[0] = key_out_stride;
+  a.out_stride[1] = value_out_stride;
+  a.slot_mapping = slot_mapping;
+  a.num_tokens = num_tokens;
+  a.signs = cache->signs;
+  a.cR = rotation_scale(cache->head_dim);
+  a.num_kv_heads = cache->num_kv_heads;
+  a.block_shift = __builtin_ctz(static_cast<unsigned>(cache->block_size));
+  a.num_blocks = cache->num_blocks;
+  const cudaError_t e =
+      launch_read(a, cache->head_dim, (cache->flags & KVQ_FLAG_VARNORM_ROTATE) != 0, stream, sms);
+  if (e == cudaErrorNotSupported) return KVQ_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
 kvq_status kvq_hadamard(void* x, int32_t dtype, int64_t rows, int32_t head_dim,
                         const int8_t* signs, int32_t inverse, kvq_stream_t stream) {
   if (rows < 0 || (dtype != 0 && dtype != 1) || (inverse != 0 && inverse != 1))
@@ -991,6 +1116,8 @@ kvq_status kvq_get_device_error(kvq_stream_t stream, uint32_t* bits) {
   cudaError_t (*take[])(unsigned*) = {take_error_bits_write, take_error_bits_write_asym,
                                       take_error_bits_plan, take_error_bits_norm_rope,
                                       take_error_bits_norm_rope_asym, take_error_bits_prefill,
+                                      take_error_bits_write_block, take_error_bits_read,
+                                      take_error_bits_prompt,
                                       KVQ_DECODE_UNITS(KVQ_UNIT_TAKE)};
 #undef KVQ_UNIT_TAKE
   for (auto f : take)

@@ -62,6 +62,7 @@ struct DecodeCfg {
   static constexpr int VW = VPS / 4;
   static constexpr int KMF = is_asym(KF) ? (KVARN ? 3 : 2) : 0;
   static constexpr int VMF = is_asym(VF) ? (KVARN ? 3 : 2) : 0;
+  static constexpr bool BLOCK = is_block(KF);  // scales per (page, kv-head), of K and V both
   static constexpr int K_HEAD = 16 * KB;  // bytes of one head's 16-token box
   static constexpr int V_HEAD = 16 * VB;
   // swizzle of the TMA boxes: 16-byte chunk index ^= address bits [7, 7+n)
@@ -88,15 +89,20 @@ struct DecodeCfg {
   static_assert(KMF == VMF || KMF == 0 || VMF == 0, "one metadata row layout for K and V");
 };
 
+// Block formats: a tile's scales, [K, V][page of the tile][kv-head], kept outside the ring,
+// whose stages are 1024-byte aligned.
+constexpr int kTileScaleBytes = 128;
+
 // Shared memory of a CTA (bytes): the ring; per warp its query rows (G rows of
 // D bf16, filled ahead of each segment) and, with KVarN, a float row for the
 // query rotation; per stage a tile header and two mbarriers; a scratch area
-// with the producer's cursor and the abort flag; and 1 KB of alignment.
+// with the producer's cursor and the abort flag; block formats' tile scales; and 1 KB of
+// alignment.
 __host__ __device__ constexpr int q_rows_bytes(int g, int d) { return (g * d * 2 + 15) / 16 * 16; }
 template <class C>
 __host__ __device__ constexpr int decode_smem_bytes(int hpc, int g) {
   return C::STAGES * C::stage_bytes(hpc) + hpc * q_rows_bytes(g, C::D) + (C::KVARN_ ? hpc * C::D * 4 : 0) +
-         C::STAGES * 48 + 256 + 1024;
+         C::STAGES * (48 + (C::BLOCK ? kTileScaleBytes : 0)) + 256 + 1024;
 }
 
 // Row of mma row r (0..15) of a tile: the QK row r holds token kRow[r].  With
@@ -277,6 +283,13 @@ __device__ __forceinline__ void tma_codes_heads(uint32_t dst, const CUtensorMap*
   if constexpr (RB > 128) tma_load_5d(dst, map, 0, 0, tok, head0, blk, bar, pol);
   else tma_load_4d(dst, map, 0, tok, head0, blk, bar, pol);
 }
+// Untiled copy of `bytes` (a multiple of 16, both ends 16-byte aligned) completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+      "r"(bytes), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -310,6 +323,7 @@ __device__ __forceinline__ float lds_half(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
   return __half2float(__ushort_as_half(r));
 }
+__device__ __forceinline__ float lds_float(uint32_t a) { return __uint_as_float(lds32(a)); }
 
 
 // Walsh-Hadamard butterfly over rows of D = 8 * E values where lane (g, c) of
@@ -574,7 +588,14 @@ __device__ __forceinline__ long long slot_index(const DecodeArgs& a, long long W
 // owns query head nn's dims 64i + 8r + e (i < DL/8, e < 8), so each 16-byte
 // load of a warp reads whole 128-byte lines; each lane reads every slot's
 // (m, l) itself, and the loads of PU slots are issued together.
-template <int D, bool KVARN>
+// Block formats, whose values may lie anywhere in float32's range: the slot's pair is
+// (m + log2 l, f), f the power of two that the normalised output was divided by to
+// bring its largest element into [1, 2).
+__device__ __forceinline__ float slot_factor(float largest) {
+  const int e = (__float_as_int(largest) >> 23) - 127;  // largest >= 0
+  return __int_as_float((min(max(e, -126), 126) + 127) << 23);
+}
+template <int D, bool KVARN, bool BLOCK>
 __device__ __forceinline__ void merge_slots(const DecodeArgs& a, int s, const SeqSpan& q,
                                             long long W, int HG, int hg, int warp, int lane, int hpc,
                                             int r_first, int step, int count, int r_last,
@@ -638,8 +659,10 @@ __device__ __forceinline__ void merge_slots(const DecodeArgs& a, int s, const Se
         }
 #pragma unroll
         for (int u = 0; u < PU; ++u) {
-          const float w = fast_exp2(ml[u][0] - M) * ml[u][1];  // 2^(m - M) l
-          Lsum += w;
+          float w = fast_exp2(ml[u][0] - M);
+          if constexpr (BLOCK) Lsum += w;
+          w *= ml[u][1];  // 2^(m - M) l
+          if constexpr (!BLOCK) Lsum += w;
 #pragma unroll
           for (int i = 0; i < DL / 8; ++i) {
             const uint32_t q[4] = {v[u][i].x, v[u][i].y, v[u][i].z, v[u][i].w};
@@ -657,6 +680,18 @@ __device__ __forceinline__ void merge_slots(const DecodeArgs& a, int s, const Se
 #pragma unroll
     for (int e = 0; e < DL; ++e) acc[e] *= il;
     if (dst >= 0) {  // an intermediate result: back into slot format
+      if constexpr (BLOCK) {
+        float most = 0.f;
+#pragma unroll
+        for (int e = 0; e < DL; ++e) most = fmaxf(most, fabsf(acc[e]));
+#pragma unroll
+        for (int o = 1; o < LQ; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const float f = slot_factor(most), by = 1.0f / f;
+#pragma unroll
+        for (int e = 0; e < DL; ++e) acc[e] *= by;
+        M += __log2f(Lsum);
+        Lsum = f;
+      }
       if (act) {
         const long long sl = dst * rows + warp * G + nn;
 #pragma unroll
@@ -821,6 +856,9 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   // rows of the partial slot are stored (two ints), [26..28) range bounds
   // (prologue), [28..30) per end of the range: the weighted start of its
   // sequence, [30] the boundary weight, [31] the first sequence's weighted start
+  // block formats: each stage's tile scales, behind the scratch words
+  const uint32_t scales_s = full_s + C::STAGES * 16 + 256;
+  const int scale_bytes = 4 * scale_pitch(hpc);  // of one page
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(scratch + 23);
   int* const done_warps = reinterpret_cast<int*>(scratch + 25);
   const int spin = a.spin_limit;
@@ -956,11 +994,16 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   const int s_first = static_cast<int>(scratch[1]);
   const long long ps_first = scratch[2];
   prefetch_q(s_first);
-  if (a.new_key != nullptr) {  // new-token append: codes stored before any tile is loaded
-    append_new_tokens<D, KF, VF, KVARN, PAGES>(a, R0, R1, s_first, ps_first, h, lane);
-    // the stores (generic proxy) before the tensor loads (async proxy) the
-    // barrier below lets thread 0 issue
-    asm volatile("fence.proxy.async.global;" ::: "memory");
+  // new-token append: codes stored before any tile is loaded (block formats: by a launch of
+  // their own ahead of this one, as a row may change the scale of rows that other CTAs read)
+  const bool append = !C::BLOCK && a.new_key != nullptr;
+  if constexpr (!C::BLOCK) {
+    if (append) {
+      append_new_tokens<D, KF, VF, KVARN, PAGES>(a, R0, R1, s_first, ps_first, h, lane);
+      // the stores (generic proxy) before the tensor loads (async proxy) the
+      // barrier below lets thread 0 issue
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+    }
   }
 
   const long long lam_first = scratch[31];
@@ -971,10 +1014,17 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   }
   // the append's stores before thread 0's first tensor loads (the barriers and
   // flags were set up before the range scan, whose barriers publish them)
-  if (a.new_key != nullptr) __syncthreads();
+  if (append) __syncthreads();
 
   // ---- producer cursor (thread 0): walks the range tile by tile
-  const uint32_t tile_bytes = hpc * (C::K_HEAD + C::V_HEAD) + hpc * (C::KMF + C::VMF) * 32;
+  const uint32_t tile_bytes = hpc * (C::K_HEAD + C::V_HEAD) + hpc * (C::KMF + C::VMF) * 32 +
+                              (C::BLOCK ? (split ? 4 : 2) * scale_bytes : 0);
+  auto load_scales = [&](int st, int page, int b) {  // of block b, the tile's page `page`, both tensors
+    const uint32_t to = scales_s + st * kTileScaleBytes + page * scale_bytes;
+    const size_t at = static_cast<size_t>(b) * scale_pitch(a.num_kv_heads) + hg * hpc;
+    bulk_load(to, reinterpret_cast<const float*>(a.k_meta[0]) + at, scale_bytes, full_s + 8 * st);
+    bulk_load(to + kTileScaleBytes / 2, reinterpret_cast<const float*>(a.v_meta[0]) + at, scale_bytes, full_s + 8 * st);
+  };
   // The cursor lives in shared memory: only thread 0 uses it, and registers
   // held by every thread for it would be taken from the consumers.
   Cursor* cur = reinterpret_cast<Cursor*>(scratch + 16);
@@ -1091,6 +1141,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
         if constexpr (C::VMF > 0)
           tma_load_4d(sb + vm_off + hf * C::meta_half(hpc, C::VMF), &maps.vm[0], 0, 0, hg * hpc, b,
                       bar, pol);
+        if constexpr (C::BLOCK) load_scales(st, hf, b);
       }
     } else {  // one box per tile (pages of 16 or more tokens)
       mbar_arrive_expect(bar, tile_bytes);
@@ -1109,6 +1160,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
         tma_load_4d(sb + m_off, &maps.km[cl], off, 0, hg * hpc, blk, bar, pol);
       if constexpr (C::VMF > 0)
         tma_load_4d(sb + vm_off, &maps.vm[cl], off, 0, hg * hpc, blk, bar, pol);
+      if constexpr (C::BLOCK) load_scales(st, 0, blk);
     }
     ++u.i;
     if (++u.t == u.tiles && u.i < n) {  // on to the next sequence with tokens
@@ -1158,7 +1210,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   const uint32_t meta_k = m_off + warp * C::KMF * fstr;
   const uint32_t meta_v = vm_off + warp * C::VMF * fstr;
   // this warp's kv-head scales (per-kv-head scales, when given, replace the tensor's)
-  const float vsc = is_asym(VF) ? 1.0f : (a.v_head_scale != nullptr ? a.v_head_scale[h] : a.v_scale);
+  const float vsc = is_asym(VF) || C::BLOCK ? 1.0f : (a.v_head_scale != nullptr ? a.v_head_scale[h] : a.v_scale);
   const float qks = (!is_asym(KF) && a.k_head_scale != nullptr) ? a.qk_base * a.k_head_scale[h]
                                                                 : a.qk_scale;
 
@@ -1293,7 +1345,13 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
         ks0 *= sg0; kz0 *= sg0; ks1 *= sg1; kz1 *= sg1;
       }
     }
-    if constexpr (KF == INT8) {
+    // block formats: the scales of the pages that rows 0-7 and 8-15 lie in
+    const uint32_t scale_s = scales_s + st * kTileScaleBytes + 4 * warp;
+    if constexpr (C::BLOCK) {
+      ks0 = a.qk_base * lds_float(scale_s + (split ? (row0 >> 3) * scale_bytes : 0));
+      ks1 = split ? a.qk_base * lds_float(scale_s + (row1 >> 3) * scale_bytes) : ks0;
+    }
+    if constexpr (code_fmt(KF) == INT8) {
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -1304,7 +1362,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
 #pragma unroll
     for (int j = 0; j < C::KSTEPS; ++j) {
       uint32_t a0, a1, a2, a3;
-      k_frag<KF, C::KW>(kw, j, a0, a1, a2, a3);
+      k_frag<code_fmt(KF), C::KW>(kw, j, a0, a1, a2, a3);
       if (j & 1) mma16816<KF == BF16>(sbb[0], sbb[1], sbb[2], sbb[3], a0, a1, a2, a3, qf[j][0], qf[j][1]);
       else mma16816<KF == BF16>(sa[0], sa[1], sa[2], sa[3], a0, a1, a2, a3, qf[j][0], qf[j][1]);
     }
@@ -1314,11 +1372,12 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
 #pragma unroll
       for (int q = 0; q < 4; ++q) sacc[q] = sa[q] + sbb[q];
       if constexpr (!is_asym(KF)) {
-        constexpr float bias = KF == INT8 ? 1152.0f : 0.0f;
-        sl[0] = (sacc[0] - bias * qsum0) * qks;
-        sl[1] = (sacc[1] - bias * qsum1) * qks;
-        sl[2] = (sacc[2] - bias * qsum0) * qks;
-        sl[3] = (sacc[3] - bias * qsum1) * qks;
+        constexpr float bias = code_fmt(KF) == INT8 ? 1152.0f : 0.0f;
+        const float f0 = C::BLOCK ? ks0 : qks, f1 = C::BLOCK ? ks1 : qks;
+        sl[0] = (sacc[0] - bias * qsum0) * f0;
+        sl[1] = (sacc[1] - bias * qsum1) * f0;
+        sl[2] = (sacc[2] - bias * qsum0) * f1;
+        sl[3] = (sacc[3] - bias * qsum1) * f1;
       } else {
         sl[0] = (ks0 * (sacc[0] - qb0) + kz0 * qsum0) * a.qk_scale;
         sl[1] = (ks0 * (sacc[1] - qb1) + kz0 * qsum1) * a.qk_scale;
@@ -1359,11 +1418,15 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
         vs0 *= sg0; vz0 *= sg0; vs1 *= sg1; vz1 *= sg1;
       }
     }
+    if constexpr (C::BLOCK) {
+      vs0 = lds_float(scale_s + kTileScaleBytes / 2 + (split ? (row0 >> 3) * scale_bytes : 0));
+      vs1 = split ? lds_float(scale_s + kTileScaleBytes / 2 + (row1 >> 3) * scale_bytes) : vs0;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(empty_s + 8 * st);
     __syncwarp();
 
-    if constexpr (VF == INT8) {
+    if constexpr (code_fmt(VF) == INT8) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -1374,7 +1437,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
       for (int u = 0; u < 4; ++u)
         if (!in_view(v_token(c, u))) {
 #pragma unroll
-          for (int q = 0; q < C::VW; ++q) vw[u][q] = (VF == INT8) ? 0x80808080u : 0u;
+          for (int q = 0; q < C::VW; ++q) vw[u][q] = (code_fmt(VF) == INT8) ? 0x80808080u : 0u;
         }
     }
 
@@ -1408,7 +1471,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
       for (int o = 4; o <= 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
       return x;
     };
-    if constexpr (is_asym(VF)) {
+    if constexpr (is_asym(VF) || C::BLOCK) {
       // The operand is p times the row's scale, in fp16, whatever the scale's size: m is
       // the maximum less the lift that brings the largest operand of the tile that
       // raises it to 2^10..2^11, and it is raised when one passes 2^15.  (With p <= 2^8
@@ -1432,15 +1495,19 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
         mx0 = tile_max(fmaxf(sl[0], sl[2]));
         mx1 = tile_max(fmaxf(sl[1], sl[3]));
         // 2^lift times the largest scale is in [2^10, 2^11)
-        const float vm = fminf(fmaxf(tile_max(fmaxf(fabsf(vs0), fabsf(vs1))), 0x1p-30f), 0x1p33f);
+        // (fp16 scales lie within 2^-24 .. 2^16 and with a deviation 2^32, a page's anywhere)
+        const float vm = fminf(fmaxf(tile_max(fmaxf(fabsf(vs0), fabsf(vs1))), C::BLOCK ? 0x1p-100f : 0x1p-30f),
+                               C::BLOCK ? 0x1p122f : 0x1p33f);
         const float lift = static_cast<float>(137 - (__float_as_int(vm) >> 23));
         raise(mx0 - lift, mx1 - lift);
         products();
       }
       l0 += sum0;
       l1 += sum1;
-      z0 += pr[0] * vz0 + pr[2] * vz1;
-      z1 += pr[1] * vz0 + pr[3] * vz1;
+      if constexpr (!C::BLOCK) {
+        z0 += pr[0] * vz0 + pr[2] * vz1;
+        z1 += pr[1] * vz0 + pr[3] * vz1;
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u) pr[u] = px[u];
     } else {
@@ -1465,7 +1532,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
 #pragma unroll
     for (int d = 0; d < C::DTILES; ++d) {
       uint32_t a0, a1, a2, a3;
-      v_frag<VF, C::VW>(vw, d, a0, a1, a2, a3);
+      v_frag<code_fmt(VF), C::VW>(vw, d, a0, a1, a2, a3);
       mma16816<VF == BF16>(Oa[2 * d], Ob[2 * d], Oa[2 * d + 1], Ob[2 * d + 1], a0, a1, a2, a3, b0,
                            b1);
     }
@@ -1526,6 +1593,29 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
     }
 
     // ---- part of a sequence: (m, l, acc) into this range's slot, then publish
+    if constexpr (C::BLOCK) {
+      float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        a0 = fmaxf(a0, fabsf(Oa[e]));
+        a1 = fmaxf(a1, fabsf(Ob[e]));
+      }
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) {
+        a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, o));
+        a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, o));
+      }
+      const float f0 = slot_factor(a0), f1 = slot_factor(a1), by0 = 1.0f / f0, by1 = 1.0f / f1;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        Oa[e] *= by0;
+        Ob[e] *= by1;
+      }
+      m0 += __log2f(L0);
+      m1 += __log2f(L1);
+      L0 = f0;
+      L1 = f1;
+    }
     const size_t slot = ((static_cast<size_t>(k) * HG + hg) * 2 + j) * (hpc * G) + warp * G;
     if (2 * c < G) store_f16_run<E>(a.ws_acc + (slot + 2 * c) * D + g * E, Oa);
     if (2 * c + 1 < G) store_f16_run<E>(a.ws_acc + (slot + 2 * c + 1) * D + g * E, Ob);
@@ -1616,13 +1706,13 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
                     bwm};
     const int ka = first_range(a, Wm, q), kb = last_range(a, Wm, q);
     if (kb - ka + 1 <= kTreeRanges) {  // one level: every range's slot, straight to the output
-      merge_slots<D, KVARN>(a, s, q, Wm, HG, hg, warp, lane, hpc, ka, 1, kb - ka + 1, kb, -1);
+      merge_slots<D, KVARN, C::BLOCK>(a, s, q, Wm, HG, hg, warp, lane, hpc, ka, 1, kb - ka + 1, kb, -1);
       continue;
     }
     const int nteams = (kb - ka) / kTeam + 1;
     const int lo = ka + (k - ka) / kTeam * kTeam, hi = min(kb, lo + kTeam - 1);
     const long long rep = slot_index(a, Wm, q, lo, HG, hg);
-    merge_slots<D, KVARN>(a, s, q, Wm, HG, hg, warp, lane, hpc, lo, 1, hi - lo + 1, kb, rep);
+    merge_slots<D, KVARN, C::BLOCK>(a, s, q, Wm, HG, hg, warp, lane, hpc, lo, 1, hi - lo + 1, kb, rep);
     __syncthreads();  // every warp's rows of the team result are stored
     if (warp == pub) {
       if (lane == 0) {
@@ -1648,7 +1738,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
     }
     __syncthreads();
     if (scratch[4 + pm])
-      merge_slots<D, KVARN>(a, s, q, Wm, HG, hg, warp, lane, hpc, ka, kTeam, nteams, kb, -1);
+      merge_slots<D, KVARN, C::BLOCK>(a, s, q, Wm, HG, hg, warp, lane, hpc, ka, kTeam, nteams, kb, -1);
   }
 }
 

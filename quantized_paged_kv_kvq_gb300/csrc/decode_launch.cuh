@@ -125,7 +125,9 @@ cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
 
   auto kern_one = decode_partition_kernel<D, KF, VF, KVARN, kPagesOne>;
   auto kern_split = decode_partition_kernel<D, KF, VF, KVARN, kPages8>;
-  auto kern_mixed = decode_partition_kernel<D, KF, VF, KVARN, kPagesMixed>;
+  // block formats: one pool only (kern_mixed is not used)
+  auto kern_mixed = decode_partition_kernel<D, KF, VF, KVARN, C::BLOCK ? kPagesOne : kPagesMixed>;
+  if (C::BLOCK && a.seq_class != nullptr) return cudaErrorNotSupported;
   auto kern_window = decode_partition_kernel<D, KF, VF, KVARN, kPagesWindow>;
   auto kern_split_window = decode_partition_kernel<D, KF, VF, KVARN, kPages8Window>;
   const int smem = decode_smem_bytes<C>(hpc, a.gqa);
@@ -148,7 +150,7 @@ cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
   }
   const dim3 grid(a.num_ctas, a.num_kv_heads / hpc, 1);
   if (a.seq_class != nullptr) {  // a class array: the mixed instance (pages of 16 or more)
-    kern_mixed<<<grid, hpc * 32, smem, st>>>(args, maps);
+    if constexpr (!C::BLOCK) kern_mixed<<<grid, hpc * 32, smem, st>>>(args, maps);
   } else {  // one pool: class 0's maps only
     DecodeMaps<1> one;
     one.k[0] = maps.k[0];

@@ -12,9 +12,14 @@
 
 namespace kvq {
 
-enum Fmt : int { INT8 = 1, E4M3 = 2, E5M2 = 3, INT4A = 4, UINT8A = 5, BF16 = 6 };
+enum Fmt : int { INT8 = 1, E4M3 = 2, E5M2 = 3, INT4A = 4, UINT8A = 5, BF16 = 6, INT8B = 7, E4M3B = 8 };
 
 __host__ __device__ constexpr bool is_asym(int f) { return f == INT4A || f == UINT8A; }
+// A float32 scale per (page, kv-head), and what its codes are.
+__host__ __device__ constexpr bool is_block(int f) { return f == INT8B || f == E4M3B; }
+__host__ __device__ constexpr int code_fmt(int f) { return f == INT8B ? INT8 : f == E4M3B ? E4M3 : f; }
+// Scales of a page: one per kv-head, the row padded to 16 bytes.
+__host__ __device__ constexpr int scale_pitch(int num_kv_heads) { return (num_kv_heads + 3) / 4 * 4; }
 __host__ __device__ constexpr int row_bytes(int f, int d) {
   return f == INT4A ? d / 2 : f == BF16 ? 2 * d : d;
 }

@@ -229,6 +229,60 @@ cudaError_t launch_prefill(const PrefillArgs& a, int head_dim, cudaStream_t st);
 
 cudaError_t launch_write(const WriteArgs& a, int head_dim, int kf, int vf, bool kvarn,
                          cudaStream_t st);
+// Block formats (k_meta / v_meta: float32 scales).  slot_mapping nullptr: token t is the last
+// one of sequence t, in the page that its block table names.
+struct AppendSlots {
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  int max_blocks_per_seq;
+  int max_context_len;
+};
+cudaError_t launch_write_block(const WriteArgs& a, const AppendSlots& s, int head_dim, int kf, int vf,
+                               cudaStream_t st, int num_sms);
+
+// Rows of the cache as bf16 (kvq_read_cache).
+struct ReadArgs {
+  const uint8_t* codes[2];  // K, V
+  const void* meta[2];      // fp16 fields, or float32 scales (block formats)
+  const float* head_scale[2];
+  float scale[2];
+  int fmt[2];
+  uint16_t* out[2];  // bf16 bits
+  int64_t out_stride[2];
+  const int64_t* slot_mapping;
+  int64_t num_tokens;
+  const int8_t* signs;
+  float cR;
+  int num_kv_heads;
+  int block_shift;
+  int num_blocks;
+};
+cudaError_t launch_read(const ReadArgs& a, int head_dim, bool kvarn, cudaStream_t st, int num_sms);
+
+// Attention of whole prompts in 16 bits (kvq_prompt_attention).
+struct PromptArgs {
+  const uint16_t* query;  // bf16 [total, Hq, D], tokens the strides apart (elements)
+  const uint16_t* key;
+  const uint16_t* value;
+  uint16_t* out;
+  int64_t query_stride, key_stride, value_stride, out_stride;
+  const int32_t* cu_seqlens;  // [S + 1]
+  int num_seqs;
+  int64_t total;
+  int max_len;
+  int num_q_heads;
+  int num_kv_heads;
+  int gqa;
+  float sm_scale_log2;  // sm_scale * log2(e)
+  int window;           // 0: every earlier token
+  int sinks;
+  int tokens_per_tile;  // of a row tile (set by the launcher)
+  int tiles;            // row tiles the launch has room for
+  int spin_limit;
+  int withhold_cta;
+  int withhold_tile;
+};
+cudaError_t launch_prompt(const PromptArgs& a, int head_dim, cudaStream_t st, int num_sms);
 cudaError_t launch_write_asym(const WriteArgs& a, int head_dim, int kf, int vf, bool kvarn,
                               cudaStream_t st);
 bool write_supported(int kf, int vf, bool kvarn);
@@ -246,6 +300,8 @@ using DecodeLauncher = cudaError_t (*)(const DecodeArgs& a, int head_dim, int kf
   X(decode_d128_fp8k)       \
   X(decode_d128_asym)       \
   X(decode_d128_kvarn)      \
+  X(decode_d64_block)       \
+  X(decode_d128_block)      \
   X(decode_bf16)
 #define KVQ_DECLARE_UNIT(U)                                                                  \
   cudaError_t launch_##U(const DecodeArgs& a, int head_dim, int kf, int vf, bool kvarn,      \
@@ -262,6 +318,9 @@ cudaError_t take_error_bits_plan(unsigned* bits);
 cudaError_t take_error_bits_norm_rope(unsigned* bits);
 cudaError_t take_error_bits_norm_rope_asym(unsigned* bits);
 cudaError_t take_error_bits_prefill(unsigned* bits);
+cudaError_t take_error_bits_write_block(unsigned* bits);
+cudaError_t take_error_bits_read(unsigned* bits);
+cudaError_t take_error_bits_prompt(unsigned* bits);
 
 cudaError_t launch_hadamard(void* x, int dtype, int64_t rows, int head_dim, const int8_t* signs,
                             int inverse, float cR, cudaStream_t st);

@@ -18,8 +18,10 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvq.so")
 
-FMT = {"int8": 1, "fp8_e4m3": 2, "fp8_e5m2": 3, "int4_asym": 4, "uint8_asym": 5, "bf16": 6}
+FMT = {"int8": 1, "fp8_e4m3": 2, "fp8_e5m2": 3, "int4_asym": 4, "uint8_asym": 5, "bf16": 6,
+       "int8_block": 7, "fp8_e4m3_block": 8}
 ASYM = ("int4_asym", "uint8_asym")
+BLOCK = ("int8_block", "fp8_e4m3_block")
 FLAG_VARNORM_ROTATE = 1
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARGUMENT", 2: "KVQ_ERR_UNSUPPORTED",
           3: "KVQ_ERR_WORKSPACE", 4: "KVQ_ERR_CUDA"}
@@ -102,6 +104,9 @@ SIGNATURES = {
                                           ctypes.POINTER(_SZ)]),
     "kvq_paged_prefill": (_I32, [_DESC, _P, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _P, _I32, _P,
                                  _I32, _F32, _I32, _I32, _P, _SZ, _P]),
+    "kvq_prompt_attention": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _I32, _I32, _I32,
+                                    _I32, _F32, _I32, _I32, _P]),
+    "kvq_read_cache": (_I32, [_DESC, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P]),
     "kvq_hadamard": (_I32, [_P, _I32, _I64, _I32, _P, _I32, _P]),
     "kvq_calibrate_scale": (_I32, [_P, _I64, _F32, _P, _P]),
     "kvq_calibrate_head_scales": (_I32, [_P, _I64, _I32, _I32, _I64, _F32, _P, _P]),
@@ -151,7 +156,8 @@ class KVCache:
     """One layer's paged cache: caller-owned device tensors + description.
 
     k_cache / v_cache: uint8 [num_blocks, block_size, num_kv_heads, row_bytes]
-    k_meta / v_meta:   fp16 [num_blocks, num_kv_heads, F, block_size] (asymmetric formats)
+    k_meta / v_meta:   fp16 [num_blocks, num_kv_heads, F, block_size] (asymmetric formats);
+                       fp32 [num_blocks, num_kv_heads rounded up to 4] (block formats)
     signs:             int8 [head_dim] of +-1 (KVarN rotation) or None
 
     The tensors may hold more blocks than num_blocks.
@@ -193,6 +199,11 @@ def meta_fields(fmt: str, varnorm_rotate: bool) -> int:
     return 0
 
 
+def scale_pitch(num_kv_heads: int) -> int:
+    """Entries of a page's row of scales (block formats)."""
+    return (num_kv_heads + 3) // 4 * 4
+
+
 def alloc_kv_cache(k_fmt, v_fmt, num_blocks, block_size, num_kv_heads, head_dim,
                    k_scale=1.0, v_scale=1.0, varnorm_rotate=False, signs=None,
                    device="cuda", fill: Optional[int] = None) -> KVCache:
@@ -205,6 +216,11 @@ def alloc_kv_cache(k_fmt, v_fmt, num_blocks, block_size, num_kv_heads, head_dim,
         return t
 
     def meta(fmt):
+        if fmt in BLOCK:
+            t = torch.empty((num_blocks, scale_pitch(num_kv_heads)), dtype=torch.float32, device=device)
+            if fill is not None:
+                t.view(torch.uint8).fill_(fill)
+            return t
         nf = meta_fields(fmt, varnorm_rotate)
         if not nf:
             return None
@@ -429,6 +445,11 @@ def _cache_desc(dev: int, cache: KVCache) -> _CacheDesc:
     if c.v_fmt in ASYM:
         _need(c.v_meta is not None, "v_meta is missing: rows of this format have fields")
         _pool(dev, "v_meta", c.v_meta, torch.float16, blocks, hkv, 3 if rot else 2, bs)
+    for name, fmt, m in (("k_meta", c.k_fmt, c.k_meta), ("v_meta", c.v_fmt, c.v_meta)):
+        if fmt in BLOCK:
+            _need(m is not None, f"{name} is missing: pages of this format have scales")
+            _need(m.dim() == 2 and m.shape[0] >= blocks, f"{name} must have a row for each of {blocks} blocks")
+            _tensors(dev, (name, m, torch.float32, (m.shape[0], scale_pitch(hkv))))
     if rot and c.signs is not None:
         _tensors(dev, ("signs", c.signs, torch.int8, (d,)))
     if c.k_head_scales is not None:
@@ -647,6 +668,45 @@ def kvq_paged_prefill(cache: KVCache, query: torch.Tensor, out: torch.Tensor,
     return out
 
 
+def kvq_prompt_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor, out: torch.Tensor,
+                         cu_seqlens: torch.Tensor, max_len: int, sm_scale: float, window: int = 0,
+                         num_sinks: int = 0, stream=None) -> torch.Tensor:
+    """out <- causal attention within each of the packed sequences (query, out: bf16 [T, Hq, D];
+    key, value: bf16 [T, Hkv, D], token strides free; tokens cu_seqlens[s]..cu_seqlens[s+1]-1
+    are sequence s) through `window` (0: no limit) and num_sinks."""
+    t, hq, d = query.shape
+    q, kv = (t, hq, d), (t, key.shape[1], d)
+    s = cu_seqlens.numel() - 1
+    _need(s >= 0, "cu_seqlens must have an entry more than there are sequences")
+    _int32(max_len=max_len, window=window, num_sinks=num_sinks)
+    dev = _device_of("query", query)
+    qs, ks = _rows(dev, "query", query, q), _rows(dev, "key", key, kv)
+    vs, os = _rows(dev, "value", value, kv), _rows(dev, "out", out, q)
+    _tensors(dev, ("cu_seqlens", cu_seqlens, torch.int32, (s + 1,)))
+    st = load_library().kvq_prompt_attention(
+        out.data_ptr(), os, query.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs,
+        cu_seqlens.data_ptr(), s, t, max_len, hq, kv[1], d, float(sm_scale), window, num_sinks,
+        _raw_stream(dev, stream))
+    _check(st, "kvq_prompt_attention")
+    return out
+
+
+def kvq_read_cache(cache: KVCache, slot_mapping: torch.Tensor, key_out: torch.Tensor,
+                   value_out: torch.Tensor, stream=None) -> None:
+    """key_out, value_out (bf16 [T, Hkv, D], token strides free) <- the rows at slot_mapping
+    (int64 [T]; a negative slot leaves its row as it was), dequantized."""
+    t = slot_mapping.numel()
+    kv = (t, cache.num_kv_heads, cache.head_dim)
+    dev = _device_of("slot_mapping", slot_mapping)
+    _tensors(dev, ("slot_mapping", slot_mapping, torch.int64, (t,)))
+    ks, vs = _rows(dev, "key_out", key_out, kv), _rows(dev, "value_out", value_out, kv)
+    c = _cache_desc(dev, cache)
+    st = load_library().kvq_read_cache(
+        ctypes.byref(c), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), key_out.data_ptr(),
+        value_out.data_ptr(), ks, vs, slot_mapping.data_ptr(), t, _raw_stream(dev, stream))
+    _check(st, "kvq_read_cache")
+
+
 def kvq_hadamard(x: torch.Tensor, signs: Optional[torch.Tensor] = None, inverse: bool = False,
                  stream=None) -> torch.Tensor:
     """In-place rotation of the rows of x (float32 or bf16, [..., D], contiguous)."""
@@ -681,7 +741,7 @@ def kvq_calibrate_head_scales(x: torch.Tensor, qmax: float, out: torch.Tensor, s
 
 
 def kvq_debug_arm_wait_timeout(polls: int, cta: int, tile: int) -> None:
-    """Test hook: the next decode or chunk-attention launch polls each pipeline wait at
+    """Test hook: the next decode, chunk- or prompt-attention launch polls each pipeline wait at
     most `polls` times, and CTA `cta` (first kv-head group; first part of the keys) never
     gets its range's tile `tile`, so that a wait runs out (KVQ_DEVERR_TIMEOUT); one
     launch only."""
