@@ -34,7 +34,7 @@ bool pairing_ok(int kf, int vf, bool kvarn) {
   return ak == av;
 }
 bool scaled(int f) { return !is_asym(f) && !is_block(f) && f != KVQ_FMT_BF16; }
-bool has_meta(int f) { return is_asym(f) || is_block(f); }
+constexpr bool has_meta(int f) { return is_asym(f) || is_block(f); }
 
 // A power of two from 8 to 128: a 16-token tile lies in one block, or in two
 // consecutive entries of the block table (8-token pages).
@@ -251,7 +251,7 @@ struct PrefillShape {
 // 138 us, 8 257 / 257, 1 x 8,192 keys and 32 tiles 193 / 217; KVarN, 16 x 4,096 keys:
 // 2 tiles 223 / 222, 8 x 4,096: 4 tiles 182 / 210, 8 289 / 389; int4 4 tiles 165 / 177;
 // bf16 as int8.
-constexpr int64_t stage_tiles(int fmt) { return is_asym(fmt) ? 3 : 8; }
+constexpr int64_t stage_tiles(int fmt) { return has_meta(fmt) ? 3 : 8; }
 constexpr int64_t kStageBytes = 16ll << 30;
 // What can be said of a batch's sizes without a device.
 kvq_status check_prefill(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
@@ -262,7 +262,6 @@ kvq_status check_prefill(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
     return KVQ_ERR_INVALID_ARGUMENT;
   if (num_q_heads % c->num_kv_heads) return KVQ_ERR_INVALID_ARGUMENT;
   if (num_q_heads / c->num_kv_heads > 8) return KVQ_ERR_UNSUPPORTED;
-  if (is_block(c->k_fmt)) return KVQ_ERR_UNSUPPORTED;
   if (total_q > INT32_MAX || max_context_len > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->block_size) * c->num_kv_heads * c->head_dim * 2 > INT32_MAX)
     return KVQ_ERR_UNSUPPORTED;  // a block's bytes fit 31 bits

@@ -225,13 +225,14 @@ __device__ __forceinline__ int tile_key(const Span& s, int i) { return kKeys * (
 
 // A row's fields, each an fp16 value twice, as dequantize16 takes them.  Rotated rows:
 // scale and zero point times the deviation, in float32 (products of 11 bits each: exact).
-template <bool KVARN>
+// Block formats: the bits of the page's scale, a float32, in the first.
+template <int F, bool KVARN>
 struct RowFields {
   uint32_t s, z;
   __device__ __forceinline__ RowFields(uint32_t scale, uint32_t zero, uint32_t) : s(scale), z(zero) {}
 };
-template <>
-struct RowFields<true> {
+template <int F>
+struct RowFields<F, true> {
   float s, z;
   __device__ __forceinline__ RowFields(uint32_t scale, uint32_t zero, uint32_t deviation) {
     const float g = __half2float(__ushort_as_half(static_cast<uint16_t>(deviation)));
@@ -243,9 +244,10 @@ struct RowFields<true> {
 // 16 bytes of codes as 16-bit operands: 16 (8-bit codes) or 32 (int4) fp16
 // values, in order.  Asymmetric rows are rounded once, to fp16: code * scale + zero
 // point by a fused fp16 operation, rotated rows (code * (scale * deviation) + zero point *
-// deviation) in float32, where code * scale may pass fp16's range on the way.
+// deviation) in float32, where code * scale may pass fp16's range on the way; rows of block
+// formats too, code * scale in float32.
 template <int F, bool KVARN>
-__device__ __forceinline__ void dequantize16(const uint4& raw, const RowFields<KVARN>& row,
+__device__ __forceinline__ void dequantize16(const uint4& raw, const RowFields<F, KVARN>& row,
                                              uint32_t (&o)[F == INT4A ? 16 : 8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   constexpr uint32_t K64 = 0x64646464u;
@@ -283,6 +285,30 @@ __device__ __forceinline__ void dequantize16(const uint4& raw, const RowFields<K
     } else if constexpr (F == E5M2) {
       o[2 * i] = prmt(w[i], 0u, 0x1404);
       o[2 * i + 1] = prmt(w[i], 0u, 0x3424);
+    } else if constexpr (is_block(F)) {
+      const float s = __uint_as_float(row.s);
+      float x[4];
+      if constexpr (F == INT8B) {  // 2^23 + (code + 128), less both
+        const uint32_t b = w[i] ^ 0x80808080u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(prmt(b, 0x4B000000u, 0x7440u + e));
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) add2(x[e], x[e + 1], x[e], x[e + 1], -8388736.f, -8388736.f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t h = e4m3x2_to_f16x2((w[i] >> (16 * e)) & 0xFFFFu);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          x[2 * e] = f.x;
+          x[2 * e + 1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        float u, v;
+        mul2(u, v, x[e], x[e + 1], s, s);
+        o[2 * i + e / 2] = pack_half2(u, v);
+      }
     } else if constexpr (F == UINT8A) {
       affine2(w[i], o + 2 * i);
     } else {  // INT4A: element 2i in the low nibble of byte i
@@ -331,6 +357,11 @@ __device__ __forceinline__ uint4 ldsv4(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
   return r;
 }
+__device__ __forceinline__ uint32_t lds_word(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t lds_pair(uint32_t a) {  // a 16-bit value, twice
   uint16_t r;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
@@ -353,8 +384,8 @@ __device__ __forceinline__ uint32_t chunk_addr(uint32_t tile, int row, int q, in
 // One of the two caches, as the producers read it.
 struct Source {
   const uint8_t* codes;  // of the kv-head
-  const __half* meta;    // of the kv-head, or nullptr
-  uint32_t page_bytes, meta_page;  // codes of a block in bytes; metadata of a block in halves
+  const __half* meta;    // of the kv-head, or nullptr (block formats: its float32 scales)
+  uint32_t page_bytes, meta_page;  // codes of a block in bytes; metadata of a block in halves (floats)
   int token_bytes;
   int fmt, fields;
 };
@@ -366,9 +397,9 @@ __device__ __forceinline__ Source make_source(const uint8_t* cache, const __half
   s.token_bytes = hkv * rb;
   s.page_bytes = static_cast<uint32_t>(bs) * s.token_bytes;  // below 2^31: checked on the host
   s.fmt = fmt;
-  s.fields = is_asym(fmt) ? (kvarn ? 3 : 2) : 0;
-  s.meta = is_asym(fmt) ? meta + static_cast<size_t>(h) * s.fields * bs : nullptr;
-  s.meta_page = static_cast<uint32_t>(hkv) * s.fields * bs;
+  s.fields = is_asym(fmt) ? (kvarn ? 3 : 2) : is_block(fmt) ? 1 : 0;
+  s.meta = is_asym(fmt) ? meta + static_cast<size_t>(h) * s.fields * bs : is_block(fmt) ? meta + 2 * h : nullptr;
+  s.meta_page = is_block(fmt) ? scale_pitch(hkv) : static_cast<uint32_t>(hkv) * s.fields * bs;
   return s;
 }
 
@@ -473,7 +504,12 @@ struct Producer {
     if (s.fmt == BF16) copy_codes<BF16>(s, k, slot, dst);
     else if (s.fmt == INT4A) copy_codes<INT4A>(s, k, slot, dst);
     else copy_codes<INT8>(s, k, slot, dst);  // any 8-bit code
-    if (s.fields > 0) {  // a pair of tokens per thread and field
+    if (is_block(s.fmt)) {  // a token per thread: its page's scale
+      const int blk = __shfl_sync(0xffffffffu, k.block, tid >> a.block_shift);
+      cp_async_or_zero<4>(smem + C::META + slot * 3 * kKeys * 2 + tid * 4,
+                          reinterpret_cast<const float*>(s.meta) + static_cast<unsigned long long>(static_cast<uint32_t>(blk)) * s.meta_page,
+                          needed(k.t0 + tid));
+    } else if (s.fields > 0) {  // a pair of tokens per thread and field
       const int row = 2 * (tid & 63), t = k.t0 + row;
       const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
       const __half* src = s.meta + static_cast<unsigned long long>(static_cast<uint32_t>(blk)) * s.meta_page +
@@ -490,7 +526,8 @@ struct Producer {
     using P = Pieces<F, C::D>;
     const P p(tid);
     const uint32_t raw = smem + C::RAWQ + slot * C::RAW + tid * 16;
-    const uint32_t meta = smem + C::META + slot * 3 * kKeys * 2 + p.row0 * 2;
+    constexpr int MB = is_block(F) ? 4 : 2;  // bytes of a row's field
+    const uint32_t meta = smem + C::META + slot * 3 * kKeys * 2 + p.row0 * MB;
     const bool all = !is_asym(F) || all_needed(k.t0);
     uint32_t to[P::OUT];
 #pragma unroll
@@ -514,6 +551,7 @@ struct Producer {
             if (KVARN) sg[u] = lds_pair(meta + (2 * kKeys + i * P::STEP) * 2);
           }
         }
+        if constexpr (is_block(F)) sc[u] = lds_word(meta + i * P::STEP * MB);  // 0 for a row that no one sees
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -567,6 +605,8 @@ struct Producer {
       case INT8: return convert<INT8, false, IS_V>(k, slot, dst);
       case E4M3: return convert<E4M3, false, IS_V>(k, slot, dst);
       case E5M2: return convert<E5M2, false, IS_V>(k, slot, dst);
+      case INT8B: return convert<INT8B, false, IS_V>(k, slot, dst);
+      case E4M3B: return convert<E4M3B, false, IS_V>(k, slot, dst);
       case INT4A:
         return s.fields == 3 ? convert<INT4A, true, IS_V>(k, slot, dst) : convert<INT4A, false, IS_V>(k, slot, dst);
       case UINT8A:
@@ -773,7 +813,10 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
       const int off = t & (bs - 1);
       const uint8_t* row = s.codes + static_cast<size_t>(blk) * s.page_bytes + static_cast<size_t>(off) * s.token_bytes;
       __half sc{}, zp{}, sg{};
-      if (s.fields > 0) {
+      float ps = 0.f;
+      if (is_block(s.fmt)) {
+        ps = reinterpret_cast<const float*>(s.meta)[static_cast<size_t>(blk) * s.meta_page];
+      } else if (s.fields > 0) {
         const __half* m = s.meta + static_cast<size_t>(blk) * s.meta_page + off;
         sc = m[0];
         zp = m[bs];
@@ -789,6 +832,10 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
           v = static_cast<uint32_t>(row[d]) << 8;
         } else if (s.fmt == E4M3) {
           v = e4m3x2_to_f16x2(row[d]) & 0xFFFFu;
+        } else if (is_block(s.fmt)) {  // as dequantize16
+          const float c = s.fmt == INT8B ? static_cast<float>(static_cast<int8_t>(row[d]))
+                                         : __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_to_f16x2(row[d]))));
+          v = __half_as_ushort(__float2half_rn(c * ps));
         } else if (s.fields > 0) {
           const int c = s.fmt == INT4A ? (row[d / 2] >> (4 * (d & 1))) & 15 : row[d];
           __half x = __hfma(__int2half_rn(c), sc, zp);  // as dequantize16
@@ -1293,6 +1340,7 @@ __device__ __forceinline__ bool stage_tile(const PrefillArgs& a, const Source& s
       o[3] = w.w;
     } else {
       uint32_t f[3] = {0, 0, 0};
+      if (is_block(F) && need) f[0] = __float_as_uint(reinterpret_cast<const float*>(s.meta)[blk * s.meta_page]);
       if (is_asym(F) && need) {
         const __half* m = s.meta + blk * s.meta_page + (row & mask);
 #pragma unroll
@@ -1324,6 +1372,8 @@ __device__ __forceinline__ bool stage_any(const PrefillArgs& a, const Source& s,
     case INT8: return stage_tile<D, INT8, false, IS_V>(a, s, span, pages, t0, dst, tid);
     case E4M3: return stage_tile<D, E4M3, false, IS_V>(a, s, span, pages, t0, dst, tid);
     case E5M2: return stage_tile<D, E5M2, false, IS_V>(a, s, span, pages, t0, dst, tid);
+    case INT8B: return stage_tile<D, INT8B, false, IS_V>(a, s, span, pages, t0, dst, tid);
+    case E4M3B: return stage_tile<D, E4M3B, false, IS_V>(a, s, span, pages, t0, dst, tid);
     case INT4A:
       return s.fields == 3 ? stage_tile<D, INT4A, true, IS_V>(a, s, span, pages, t0, dst, tid)
                            : stage_tile<D, INT4A, false, IS_V>(a, s, span, pages, t0, dst, tid);

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import blocks as B
 from quantized_paged_kv_kvq_gb300 import kvq
 
 from block_testing import PAIRS, Blocked
@@ -306,3 +307,115 @@ def test_a_captured_step_grows_its_pages_at_every_replay():
         # the element bound alone: new values of size 27 put |out| at some units, whose rounding
         # to bf16 is off by |out| 2^-10 on average (a quarter step), past a mean of 2e-3
         assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+
+
+# ---- chunk attention -------------------------------------------------------------
+def check_chunks(p, counts, g, window=0, sinks=0):
+    cu = np.concatenate([[0], np.cumsum(counts)])
+    q = random_query(int(cu[-1]), p.hkv * g, p.d)
+    ref, tol = p.expect(q, cu, p.d ** -0.5, window, sinks, key=2.0 ** -11)
+    most = int(np.max(counts, initial=0))
+    ws = garbage(kvq.kvq_prefill_workspace_size(p.cache, len(p.lens), q.shape[1], q.shape[0], most, p.max_len))
+    out = torch.full_like(q, 7.0)
+    kvq.kvq_paged_prefill(p.cache, q, out, ints(cu), p.block_table, p.context_lens, most, p.max_len, p.d ** -0.5, window, sinks, ws)
+    check_close(out, ref, tol)
+    assert kvq.kvq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("pair", sorted(PAIRS))
+@pytest.mark.parametrize("hkv,g,d,bs", [(2, 4, 128, 16), (2, 3, 64, 8), (1, 8, 128, 128), (5, 1, 64, 32), (3, 2, 64, 64)])
+def test_chunks(pair, hkv, g, d, bs):
+    """Prompts from nothing, chunks behind cached tokens, single tokens, no tokens."""
+    p = Blocked(pair, [40, 130, 1, 300, 200, 0, 129], hkv, d, bs)
+    p.fill()
+    check_chunks(p, [40, 7, 1, 1, 70, 0, 128], g)
+    check_chunks(p, [40, 7, 1, 9, 70, 0, 12], g, 50, 20)
+
+
+@pytest.mark.parametrize("pair", ["int8", "e4m3"])
+def test_chunks_dequantized_ahead_and_keys_in_parts(pair):
+    p = Blocked(pair, [620, 700], 2, 128, 16)
+    p.fill()
+    check_chunks(p, [600, 500], 4)
+    check_chunks(p, [600, 500], 8, 100, 20)
+    p = Blocked(pair, [3000], 1, 64, 8)
+    p.fill()
+    check_chunks(p, [3], 8)
+
+
+def test_chunks_with_values_that_are_not_finite():
+    """A NaN value, an infinite scale: the rows that see them and no others."""
+    for rows in (100, 600):  # dequantized by each CTA, and ahead
+        p = Blocked("e4m3", [rows], 2, 64, 8)
+        p.fill()
+        blk, off = p.table[0, 60 // 8], 60 % 8
+        p.cache.v_cache[blk, off, 0, 9] = 0x7F
+        p.cache.v_meta[p.table[0, 80 // 8], 1] = float("inf")
+        cu = ints([0, rows])
+        q, out = random_query(rows, 4, 64), torch.empty((rows, 4, 64), dtype=torch.bfloat16, device=DEV)
+        ws = garbage(kvq.kvq_prefill_workspace_size(p.cache, 1, 4, rows, rows, rows))
+        kvq.kvq_paged_prefill(p.cache, q, out, cu, p.block_table, p.context_lens, rows, rows, 0.125, 0, 0, ws)
+        good = torch.isfinite(out)
+        assert good[:60].all() and good[60:, :2, :9].all() and good[60:, :2, 10:].all() and not good[60:, :2, 9].any()
+        assert good[:80, 2:].all() and not good[88:, 2:].any(-1).any()
+
+
+# ---- the operators together ------------------------------------------------------
+@pytest.mark.parametrize("pair,bs", [("e4m3", 16), ("int8", 32)])
+def test_a_serving_loop(pair, bs):
+    """Prompts attend in 16 bits while they are stored; further chunks and single tokens attend to
+    the pages; what was stored is read back.  Nothing comes back to the host in between."""
+    hq, hkv, d, nb = 8, 2, 64, 60
+    p = Blocked(pair, [0, 0, 0], hkv, d, bs)
+    p.nb, p.cache = nb, kvq.alloc_kv_cache(p.k_fmt, p.v_fmt, nb, bs, hkv, d, device=DEV, fill=0xFF)
+    p.kc, p.vc = (np.full((nb, bs, hkv, d), 0xFF, np.uint8) for _ in range(2))
+    p.ks, p.vs = (np.full((nb, 4), 0xFFFFFFFF, np.uint32).view(np.float32) for _ in range(2))
+    rope_table = torch.empty((512, d // 2, 2), device=DEV)
+    kvq.kvq_rope_table(rope_table, 10000.0)
+    rope = kvq.Rope(rope_table)
+    lens, rng = ints([0, 0, 0]), ints([0, nb])
+    table, free = torch.full((3, 20), -1, dtype=torch.int32, device=DEV), ints(np.random.default_rng(0).permutation(nb))
+    new_lens, total = torch.empty(3, dtype=torch.int32, device=DEV), 0
+    for step, new in enumerate(([130, 7, 64], [1, 40, 0], [1, 1, 1], [1, 1, 1], [3, 0, 200])):
+        n = sum(new) + 5
+        new_lens.copy_(ints(new))
+        slots, pos = torch.empty(n, dtype=torch.int64, device=DEV), torch.empty(n, dtype=torch.int32, device=DEV)
+        after, cu, rest = torch.empty_like(lens), torch.empty(4, dtype=torch.int32, device=DEV), torch.empty_like(rng)
+        kvq.kvq_plan_step(lens, new_lens, table, free, rng, bs, nb, slots, pos, after, cu, rest)
+        qkv = random_query(n, hq + 2 * hkv, d, seed=step)
+        qkv = (qkv.float() * 1.5 ** step).to(torch.bfloat16)
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+        kvq.kvq_norm_rope(rope, q, k, pos, q, k)
+        out = torch.full((n, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+        query = q.contiguous()
+        if step == 0:
+            kvq.kvq_prompt_attention(q, k, v, out, cu, 130, d ** -0.5)
+            kvq.kvq_write_cache(p.cache, k, v, slots)
+        elif max(new) == 1:
+            ws = garbage(kvq.kvq_decode_workspace_size(p.cache, 3, hq, 320))
+            kvq.kvq_decode_append(p.cache, k[:3], v[:3], query[:3], out[:3], table, after, 320, d ** -0.5, ws)
+        else:
+            kvq.kvq_write_cache(p.cache, k, v, slots)
+            ws = garbage(kvq.kvq_prefill_workspace_size(p.cache, 3, hq, n, max(new), 320))
+            kvq.kvq_paged_prefill(p.cache, query, out, cu, table, after, max(new), 320, d ** -0.5, 0, 0, ws)
+        lens, rng = after, rest
+        # the oracle, from the same rotated rows
+        p.table, p.lens, at = table.cpu().numpy(), after.cpu().numpy(), cu.tolist()
+        p.record(k, v, slots.cpu().numpy())
+        p.same()
+        if step == 0:
+            for s in range(3):
+                a, b = at[s], at[s + 1]
+                ref, tol = B.attention(*(x[a:b].double().cpu().numpy() for x in (query, k, v)), d ** -0.5)
+                assert (np.abs(out[a:b].double().cpu().numpy() - ref) <= tol).all()
+        else:
+            ref, tol = p.expect(query, at, d ** -0.5, key=2.0 ** -11)
+            assert (np.abs(out.double().cpu().numpy() - ref) <= tol)[:at[-1]].all()
+        assert (out[at[-1]:] == 7).all()
+    assert kvq.kvq_get_device_error() == 0
+    for s in range(3):
+        n = int(p.lens[s])
+        ko, vo = (torch.empty((n, hkv, d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        kvq.kvq_read_cache(p.cache, ints(p.slots(s, np.arange(n)), torch.int64), ko, vo)
+        for got, want in zip((ko, vo), p.sequence(s, n)):
+            assert (np.abs(got.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -8) + 1e-30).all()
