@@ -97,12 +97,14 @@ constexpr int kTileScaleBytes = 128;
 // D bf16, filled ahead of each segment) and, with KVarN, a float row for the
 // query rotation; per stage a tile header and two mbarriers; a scratch area
 // with the producer's cursor and the abort flag; block formats' tile scales; and 1 KB of
-// alignment.
+// alignment.  Block formats rely on the window's declared alignment instead (and look whether
+// it holds): with 8 query heads of 128 a kv-head that 1 KB would leave room for one CTA per
+// SM (146 us for 12 x 4,096..32,768 tokens and 64 / 8 heads of 128 in e4m3, against 91).
 __host__ __device__ constexpr int q_rows_bytes(int g, int d) { return (g * d * 2 + 15) / 16 * 16; }
 template <class C>
 __host__ __device__ constexpr int decode_smem_bytes(int hpc, int g) {
   return C::STAGES * C::stage_bytes(hpc) + hpc * q_rows_bytes(g, C::D) + (C::KVARN_ ? hpc * C::D * 4 : 0) +
-         C::STAGES * (48 + (C::BLOCK ? kTileScaleBytes : 0)) + 256 + 1024;
+         C::STAGES * (48 + (C::BLOCK ? kTileScaleBytes : 0)) + 256 + (C::BLOCK ? 0 : 1024);
 }
 
 // Row of mma row r (0..15) of a tile: the QK row r holds token kRow[r].  With
@@ -823,6 +825,10 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t base_s = (raw_s + 1023u) & ~1023u;  // the window is padded by 1 KB
   uint8_t* smem = smem_raw + (base_s - raw_s);
+  if (C::BLOCK && base_s != raw_s) {  // there is no room to align by: nothing is computed
+    if (threadIdx.x == 0) raise_error(16u);
+    return;
+  }
 
   const int k = blockIdx.x, NC = gridDim.x, hg = blockIdx.y, HG = gridDim.y;
   const int hpc = a.heads_per_cta;

@@ -9,7 +9,16 @@
 // Mapping: a thread makes 16 consecutive elements of a row (32 bytes, two stores);
 // a token's rows of all heads lie behind each other in the cache and in the output,
 // so consecutive threads read and write whole lines.  K and V are one launch (grid.y).
-// Bound by HBM: D codes read and 2 D bytes written per row.
+// Bound by HBM: D codes read and 2 D bytes written per row (65,536 tokens, 8 heads of 128:
+// int8 per page 65 us, 6.2 TB/s; int4 64 us, 5.3).
+//
+// KVarN: H applies to the codes first, H (code * scale + zero) = scale H code + zero D e_0,
+// which are whole numbers and so exact in the tensor cores.  Of the log2 D bits of an
+// element's number, a warp's mma.sync m16n8k16 (16 rows by 16 x 8 of +-1, twice) turns four
+// and butterflies within a thread the rest: no value goes from lane to lane.  Codes
+// enter as 1024 + code, whose part 1024 D comes off element 0.
+#include <algorithm>
+
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 #include "mbarrier.cuh"
@@ -65,94 +74,206 @@ __device__ __forceinline__ void codes16(const uint8_t* p, float (&x)[16]) {
   }
 }
 
-template <int D, int F, bool KVARN>
+template <int D, int F>
 __device__ __forceinline__ void read_rows(const ReadArgs& a, int which) {
   constexpr int P = D / 16, RB = row_bytes(F, D);  // threads and bytes of a row
   const int Hkv = a.num_kv_heads, per_token = Hkv * P;
   const int64_t total = a.num_tokens * per_token, stride = static_cast<int64_t>(gridDim.x) * kThreads;
   const uint8_t* const codes = a.codes[which];
   const int shift = a.block_shift, mask = (1 << shift) - 1;
-  // whole warps take part in every turn: KVarN's lanes exchange values
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads; i0 < total; i0 += stride) {
-    const int64_t i = i0 + threadIdx.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += stride) {
     const int64_t t = i / per_token;
     const int in_token = static_cast<int>(i - t * per_token), h = in_token / P, part = in_token % P;
-    const int64_t slot = i < total ? a.slot_mapping[t] : -1;
-    bool read = slot >= 0;
-    if (read && (slot >> shift) >= a.num_blocks) {
+    const int64_t slot = a.slot_mapping[t];
+    if (slot < 0) continue;
+    if ((slot >> shift) >= a.num_blocks) {
       if (which == 0) raise_error(1u);  // KVQ_DEVERR_SLOT_RANGE
-      read = false;
+      continue;
     }
     float x[16];
+    const int64_t blk = slot >> shift;
+    const int off = static_cast<int>(slot) & mask;
+    codes16<code_fmt(F)>(codes + (static_cast<size_t>(slot) * Hkv + h) * RB + part * (RB / P), x);
+    if constexpr (is_asym(F)) {
+      const __half* m = static_cast<const __half*>(a.meta[which]) + ((blk * Hkv + h) * 2 << shift) + off;
+      const float s = __half2float(m[0]), z = __half2float(m[1 << shift]);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.f;
-    if (read) {
-      const int64_t blk = slot >> shift;
-      const int off = static_cast<int>(slot) & mask;
-      codes16<code_fmt(F)>(codes + (static_cast<size_t>(slot) * Hkv + h) * RB + part * (RB / P), x);
-      if constexpr (is_asym(F)) {
-        constexpr int NF = KVARN ? 3 : 2;
-        const __half* m = static_cast<const __half*>(a.meta[which]) + ((blk * Hkv + h) * NF << shift) + off;
-        const float s = __half2float(m[0]), z = __half2float(m[1 << shift]);
-        const float g = KVARN ? __half2float(m[2 << shift]) : 1.f;
+      for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], s, z);
+    } else if constexpr (F != BF16) {
+      const float s = is_block(F) ? static_cast<const float*>(a.meta[which])[blk * scale_pitch(Hkv) + h]
+                      : a.head_scale[which] != nullptr ? a.head_scale[which][h] : a.scale[which];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = KVARN ? fmaf(x[e], s, z) * g : fmaf(x[e], s, z);
-      } else if constexpr (F != BF16) {
-        const float s = is_block(F) ? static_cast<const float*>(a.meta[which])[blk * scale_pitch(Hkv) + h]
-                        : a.head_scale[which] != nullptr ? a.head_scale[which][h] : a.scale[which];
+      for (int e = 0; e < 16; ++e) x[e] *= s;
+    }
+    uint4* const to = reinterpret_cast<uint4*>(a.out[which] + t * a.out_stride[which] + h * D + part * 16);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] *= s;
+    for (int k = 0; k < 2; ++k)
+      to[k] = make_uint4(pack_bf162(x[8 * k], x[8 * k + 1]), pack_bf162(x[8 * k + 2], x[8 * k + 3]),
+                         pack_bf162(x[8 * k + 4], x[8 * k + 5]), pack_bf162(x[8 * k + 6], x[8 * k + 7]));
+  }
+}
+
+// Rotated rows: a warp takes 16 consecutive tokens of a kv-head (rows g and g + 8 to lanes
+// (g, c), which hold the D / 4 consecutive elements from c D / 4 on).  The bits of an
+// element's number within a lane: two are the k-slots' (uint8: b0, b1 of 4 consecutive
+// codes; int4: b2, b0, as a mask takes nibbles 4 apart out of a word together), the others
+// number the products j; c is the k-slots' other two.
+template <int D, int F>
+__device__ __forceinline__ void read_rotated(const ReadArgs& a, int which) {
+  constexpr int E = D / 4, J = E / 4, W = E * (F == INT4A ? 4 : 8) / 32;  // elements, products and words of a lane's row
+  constexpr uint32_t K64 = 0x64646464u;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int Hkv = a.num_kv_heads, shift = a.block_shift, mask = (1 << shift) - 1;
+  const int64_t warps = (a.num_tokens + 15) / 16 * Hkv;
+  // B: +-1 of (k-slot (c, s), column (c', s')), c' = column / 2, s' = column % 2 + 2 t
+  uint32_t b[2][2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      auto one = [&](int i) {
+        return (__popc(c & (g >> 1)) + __popc((i + 2 * q) & ((g & 1) + 2 * t))) & 1 ? 0xBC00u : 0x3C00u;
+      };
+      b[t][q] = one(0) | one(1) << 16;
+    }
+  uint32_t flips = 0;  // the diagonal's signs of this lane's elements
+  if (a.signs != nullptr) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) flips |= (a.signs[c * E + e] < 0 ? 1u : 0u) << e;
+  }
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); w < warps;
+       w += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
+    const int64_t tile = w / Hkv;
+    const int h = static_cast<int>(w - tile * Hkv);
+    uint32_t code[2][W];
+    float scale[2], zero[2];
+    bool read[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int64_t t = tile * 16 + g + 8 * r, slot = t < a.num_tokens ? a.slot_mapping[t] : -1;
+      read[r] = slot >= 0;
+      if (read[r] && (slot >> shift) >= a.num_blocks) {
+        if (which == 0) raise_error(1u);  // KVQ_DEVERR_SLOT_RANGE
+        read[r] = false;
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) code[r][i] = 0;
+      scale[r] = zero[r] = 0.f;
+      if (read[r]) {
+        const uint8_t* p = a.codes[which] + (static_cast<size_t>(slot) * Hkv + h) * row_bytes(F, D) + c * (4 * W);
+        if constexpr (W >= 4) {
+#pragma unroll
+          for (int i = 0; i < W; i += 4) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(p + 4 * i));
+            code[r][i] = x.x;
+            code[r][i + 1] = x.y;
+            code[r][i + 2] = x.z;
+            code[r][i + 3] = x.w;
+          }
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+          code[r][0] = x.x;
+          code[r][1] = x.y;
+        }
+        const __half* m = static_cast<const __half*>(a.meta[which]) + (((slot >> shift) * Hkv + h) * 3 << shift) + (slot & mask);
+        const float f = __half2float(__ldg(m + (2 << shift))) * a.cR;
+        scale[r] = __half2float(__ldg(m)) * f;
+        zero[r] = __half2float(__ldg(m + (1 << shift))) * f;
       }
     }
-    if constexpr (KVARN) {
-      fwht_lanes<16, P>(x, part);
+    float v[2][J][4];  // [row][j][s']
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] *= a.cR;
-        if (a.signs != nullptr && a.signs[part * 16 + e] < 0) x[e] = -x[e];
+    for (int j = 0; j < J; ++j) {
+      uint32_t x[2][2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if constexpr (F == INT4A) {
+          const uint32_t n = code[r][j >> 1] >> (8 * (j & 1));  // nibbles 2 (j & 1), and that + 1
+          x[r][0] = and_or(n, 0x000F000Fu, 0x64006400u);
+          x[r][1] = and_or(n >> 4, 0x000F000Fu, 0x64006400u);
+        } else {
+          x[r][0] = prmt(code[r][j], K64, 0x4140);
+          x[r][1] = prmt(code[r][j], K64, 0x4342);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(d, x[0][0], x[1][0], x[0][1], x[1][1], b[t][0], b[t][1]);
+        v[0][j][2 * t] = d[0];
+        v[0][j][2 * t + 1] = d[1];
+        v[1][j][2 * t] = d[2];
+        v[1][j][2 * t + 1] = d[3];
       }
     }
-    if (read) {
-      uint4* const to = reinterpret_cast<uint4*>(a.out[which] + t * a.out_stride[which] + h * D + part * 16);
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        to[k] = make_uint4(pack_bf162(x[8 * k], x[8 * k + 1]), pack_bf162(x[8 * k + 2], x[8 * k + 3]),
-                           pack_bf162(x[8 * k + 4], x[8 * k + 5]), pack_bf162(x[8 * k + 6], x[8 * k + 7]));
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int bit = 1; bit < J; bit <<= 1)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if ((j & bit) == 0)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const float p = v[r][j][e], q = v[r][j][e + 1], y = v[r][j + bit][e], z = v[r][j + bit][e + 1];
+              add2(v[r][j][e], v[r][j][e + 1], p, q, y, z);
+              sub2(v[r][j + bit][e], v[r][j + bit][e + 1], p, q, y, z);
+            }
+      if (c == 0) v[r][0][0] -= 1024.f * D;
+      const float at0 = c == 0 ? zero[r] * D : 0.f;
+      // in the order of the elements
+      float y[E];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int e = F == INT4A ? (s >> 1) + 2 * (j & 1) + 4 * (s & 1) + 8 * (j >> 1) : 4 * j + s;
+          const float x = fmaf(v[r][j][s], scale[r], e == 0 ? at0 : 0.f);
+          y[e] = flips >> e & 1 ? -x : x;
+        }
+      if (read[r]) {
+        uint4* const to = reinterpret_cast<uint4*>(a.out[which] + (tile * 16 + g + 8 * r) * a.out_stride[which] + h * D + c * E);
+#pragma unroll
+        for (int k = 0; k < E / 8; ++k)
+          to[k] = make_uint4(pack_bf162(y[8 * k], y[8 * k + 1]), pack_bf162(y[8 * k + 2], y[8 * k + 3]),
+                             pack_bf162(y[8 * k + 4], y[8 * k + 5]), pack_bf162(y[8 * k + 6], y[8 * k + 7]));
+      }
     }
   }
 }
 
-template <int D, bool KVARN>
+template <int D>
 __global__ void __launch_bounds__(kThreads) read_cache_kernel(const ReadArgs a) {
   const int which = blockIdx.y;
-  if constexpr (KVARN) {
-    if (a.fmt[which] == INT4A) read_rows<D, INT4A, true>(a, which);
-    else read_rows<D, UINT8A, true>(a, which);
-  } else {
-    switch (a.fmt[which]) {
-      case INT8: read_rows<D, INT8, false>(a, which); break;
-      case E4M3: read_rows<D, E4M3, false>(a, which); break;
-      case E5M2: read_rows<D, E5M2, false>(a, which); break;
-      case INT4A: read_rows<D, INT4A, false>(a, which); break;
-      case UINT8A: read_rows<D, UINT8A, false>(a, which); break;
-      case INT8B: read_rows<D, INT8B, false>(a, which); break;
-      case E4M3B: read_rows<D, E4M3B, false>(a, which); break;
-      default: read_rows<D, BF16, false>(a, which); break;
-    }
+  switch (a.fmt[which]) {
+    case INT8: read_rows<D, INT8>(a, which); break;
+    case E4M3: read_rows<D, E4M3>(a, which); break;
+    case E5M2: read_rows<D, E5M2>(a, which); break;
+    case INT4A: read_rows<D, INT4A>(a, which); break;
+    case UINT8A: read_rows<D, UINT8A>(a, which); break;
+    case INT8B: read_rows<D, INT8B>(a, which); break;
+    case E4M3B: read_rows<D, E4M3B>(a, which); break;
+    default: read_rows<D, BF16>(a, which); break;
   }
+}
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) read_rotated_kernel(const ReadArgs a) {
+  const int which = blockIdx.y;
+  if (a.fmt[which] == INT4A) read_rotated<D, INT4A>(a, which);
+  else read_rotated<D, UINT8A>(a, which);
 }
 
 }  // namespace
 
 cudaError_t launch_read(const ReadArgs& a, int head_dim, bool kvarn, cudaStream_t st, int num_sms) {
-  const int64_t threads = a.num_tokens * a.num_kv_heads * (head_dim / 16);
-  const int64_t ctas = (threads + kThreads - 1) / kThreads;
-  const dim3 grid(static_cast<unsigned>(ctas < 8ll * num_sms ? ctas : 8ll * num_sms), 2, 1);
-  if (head_dim == 64 && kvarn) read_cache_kernel<64, true><<<grid, kThreads, 0, st>>>(a);
-  else if (head_dim == 64) read_cache_kernel<64, false><<<grid, kThreads, 0, st>>>(a);
-  else if (head_dim == 128 && kvarn) read_cache_kernel<128, true><<<grid, kThreads, 0, st>>>(a);
-  else if (head_dim == 128) read_cache_kernel<128, false><<<grid, kThreads, 0, st>>>(a);
-  else return cudaErrorNotSupported;
+  if (head_dim != 64 && head_dim != 128) return cudaErrorNotSupported;
+  const int64_t ctas = kvarn ? ((a.num_tokens + 15) / 16 * a.num_kv_heads + kThreads / 32 - 1) / (kThreads / 32)
+                             : (a.num_tokens * a.num_kv_heads * (head_dim / 16) + kThreads - 1) / kThreads;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ctas, 8ll * num_sms)), 2, 1);
+  if (kvarn && head_dim == 64) read_rotated_kernel<64><<<grid, kThreads, 0, st>>>(a);
+  else if (kvarn) read_rotated_kernel<128><<<grid, kThreads, 0, st>>>(a);
+  else if (head_dim == 64) read_cache_kernel<64><<<grid, kThreads, 0, st>>>(a);
+  else read_cache_kernel<128><<<grid, kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 

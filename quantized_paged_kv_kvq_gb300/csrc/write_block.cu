@@ -19,7 +19,9 @@
 // share a CTA.  A CTA looks for the runs that begin among its `step` tokens by
 // comparing each token's page with that of the token before it, so the slots alone say
 // where runs begin and end: no search over sequences, no atomics.  step grows with the
-// call from 1 (a decode step: every request's run starts at once) to a page.
+// call from 1 (a decode step: every request's run starts at once) to a page.  A thread a
+// token, the CTA loads the places of the tokens around its own and marks, a bit each, which
+// are there and which begin a run: the warps then only read bits.
 // Bound by HBM: 4 D bytes read and 2 D written per token and head.
 #include <algorithm>
 
@@ -36,7 +38,27 @@ namespace {
 constexpr int kWarps = 8;
 constexpr float kSmallest = 1.17549435e-38f;  // 2^-126: 1 / scale stays finite
 
+constexpr int kBack = 32;  // tokens before its own whose places a CTA keeps, too
+
 __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
+
+// (c << 16) | (sat(a) << 8) | sat(b), sat = clamp to [-128, 127]
+__device__ __forceinline__ uint32_t pack_sat_s8(int a, int b, uint32_t c) {
+  uint32_t d;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// Four bf16 values times inv as code bytes (as quantize_store makes them).
+template <int F>
+__device__ __forceinline__ uint32_t quantize4(uint32_t lo, uint32_t hi, float inv) {
+  float a, b, c, d;
+  mul2(a, b, bf16_lo(lo), bf16_hi(lo), inv, inv);
+  mul2(c, d, bf16_lo(hi), bf16_hi(hi), inv, inv);
+  if constexpr (F == INT8)
+    return pack_sat_s8(__float2int_rn(b), __float2int_rn(a), pack_sat_s8(__float2int_rn(d), __float2int_rn(c), 0u));
+  else
+    return f32x2_to_fp8x2<E4M3>(a, b) | f32x2_to_fp8x2<E4M3>(c, d) << 16;
+}
 
 // Code bytes times 2^-k (f), rounded again.
 template <int F>
@@ -60,10 +82,15 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 }
 
 template <int D, int CH>  // head_dim, warps per run and head
-__global__ void __launch_bounds__(kWarps * 32) write_block_kernel(const WriteArgs a, const AppendSlots ap, int kf, int vf, int step) {
+__global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_kernel(const WriteArgs a, const AppendSlots ap, int kf, int vf, int step) {
   constexpr int LPR = RowGeom<D>::LPR, RPI = RowGeom<D>::RPI, NP = 16 / RPI;
   constexpr unsigned kAll = 0xffffffffu;
+  constexpr int kNear = (CH <= 2 ? 1 : 2) * kWarps * 32;  // tokens whose places the CTA keeps
   __shared__ uint32_t most[2][kWarps];
+  __shared__ int front[2][kWarps];
+  __shared__ uint32_t is_there[kNear / 32], begins[kNear / 32];
+  __shared__ int near_page[kNear];
+  __shared__ uint8_t near_off[kNear];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LPR, grp = lane / LPR, chunk = warp % CH;
   const int Hkv = a.num_kv_heads, bs = a.block_size;
@@ -77,8 +104,8 @@ __global__ void __launch_bounds__(kWarps * 32) write_block_kernel(const WriteArg
   const int pitch = scale_pitch(Hkv);
   const uint16_t* const rows = (is_v ? a.value : a.key) + static_cast<size_t>(active ? h : 0) * D + sub * 8;
   const int64_t stride = is_v ? a.value_stride : a.key_stride;
-  const int64_t n = a.num_tokens, t_end = min(n, (static_cast<int64_t>(blockIdx.x) + 1) * step);
-  const bool reports = blockIdx.y == 0 && warp == 0;
+  const int64_t n = a.num_tokens, t_begin = static_cast<int64_t>(blockIdx.x) * step, t_end = min(n, t_begin + step);
+  const int64_t near0 = t_begin - kBack;
   int parity = 0;
 
   // Page and offset of token t: page -1 if it is skipped.
@@ -101,25 +128,60 @@ __global__ void __launch_bounds__(kWarps * 32) write_block_kernel(const WriteArg
     return p;
   };
 
-  // The run of `len` tokens from t0 on in `page`, the foremost of them at offset `first`.
-  auto store_run = [&](int page, int64_t t0, int64_t len, int first) {
+  // Its tokens' rows on their way into L2 meanwhile: the rows of this warp's share of the heads.
+  for (int64_t r = t_begin + chunk * (32 / (D / 64)) + lane / (D / 64); active && r < t_end; r += CH * (32 / (D / 64)))
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(rows - sub * 8 + r * stride + lane % (D / 64) * 64));
+  // The places of the tokens from kBack before this CTA's first one on (those behind: looked up
+  // when they are asked for).
+  for (int i = threadIdx.x; i < kNear; i += kWarps * 32) {
+    const int64_t t = near0 + i;
+    const bool own = t >= t_begin && t < t_end;
+    const int2 p = t >= 0 && t < n && (own || !append) ? place(t, blockIdx.y == 0 && own) : make_int2(-1, 0);
+    near_page[i] = p.x;
+    near_off[i] = static_cast<uint8_t>(p.y);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kNear; i += kWarps * 32) {
+    const int page = near_page[i];
+    int before = -1;  // page of the last token before it, at most kBack back
+    if (page >= 0 && !append && i >= kBack)
+      for (int d = 1; d <= kBack && before < 0; ++d) before = near_page[i - d];
+    const uint32_t there = __ballot_sync(kAll, page >= 0), first = __ballot_sync(kAll, page >= 0 && i >= kBack && page != before);
+    if (lane == 0) {
+      is_there[i / 32] = there;
+      begins[i / 32] = first;
+    }
+  }
+  __syncthreads();
+  auto place_of = [&](int64_t t) {  // (-1, 0) outside the call
+    const int64_t i = t - near0;
+    if (i >= 0 && i < kNear) return make_int2(near_page[i], near_off[i]);
+    return t >= 0 && t < n ? place(t, false) : make_int2(-1, 0);
+  };
+
+  // The run of `len` tokens from t0 on in `page` (skipped ones among them).
+  auto store_run = [&](int page, int64_t t0, int64_t len) {
     float* const scale_at = scales + static_cast<size_t>(page) * pitch + h;
-    const float old = active && first > 0 ? *scale_at : 0.0f;
+    const float was = active ? *scale_at : 0.0f;  // means nothing where the page is begun
     uint4 v[NP];
     uint32_t m2 = 0;
-    int off[NP];  // of the rows, -1: not this thread's, or skipped
+    int first = bs;  // the foremost offset
+    const uint16_t* const row0 = rows + t0 * stride;
+    uint32_t off[(NP + 3) / 4];  // offsets of the rows, a byte each, 255: not this thread's, or skipped
     auto load = [&](int64_t r0) {  // rows r0 .. r0 + 15 of the run
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const int64_t r = r0 + i * RPI + grp;
         const bool read = active && r < len;
-        v[i] = read ? ldg_stream16(rows + (t0 + r) * stride) : make_uint4(0, 0, 0, 0);
-        const int64_t slot = read && !append ? a.slot_mapping[t0 + r] : -1;
-        off[i] = append && read ? first : (slot >> a.block_shift) == page ? static_cast<int>(slot) & (bs - 1) : -1;
+        v[i] = read ? ldg_stream16(row0 + r * stride) : make_uint4(0, 0, 0, 0);
+        const int2 p = read ? place_of(t0 + r) : make_int2(-1, 0);
+        const uint32_t o = p.x == page && read ? p.y : 255u;
+        off[i / 4] = (i % 4 ? off[i / 4] : 0u) | o << (8 * (i % 4));
+        first = min(first, static_cast<int>(o));
       }
 #pragma unroll
       for (int i = 0; i < NP; ++i)
-        if (off[i] < 0) v[i] = make_uint4(0, 0, 0, 0);
+        if ((off[i / 4] >> (8 * (i % 4)) & 255u) == 255u) v[i] = make_uint4(0, 0, 0, 0);
     };
     auto take_max = [&]() {
       uint32_t x = 0;
@@ -148,13 +210,21 @@ __global__ void __launch_bounds__(kWarps * 32) write_block_kernel(const WriteArg
     load(16 * chunk);
     take_max();
     uint32_t m = __reduce_max_sync(kAll, max(m2 & 0xFFFFu, m2 >> 16));
+    first = __reduce_min_sync(kAll, first);
     if constexpr (CH > 1) {
-      if (lane == 0) most[parity][warp] = m;
+      if (lane == 0) {
+        most[parity][warp] = m;
+        front[parity][warp] = first;
+      }
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < CH; ++i) m = max(m, most[parity][warp / CH * CH + i]);
+      for (int i = 0; i < CH; ++i) {
+        m = max(m, most[parity][warp / CH * CH + i]);
+        first = min(first, front[parity][warp / CH * CH + i]);
+      }
       parity ^= 1;
     }
+    const float old = first > 0 ? was : 0.0f;
     const float top = __uint_as_float(m << 16);
     const float need = m == 0 ? 0.0f : fmaxf(__fdiv_rn(top, int8 ? 127.0f : 448.0f), kSmallest);
     float scale = need;
@@ -186,52 +256,47 @@ __global__ void __launch_bounds__(kWarps * 32) write_block_kernel(const WriteArg
       if (r0 != 16 * chunk) load(r0);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const bool mine = off[i] >= 0;
-        float x[8];
-        unpack8(v[i], x);
-        const size_t row = (page_row + max(off[i], 0)) * Hkv + h;
-        if (int8) quantize_store<D, INT8, false>(x, mine, h, sub, row, codes, nullptr, inv, 0, 0, 0, 0, 0u, 0.f);
-        else quantize_store<D, E4M3, false>(x, mine, h, sub, row, codes, nullptr, inv, 0, 0, 0, 0, 0u, 0.f);
+        const uint32_t o = off[i / 4] >> (8 * (i % 4)) & 255u;
+        uint2 w;
+        if (int8) w = make_uint2(quantize4<INT8>(v[i].x, v[i].y, inv), quantize4<INT8>(v[i].z, v[i].w, inv));
+        else w = make_uint2(quantize4<E4M3>(v[i].x, v[i].y, inv), quantize4<E4M3>(v[i].z, v[i].w, inv));
+        if (o != 255u) *reinterpret_cast<uint2*>(codes + ((page_row + o) * Hkv + h) * D + sub * 8) = w;
       }
     }
   };
 
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * step; base < t_end; base += 32) {
-    const int64_t t = base + lane;
-    const int2 p = t < n ? place(t, reports && t < t_end) : make_int2(-1, 0);
-    unsigned begins = __ballot_sync(kAll, t < t_end && p.x >= 0);
-    if (!append) {  // but not those whose page is that of the last token before them, at most 32 back
-      const int2 q = t >= 32 ? place(t - 32, false) : make_int2(-1, 0);
-      const unsigned here = __ballot_sync(kAll, p.x >= 0) & ((1u << lane) - 1u), there = __ballot_sync(kAll, q.x >= 0);
-      const int from = here != 0 ? 31 - __clz(here) : there != 0 ? 31 - __clz(there) : 0;
-      const int x = __shfl_sync(kAll, p.x, from), y = __shfl_sync(kAll, q.x, from);
-      const int before = here != 0 ? x : from >= lane ? y : -1;
-      begins &= __ballot_sync(kAll, p.x != before);
-    }
-    while (begins != 0) {  // the same in every warp
-      const int src = __ffs(begins) - 1;
-      begins &= begins - 1;
-      const int page = __shfl_sync(kAll, p.x, src);
+  const int own_end = kBack + static_cast<int>(t_end - t_begin);
+  for (int w = kBack / 32; 32 * w < own_end; ++w) {
+    uint32_t starts = begins[w] & (own_end >= 32 * (w + 1) ? kAll : (1u << (own_end & 31)) - 1u);
+    while (starts != 0) {  // the same in every warp
+      const int i0 = 32 * w + __ffs(starts) - 1;
+      starts &= starts - 1;
+      const int page = near_page[i0];
       int64_t len = 1;
-      int first = __shfl_sync(kAll, p.y, src);
       if (!append) {
-        // its tokens up to the first of another page: among these 32, and on while none is 32 apart
-        unsigned other = __ballot_sync(kAll, lane > src && p.x >= 0 && p.x != page);
-        unsigned same = __ballot_sync(kAll, lane >= src && p.x == page) & (other != 0 ? (1u << (__ffs(other) - 1)) - 1u : kAll);
-        first = __reduce_min_sync(kAll, same >> lane & 1 ? p.y : 0x7fffffff);
-        int64_t last = base + 31 - __clz(same);
-        for (int64_t more = base + 32; other == 0 && more < n && more <= last + 32; more += 32) {
-          const int2 q = more + lane < n ? place(more + lane, false) : make_int2(-1, 0);
-          other = __ballot_sync(kAll, q.x >= 0 && q.x != page);
-          same = __ballot_sync(kAll, q.x == page) & (other != 0 ? (1u << (__ffs(other) - 1)) - 1u : kAll);
-          if (same == 0) continue;
-          if (more + __ffs(same) - 1 > last + 32) break;
-          first = min(first, __reduce_min_sync(kAll, same >> lane & 1 ? q.y : 0x7fffffff));
-          last = more + 31 - __clz(same);
+        // to the last token that is there before the next run begins
+        int e = w;
+        uint32_t next = begins[w] & ~((2u << (i0 & 31)) - 1u);
+        while (next == 0 && e + 1 < kNear / 32) next = begins[++e];
+        const int i1 = next != 0 ? 32 * e + __ffs(next) - 1 : kNear;
+        uint32_t there = next != 0 ? is_there[e] & ((1u << (i1 & 31)) - 1u) : is_there[e];
+        while (there == 0) there = is_there[--e];  // i0 itself at the least
+        len = 32 * e + 31 - __clz(there) - i0 + 1;
+        // past what the CTA keeps, while no two of its tokens are more than 32 apart
+        if (i1 == kNear) {
+          int64_t last = near0 + i0 + len - 1;
+          for (int64_t more = near0 + kNear; more < n && more <= last + 32; more += 32) {
+            const int2 q = place_of(more + lane);
+            const unsigned other = __ballot_sync(kAll, q.x >= 0 && q.x != page);
+            const unsigned same = __ballot_sync(kAll, q.x == page) & (other != 0 ? (1u << (__ffs(other) - 1)) - 1u : kAll);
+            if (same != 0 && more + __ffs(same) - 1 <= last + 32) last = more + 31 - __clz(same);
+            else if (same != 0) break;
+            if (other != 0) break;
+          }
+          len = last - (near0 + i0) + 1;
         }
-        len = last - (base + src) + 1;
       }
-      store_run(page, base + src, len, first);
+      store_run(page, near0 + i0, len);
     }
   }
 }
@@ -240,7 +305,7 @@ template <int D, int CH>
 cudaError_t launch_t(const WriteArgs& a, const AppendSlots& s, int kf, int vf, cudaStream_t st, int num_sms) {
   const int y = (2 * a.num_kv_heads * CH + kWarps - 1) / kWarps;
   if (y > 65535) return cudaErrorNotSupported;
-  const int64_t step = std::min<int64_t>(std::max<int64_t>(a.num_tokens * y / (6 * num_sms), 1), a.block_size);
+  const int64_t step = std::min<int64_t>(std::max<int64_t>(a.num_tokens * y / (6 * num_sms), 1), std::max(a.block_size, 32));
   const dim3 grid(static_cast<unsigned>((a.num_tokens + step - 1) / step), y, 1);
   write_block_kernel<D, CH><<<grid, kWarps * 32, 0, st>>>(a, s, kf, vf, static_cast<int>(step));
   return cudaGetLastError();

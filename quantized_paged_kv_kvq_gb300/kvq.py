@@ -180,13 +180,15 @@ class KVCache:
     v_head_scales: Optional[torch.Tensor] = None  # fp32 [num_kv_heads] (symmetric V)
 
     def desc(self) -> _CacheDesc:
-        ptr = lambda t: None if t is None else t.data_ptr()
+        if self.k_fmt in BLOCK or self.v_fmt in BLOCK:
+            _page_scales(self)
+        km, vm, sg, ks, vs = self.k_meta, self.v_meta, self.signs, self.k_head_scales, self.v_head_scales
         return _CacheDesc(FMT[self.k_fmt], FMT[self.v_fmt], self.num_kv_heads, self.head_dim,
                           self.block_size, self.num_blocks,
                           FLAG_VARNORM_ROTATE if self.varnorm_rotate else 0,
-                          float(self.k_scale), float(self.v_scale), ptr(self.k_meta),
-                          ptr(self.v_meta), ptr(self.signs), ptr(self.k_head_scales),
-                          ptr(self.v_head_scales))
+                          float(self.k_scale), float(self.v_scale), None if km is None else km.data_ptr(),
+                          None if vm is None else vm.data_ptr(), None if sg is None else sg.data_ptr(),
+                          None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr())
 
 
 def row_bytes(fmt: str, head_dim: int) -> int:
@@ -202,6 +204,17 @@ def meta_fields(fmt: str, varnorm_rotate: bool) -> int:
 def scale_pitch(num_kv_heads: int) -> int:
     """Entries of a page's row of scales (block formats)."""
     return (num_kv_heads + 3) // 4 * 4
+
+
+def _page_scales(cache: KVCache) -> None:
+    """The scales of a block format's cache are what its description says, on its codes' device."""
+    for name, fmt, m in (("k_meta", cache.k_fmt, cache.k_meta), ("v_meta", cache.v_fmt, cache.v_meta)):
+        if fmt in BLOCK:
+            want = (cache.num_blocks, scale_pitch(cache.num_kv_heads))
+            if (m is None or m.dtype is not torch.float32 or m.dim() != 2 or m.shape[0] < want[0] or m.shape[1] != want[1]
+                    or not m.is_contiguous() or m.get_device() != cache.k_cache.get_device()):
+                raise ValueError(f"{name} must be a contiguous float32 tensor of shape {want} on the codes' device, got "
+                                 + ("None" if m is None else f"{m.dtype} {tuple(m.shape)} with strides {m.stride()} on {m.device}"))
 
 
 def alloc_kv_cache(k_fmt, v_fmt, num_blocks, block_size, num_kv_heads, head_dim,
@@ -243,9 +256,9 @@ def kvq_write_cache(cache: KVCache, key: torch.Tensor, value: torch.Tensor,
     assert slot_mapping.dtype == torch.int64
     t = key.shape[0]
     d = cache.desc()
-    st = lib.kvq_write_cache(ctypes.byref(d), _ptr(cache.k_cache), _ptr(cache.v_cache), _ptr(key),
-                             _ptr(value), key.stride(0), value.stride(0), _ptr(slot_mapping), t,
-                             _stream(stream))
+    st = lib.kvq_write_cache(ctypes.byref(d), cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), key.data_ptr(),
+                             value.data_ptr(), key.stride(0), value.stride(0), slot_mapping.data_ptr(), t,
+                             _raw_stream(_current_device(), stream))
     _check(st, "kvq_write_cache")
 
 
@@ -445,11 +458,6 @@ def _cache_desc(dev: int, cache: KVCache) -> _CacheDesc:
     if c.v_fmt in ASYM:
         _need(c.v_meta is not None, "v_meta is missing: rows of this format have fields")
         _pool(dev, "v_meta", c.v_meta, torch.float16, blocks, hkv, 3 if rot else 2, bs)
-    for name, fmt, m in (("k_meta", c.k_fmt, c.k_meta), ("v_meta", c.v_fmt, c.v_meta)):
-        if fmt in BLOCK:
-            _need(m is not None, f"{name} is missing: pages of this format have scales")
-            _need(m.dim() == 2 and m.shape[0] >= blocks, f"{name} must have a row for each of {blocks} blocks")
-            _tensors(dev, (name, m, torch.float32, (m.shape[0], scale_pitch(hkv))))
     if rot and c.signs is not None:
         _tensors(dev, ("signs", c.signs, torch.int8, (d,)))
     if c.k_head_scales is not None:
