@@ -159,8 +159,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
     return t >= 0 && t < n ? place(t, false) : make_int2(-1, 0);
   };
 
-  // The run of `len` tokens from t0 on in `page` (skipped ones among them).
-  auto store_run = [&](int page, int64_t t0, int64_t len) {
+  // The run of `len` tokens from near0 + i0 on in `page` (skipped ones among them).
+  auto store_run = [&](int page, int i0, int64_t len) {
+    const int64_t t0 = near0 + i0;
     float* const scale_at = scales + static_cast<size_t>(page) * pitch + h;
     const float was = active ? *scale_at : 0.0f;  // means nothing where the page is begun
     uint4 v[NP];
@@ -171,11 +172,18 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
     auto load = [&](int64_t r0) {  // rows r0 .. r0 + 15 of the run
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const int64_t r = r0 + i * RPI + grp;
+        const int64_t r = r0 + grp + i * RPI;
         const bool read = active && r < len;
         v[i] = read ? ldg_stream16(row0 + r * stride) : make_uint4(0, 0, 0, 0);
-        const int2 p = read ? place_of(t0 + r) : make_int2(-1, 0);
-        const uint32_t o = p.x == page && read ? p.y : 255u;
+        uint32_t o = 255u;
+        if (read) {
+          if (i0 + r < kNear) {
+            if (near_page[i0 + static_cast<int>(r)] == page) o = near_off[i0 + static_cast<int>(r)];
+          } else {
+            const int2 p = place_of(t0 + r);
+            if (p.x == page) o = p.y;
+          }
+        }
         off[i / 4] = (i % 4 ? off[i / 4] : 0u) | o << (8 * (i % 4));
         first = min(first, static_cast<int>(o));
       }
@@ -239,12 +247,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
     }
     if (!active) return;
     if (lane == 0 && chunk == 0 && (k > 0 || scale != old || first == 0)) *scale_at = scale;
-    const size_t page_row = static_cast<size_t>(page) * bs;
+    uint8_t* const page_at = codes + (static_cast<size_t>(page) * bs * Hkv + h) * D;  // of the head's first row
+    const int row_step = Hkv * D;  // a row's bytes: checked on the host
     if (k > 0) {  // the rows in front, 16 bytes a lane
       constexpr int LP = D / 16;
       const float f = k < 64 ? __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : 0.0f;
       for (int r = chunk * (32 / LP) + lane / LP; r < first; r += CH * (32 / LP)) {
-        uint4* const at = reinterpret_cast<uint4*>(codes + ((page_row + r) * Hkv + h) * D) + lane % LP;
+        uint4* const at = reinterpret_cast<uint4*>(page_at + static_cast<size_t>(r) * row_step) + lane % LP;
         uint4 w = *at;
         if (int8) w = make_uint4(rescale4<INT8>(w.x, f), rescale4<INT8>(w.y, f), rescale4<INT8>(w.z, f), rescale4<INT8>(w.w, f));
         else w = make_uint4(rescale4<E4M3>(w.x, f), rescale4<E4M3>(w.y, f), rescale4<E4M3>(w.z, f), rescale4<E4M3>(w.w, f));
@@ -260,7 +269,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
         uint2 w;
         if (int8) w = make_uint2(quantize4<INT8>(v[i].x, v[i].y, inv), quantize4<INT8>(v[i].z, v[i].w, inv));
         else w = make_uint2(quantize4<E4M3>(v[i].x, v[i].y, inv), quantize4<E4M3>(v[i].z, v[i].w, inv));
-        if (o != 255u) *reinterpret_cast<uint2*>(codes + ((page_row + o) * Hkv + h) * D + sub * 8) = w;
+        if (o != 255u) *reinterpret_cast<uint2*>(page_at + static_cast<size_t>(o) * row_step + sub * 8) = w;
       }
     }
   };
@@ -296,7 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
           len = last - (near0 + i0) + 1;
         }
       }
-      store_run(page, near0 + i0, len);
+      store_run(page, i0, len);
     }
   }
 }

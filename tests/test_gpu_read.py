@@ -96,6 +96,24 @@ def test_strides_graphs_and_an_empty_call():
     assert torch.equal(bits(out[0]), bits(k)) and torch.equal(bits(out[1]), bits(v))
 
 
+@pytest.mark.parametrize("fmt", ["kvarn", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_that_are_16_byte_aligned_only(fmt, d):
+    """Rows that begin in the middle of a 32-byte sector, in either way, give the same bits."""
+    p = Paged(fmt, [70], 3, d, 16)
+    slots = p.table[0, np.arange(70) // 16] * 16 + np.arange(70) % 16
+    k, v = read(p.cache, slots, 3, d)
+    for off, stride in ((8, 3 * d + 16), (0, 3 * d + 8), (8, 3 * d + 8)):
+        flat = torch.full((2, 72 * (3 * d + 16)), 7.0, dtype=torch.bfloat16, device=DEV)
+        ko, vo = (torch.as_strided(x[off:], (70, 3, d), (stride, d, 1)) for x in flat)
+        kvq.kvq_read_cache(p.cache, ints(slots, torch.int64), ko, vo)
+        assert torch.equal(bits(ko), bits(k)) and torch.equal(bits(vo), bits(v))
+        rest = flat.clone()
+        for x in rest:
+            torch.as_strided(x[off:], (70, 3, d), (stride, d, 1)).fill_(7.0)
+        assert (rest == 7).all()
+
+
 def test_reading_and_writing_again_gives_the_same_codes():
     """INT8 rows survive the round trip through bf16 (codes of 8 bits, values of 8)."""
     p = Paged("int8", [200], 2, 128, 16)
