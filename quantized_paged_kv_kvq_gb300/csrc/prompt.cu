@@ -234,10 +234,9 @@ __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7F80u) !
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
   return (finite_bf16(w) ? w & 0xFFFFu : 0u) | (finite_bf16(w >> 16) ? w & 0xFFFF0000u : 0u);
 }
-// Whether one of two bf16 values is not finite: their exponents all ones.
-__device__ __forceinline__ bool any_not_finite(uint32_t w) {
-  return !finite_bf16(w) || !finite_bf16(w >> 16);
-}
+// Bit 15 (31) set where the lower (upper) of two bf16 values is not finite: one more in an
+// exponent of all ones carries into the sign's place.
+__device__ __forceinline__ uint32_t not_finite_bits(uint32_t w) { return (w & 0x7FFF7FFFu) + 0x00800080u; }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
@@ -299,16 +298,22 @@ __device__ __forceinline__ uint32_t ordered_pack_bf162(float lo, float hi) {
   return r;
 }
 
-// 32 bf16 values, 16-byte aligned.
-__device__ __forceinline__ void store64(uint16_t* to, const uint32_t (&w)[16]) {
+// 32 bf16 values, 16-byte aligned; by whole sectors where 32-byte aligned (a warp's store
+// touches 32 rows, a cycle each: half as many stores hold the SM up half as long).
+__device__ __forceinline__ void store64(uint16_t* to, const uint32_t (&w)[16], bool sectors) {
+  if (sectors) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(to)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    for (int k = 0; k < 2; ++k)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * k), "r"(w[8 * k]), "r"(w[8 * k + 1]),
+                   "r"(w[8 * k + 2]), "r"(w[8 * k + 3]), "r"(w[8 * k + 4]), "r"(w[8 * k + 5]), "r"(w[8 * k + 6]), "r"(w[8 * k + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(to)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
 }
 // 32 columns of a row's accumulators times mul, as bf16.
-__device__ __forceinline__ void load_result(uint32_t (&w)[16], uint32_t addr, float mul) {
-  uint32_t o[32];
-  tmem_ld32(o, addr);
-  tmem_wait_ld32(o);
+__device__ __forceinline__ void scale_result(uint32_t (&w)[16], const uint32_t* o, float mul) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) w[e] = pack_bf162(__uint_as_float(o[2 * e]) * mul, __uint_as_float(o[2 * e + 1]) * mul);
 }
@@ -326,15 +331,17 @@ __device__ __noinline__ void store_not_finite(const PromptArgs& a, const volatil
   if (mine) find_not_finite<D / 32>(a, &x, pos, live->bad_lo, live->bad_hi, hi, lo);
   __syncwarp();
   for (int k = 0; k < D / 32; ++k) {
-    uint32_t w[16];
-    load_result(w, o_addr + 32 * k, mul);
+    uint32_t o[32], w[16];
+    tmem_ld32(o, o_addr + 32 * k);
+    tmem_wait_ld32(o);
+    scale_result(w, o, mul);
     const uint32_t ups = hi[k], downs = lo[k];
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
       const uint32_t up = ups >> e & 1, down = downs >> e & 1, v = up && down ? 0x7FC0u : up ? 0x7F80u : 0xFF80u;
       if (up | down) w[e / 2] = e & 1 ? (w[e / 2] & 0xFFFFu) | v << 16 : (w[e / 2] & 0xFFFF0000u) | v;
     }
-    if (mine) store64(to + 32 * k, w);
+    if (mine) store64(to + 32 * k, w, false);
   }
 }
 
@@ -421,8 +428,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   if (wg < C::SOFT) {
     // ================= softmax: thread = row =================
     reg_take<C::R_SOFTMAX>();
-    const int half = wg, row = tid & 127;
+    const int half = wg, row = tid & 127, row_token = row / G, row_head = row - row_token * G;
     const float scale = a.sm_scale_log2;
+    const bool sectors = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0;
     const uint32_t never = scale < 0.f ? 0x7F800000u : 0xFF800000u;  // times scale: -inf
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t o_addr = tmem + C::O(half) + lane_base;
@@ -430,7 +438,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     bool ok = true;
     for (int item = 0; ok && get_item(item, x); ++item) {
       const int tiles = x.of(half);
-      const int tok = first_of(x, half, half_tokens) + row / G, last_tok = last_of(x, half, half_tokens);
+      const int tok = first_of(x, half, half_tokens) + row_token, last_tok = last_of(x, half, half_tokens);
       const bool mine = tiles > 0 && row < half_tokens * G && tok <= last_tok;
       const bool has_rows = __any_sync(0xffffffffu, mine);
       const int pos = mine ? tok : last_tok;
@@ -546,15 +554,21 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         tc_fence_after();
         const float mul = 1.f / l;
         const volatile Item* live = &ctrl->items[item % kItems];
-        uint16_t* const to = a.out + (static_cast<int64_t>(x.q0) + tok) * a.out_stride + (static_cast<int64_t>(x.h) * G + row % G) * D;
+        uint16_t* const to = a.out + (static_cast<int64_t>(x.q0) + tok) * a.out_stride + (static_cast<int64_t>(x.h) * G + row_head) * D;
         if (live->bad_hi >= 0) {
           store_not_finite<D>(a, live, o_addr, mul, mine, pos, to);
         } else {
 #pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t w[16];
-            load_result(w, o_addr + 32 * k, mul);
-            if (mine) store64(to + 32 * k, w);
+          for (int k = 0; k < D; k += 64) {
+            uint32_t o[64], w[16];
+            tmem_ld32(o, o_addr + k);
+            tmem_ld32(o + 32, o_addr + k + 32);
+            tmem_wait_ld32(o);
+            tmem_waited32(o + 32);
+            scale_result(w, o, mul);
+            if (mine) store64(to + k, w, sectors);
+            scale_result(w, o + 32, mul);
+            if (mine) store64(to + k + 32, w, sectors);
           }
         }
       }
@@ -792,16 +806,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           if (!ok) break;
           if (!sees_all(a, x, 0, half_tokens, key) || (halves > 1 && !sees_all(a, x, 1, half_tokens, key))) {
             uint4* const v = reinterpret_cast<uint4*>(smem + C::V + st * C::TILE) + 32 * w + lane;
-            bool bad = false;
-#pragma unroll 4
+            uint32_t bad = 0;
+#pragma unroll 8
             for (int k = 0; k < C::TILE / 16; k += 64) {
               const uint4 y = v[k];
-              if (any_not_finite(y.x) || any_not_finite(y.y) || any_not_finite(y.z) || any_not_finite(y.w)) {
-                bad = true;
+              bad |= not_finite_bits(y.x) | not_finite_bits(y.y) | not_finite_bits(y.z) | not_finite_bits(y.w);
+            }
+            bad &= 0x80008000u;
+            if (bad) {
+#pragma unroll 1
+              for (int k = 0; k < C::TILE / 16; k += 64) {
+                const uint4 y = v[k];
                 v[k] = make_uint4(finite_or_zero(y.x), finite_or_zero(y.y), finite_or_zero(y.z), finite_or_zero(y.w));
               }
-            }
-            if (bad) {
               atomicMin(&ctrl->items[item % kItems].bad_lo, i);
               atomicMax(&ctrl->items[item % kItems].bad_hi, i);
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -125,6 +125,21 @@ def test_strides_and_rows_outside_the_batch():
     assert kvq.kvq_get_device_error() == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_that_are_16_byte_aligned_only(d):
+    """Rows that begin in the middle of a 32-byte sector, in either way, give the same bits."""
+    q, k, v = projection(150, 4, 2, d)
+    cu = np.array([0, 100, 150])
+    one = attend(q, k, v, cu)
+    for off, stride in ((8, 4 * d + 16), (0, 4 * d + 8), (8, 4 * d + 8)):
+        flat = torch.full((160 * (4 * d + 16),), 7.0, dtype=torch.bfloat16, device=DEV)
+        out = torch.as_strided(flat[off:], (150, 4, d), (stride, d, 1))
+        attend(q, k, v, cu, out=out)
+        assert torch.equal(bits(out), bits(one))
+        out.fill_(7.0)
+        assert (flat == 7).all()
+
+
 def test_bad_offsets_are_flagged_and_cut():
     q, k, v = projection(30, 4, 2, 64)
     for cu, most in (([0, 40, 50], 30), ([0, 10, 5], 20), ([-4, 10, 20], 20), ([0, 20, 30], 12)):
@@ -211,6 +226,22 @@ def test_repeats_streams_and_graphs():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(bits(out), bits(attend(q, k, v, cu)))
+
+
+def test_two_calls_at_once():
+    """Calls on two streams share nothing."""
+    cu = np.array([0, 900, 1400])
+    sets = [projection(1400, 8, 2, 128, seed=s) for s in (1, 2)]
+    ref = [attend(*x, cu) for x in sets]
+    streams, cut = [torch.cuda.Stream() for _ in sets], ints(cu)
+    outs = [torch.empty_like(r) for r in ref]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, x, out in zip(streams, sets, outs):
+            kvq.kvq_prompt_attention(*x, out, cut, 900, 128 ** -0.5, stream=s)
+    torch.cuda.synchronize()
+    for out, r in zip(outs, ref):
+        assert torch.equal(bits(out), bits(r))
 
 
 def test_nothing_to_do():
