@@ -477,11 +477,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             if (!all) {
               const int last = pos - t0;
               const uint64_t seen = seen_columns(c0, last, a.window > 0 ? last - a.window + 1 : -1, a.sinks - t0);
-              const uint32_t lo = static_cast<uint32_t>(seen), hi = static_cast<uint32_t>(seen >> 32);
+              if (!__any_sync(0xffffffffu, seen != 0)) {  // a step that no row of the warp sees
+                sum = 0.f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                s[e] = lo >> e & 1 ? s[e] : never;
-                s[e + 32] = hi >> e & 1 ? s[e + 32] : never;
+                for (int e = 0; e < kStep / 2; ++e) p[e] = 0;
+                break;
+              }
+              if (__any_sync(0xffffffffu, ~seen != 0)) {
+                const uint32_t lo = static_cast<uint32_t>(seen), hi = static_cast<uint32_t>(seen >> 32);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  s[e] = lo >> e & 1 ? s[e] : never;
+                  s[e + 32] = hi >> e & 1 ? s[e + 32] : never;
+                }
               }
             }
             if (__any_sync(0xffffffffu, seek)) {
