@@ -142,8 +142,9 @@ typedef struct {
  *   With KVQ_FLAG_VARNORM_ROTATE the ASYM step runs on the normalised,
  *   rotated row (see kvq_hadamard for the transform's definition).
  *   BLOCK: pages fill from the front.  The tokens of a page are consecutive in a
- *          call, skipped ones between them aside (31 in a row at most); with m the largest finite |x| of their rows (per kv-head), need = 0
- *          for m = 0, else max(m / qmax, 2^-126), qmax = 127 or 448.  Where they reach
+ *          call, skipped ones between them aside (31 in a row at most); with m the
+ *          largest finite |x| of their rows (per kv-head), need = 0 for m = 0, else
+ *          max(m / qmax, 2^-126), qmax = 127 or 448.  Where they reach
  *          offset 0 the page is begun: scale = need.  Else it goes on behind the rows
  *          in front of them: scale = old * 2^k with the least k >= 0 that makes
  *          it >= need (old 0: need), and for k > 0 the codes in front become code * 2^-k,
@@ -585,7 +586,9 @@ kvq_status kvq_decode_window(const kvq_cache_desc* cache, void* k_cache, void* v
  * Arithmetic: 16-bit operands in the tensor cores, float32 sums and softmax.
  *   int8 and FP8 codes are exact in fp16; asymmetric rows are rounded once to fp16
  *   when they are dequantized ((code * scale + zero_point) [* sigma] past 65504 is
- *   infinite; only the result counts, not the product on the way);
+ *   infinite; only the result counts, not the product on the way); so are those of the
+ *   block formats (code * scale: what is past 65504 is infinite, below 2^-25 zero; the
+ *   decode keeps the scale apart and takes any);
  *   the query is rounded to fp16 as in kvq_paged_decode (KVQ_DEVERR_QUERY_RANGE);
  *   probabilities are rounded to fp16.  The 16-bit cache uses bf16 throughout.
  *   A value (V) that is not finite makes the rows that see it not finite; rows
@@ -677,13 +680,13 @@ kvq_status kvq_read_cache(const kvq_cache_desc* cache, const void* k_cache, cons
 
 /*
  * kvq_debug_arm_wait_timeout -- test hook for the bounded pipeline waits of the
- * decode, the chunk attention and the prompt attention (every mbarrier wait gives up after a number
- * of polls, sets KVQ_DEVERR_TIMEOUT and makes its CTA stop loading, publish nothing
+ * decode, the chunk attention and the prompt attention (every mbarrier wait gives up
+ * after a number of polls, sets KVQ_DEVERR_TIMEOUT and makes its CTA stop loading, publish nothing
  * and return once no copy or matrix product it issued is in flight).  It applies to
  * the next launch of the process of either kind (kvq_paged_decode*,
  * kvq_decode_append, kvq_decode_mixed, kvq_decode_window; kvq_paged_prefill;
- * kvq_prompt_attention) and then disarms itself: that launch polls each wait at most `polls` times (>= 1),
- * and CTA `cta` of the first kv-head group never issues the loads of the
+ * kvq_prompt_attention) and then disarms itself: that launch polls each wait at most
+ * `polls` times (>= 1), and CTA `cta` of the first kv-head group never issues the loads of the
  * `tile`-th tile of its range (chunk and prompt attention: CTA `cta` of the first part of the
  * keys waits for what nothing signals in place of the K of its `tile`-th tile of 128
  * keys; -1: no tile), so that the waits for that tile run out with nothing in

@@ -99,7 +99,7 @@ constexpr int kTileScaleBytes = 128;
 // with the producer's cursor and the abort flag; block formats' tile scales; and 1 KB of
 // alignment.  Block formats rely on the window's declared alignment instead (and look whether
 // it holds): with 8 query heads of 128 a kv-head that 1 KB would leave room for one CTA per
-// SM (146 us for 12 x 4,096..32,768 tokens and 64 / 8 heads of 128 in e4m3, against 91).
+// SM (146 us for 12 x 4,096..32,768 tokens and 64 / 8 heads of 128 in e4m3, against 95).
 __host__ __device__ constexpr int q_rows_bytes(int g, int d) { return (g * d * 2 + 15) / 16 * 16; }
 template <class C>
 __host__ __device__ constexpr int decode_smem_bytes(int hpc, int g) {
