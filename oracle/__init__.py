@@ -10,6 +10,8 @@ computes, written from the source pages:
   kvarn      -- variance normalisation + rotation before asymmetric codes
   cache      -- quantize-and-scatter into the paged cache, dequantization
   attention  -- float64 single-token paged decode attention
+  blocks     -- 8-bit codes with a scale per page and kv-head: the store that grows a
+                page's scale, its rows, float64 attention over rows
 
 Only tests/, __graft_entry__.smoke() and bench.py's cpu_baseline /
 reference leg may import, call or execute anything in this package.  It
@@ -18,4 +20,4 @@ imports nothing from the library.  Pins (tests/test_oracle_*.py) tie every
 function to the format definitions, closed forms, library routines and
 brute force; there is no function here whose parity is unpinned.
 """
-from . import formats, hadamard, kvarn, cache, attention  # noqa: F401
+from . import formats, hadamard, kvarn, cache, attention, blocks  # noqa: F401

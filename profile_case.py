@@ -9,7 +9,8 @@ Arguments after the workload name override its generator settings (integers).
 
   python profile_case.py operators prefill_long
 
-runs a case of perf/operators.py instead, through the library's calls.
+runs a case of perf/operators.py instead (`more_operators`: of perf/more_operators.py),
+through the library's calls.
 Everything goes through the library's public calls; nothing is checked here.
 """
 from __future__ import annotations
@@ -62,10 +63,10 @@ def run(name: str, repeats: int = 3, **overrides) -> None:
     print("device error bits:", kvq.kvq_get_device_error())
 
 
-def run_operator(name: str, repeats: int = 3) -> None:
+def run_operator(module: str, name: str, repeats: int = 3) -> None:
     kbuild.build()
-    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "perf", "operators.py")
-    spec = importlib.util.spec_from_file_location("perf_operators", path)
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "perf", module + ".py")
+    spec = importlib.util.spec_from_file_location("perf_" + module, path)
     cases = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(cases)
     cases.own = True
@@ -78,8 +79,8 @@ def run_operator(name: str, repeats: int = 3) -> None:
 
 def main(argv=None) -> None:
     argv = sys.argv[1:] if argv is None else argv
-    if argv[0] == "operators":
-        run_operator(argv[1])
+    if argv[0] in ("operators", "more_operators"):
+        run_operator(*argv)
         return
     kw = {}
     for a in argv[1:]:

@@ -125,6 +125,27 @@ def test_strides_and_rows_outside_the_batch():
     assert kvq.kvq_get_device_error() == 0
 
 
+def test_rows_past_4_gib():
+    """Tokens 32 MB apart: offsets of elements and bytes past 2^31 and 2^32."""
+    q, k, v = projection(150, 4, 2, 64)
+    cu = np.array([0, 100, 150])
+    one = attend(q, k, v, cu)
+    flat = torch.empty(150 << 24, dtype=torch.bfloat16, device=DEV)
+    far = [torch.as_strided(flat, x.shape, (1 << 24, 64, 1), 1024 * i) for i, x in enumerate((q, k, v, q))]
+    for x, y in zip(far, (q, k, v)):
+        x.copy_(y)
+    attend(*far[:3], cu, out=far[3])
+    assert torch.equal(bits(far[3]), bits(one))
+    # and written to and read back from a cache so
+    cache = kvq.alloc_kv_cache("bf16", "bf16", 10, 16, 2, 64, device=DEV)
+    slots = ints(np.arange(150), torch.int64)
+    kvq.kvq_write_cache(cache, far[1], far[2], slots)
+    outs = [torch.as_strided(flat, k.shape, (1 << 24, 64, 1), 8192 + 1024 * i) for i in range(2)]
+    kvq.kvq_read_cache(cache, slots, *outs)
+    assert torch.equal(bits(outs[0]), bits(k)) and torch.equal(bits(outs[1]), bits(v))
+    assert kvq.kvq_get_device_error() == 0
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_outputs_that_are_16_byte_aligned_only(d):
     """Rows that begin in the middle of a 32-byte sector, in either way, give the same bits."""
