@@ -180,10 +180,11 @@ class KVCache:
     v_head_scales: Optional[torch.Tensor] = None  # fp32 [num_kv_heads] (symmetric V)
 
     def desc(self) -> _CacheDesc:
-        if self.k_fmt in BLOCK or self.v_fmt in BLOCK:
+        kf, vf = self.k_fmt, self.v_fmt
+        if kf in BLOCK or vf in BLOCK:
             _page_scales(self)
         km, vm, sg, ks, vs = self.k_meta, self.v_meta, self.signs, self.k_head_scales, self.v_head_scales
-        return _CacheDesc(FMT[self.k_fmt], FMT[self.v_fmt], self.num_kv_heads, self.head_dim,
+        return _CacheDesc(FMT[kf], FMT[vf], self.num_kv_heads, self.head_dim,
                           self.block_size, self.num_blocks,
                           FLAG_VARNORM_ROTATE if self.varnorm_rotate else 0,
                           float(self.k_scale), float(self.v_scale), None if km is None else km.data_ptr(),
@@ -208,13 +209,20 @@ def scale_pitch(num_kv_heads: int) -> int:
 
 def _page_scales(cache: KVCache) -> None:
     """The scales of a block format's cache are what its description says, on its codes' device."""
-    for name, fmt, m in (("k_meta", cache.k_fmt, cache.k_meta), ("v_meta", cache.v_fmt, cache.v_meta)):
-        if fmt in BLOCK:
-            want = (cache.num_blocks, scale_pitch(cache.num_kv_heads))
-            if (m is None or m.dtype is not torch.float32 or m.dim() != 2 or m.shape[0] < want[0] or m.shape[1] != want[1]
-                    or not m.is_contiguous() or m.get_device() != cache.k_cache.get_device()):
-                raise ValueError(f"{name} must be a contiguous float32 tensor of shape {want} on the codes' device, got "
-                                 + ("None" if m is None else f"{m.dtype} {tuple(m.shape)} with strides {m.stride()} on {m.device}"))
+    blocks, pitch, dev = cache.num_blocks, (cache.num_kv_heads + 3) // 4 * 4, cache.k_cache.get_device()
+    if cache.k_fmt in BLOCK:
+        _page_scale("k_meta", cache.k_meta, blocks, pitch, dev)
+    if cache.v_fmt in BLOCK:
+        _page_scale("v_meta", cache.v_meta, blocks, pitch, dev)
+
+
+def _page_scale(name: str, m: Optional[torch.Tensor], blocks: int, pitch: int, dev: int) -> None:
+    if m is not None and m.dtype is torch.float32 and m.is_contiguous() and m.get_device() == dev:
+        shape = m.shape
+        if len(shape) == 2 and shape[1] == pitch and shape[0] >= blocks:
+            return
+    raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(blocks, pitch)} on the codes' device, got "
+                     + ("None" if m is None else f"{m.dtype} {tuple(m.shape)} with strides {m.stride()} on {m.device}"))
 
 
 def alloc_kv_cache(k_fmt, v_fmt, num_blocks, block_size, num_kv_heads, head_dim,
