@@ -70,8 +70,13 @@ constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is 
 // dominates (often a first token whose own value is next to nothing).
 constexpr float kLift = 7.0f;
 
-template <int D_, int ROWS_, bool STAGED = false>  // head_dim, rows, keys dequantized ahead
+// head_dim, rows, keys dequantized ahead, block formats (in instances of their own: beside
+// the other formats' their conversion cost those 2 %)
+template <int D_, int ROWS_, bool STAGED = false, bool BLOCK_ = false>
 struct Cfg {
+  static constexpr bool BLOCK = BLOCK_;
+  // whether fmt is a block format (keys dequantized ahead: of any)
+  static __device__ __forceinline__ bool block(int fmt) { return BLOCK || (STAGED && is_block(fmt)); }
   static constexpr int D = D_, ROWS = ROWS_;
   static constexpr int NW = ROWS == 256 ? 2 : 1;  // softmax warpgroups
   static constexpr int THREADS = 128 * NW + (STAGED ? 0 : 2 * kProducers) + 128;
@@ -390,16 +395,16 @@ struct Source {
   int fmt, fields;
 };
 __device__ __forceinline__ Source make_source(const uint8_t* cache, const __half* meta, int fmt, int kvarn, int d,
-                                              int hkv, int h, int bs) {
+                                              int hkv, int h, int bs, bool block) {
   Source s;
   const int rb = row_bytes(fmt, d);
   s.codes = cache + static_cast<size_t>(h) * rb;
   s.token_bytes = hkv * rb;
   s.page_bytes = static_cast<uint32_t>(bs) * s.token_bytes;  // below 2^31: checked on the host
   s.fmt = fmt;
-  s.fields = is_asym(fmt) ? (kvarn ? 3 : 2) : is_block(fmt) ? 1 : 0;
-  s.meta = is_asym(fmt) ? meta + static_cast<size_t>(h) * s.fields * bs : is_block(fmt) ? meta + 2 * h : nullptr;
-  s.meta_page = is_block(fmt) ? scale_pitch(hkv) : static_cast<uint32_t>(hkv) * s.fields * bs;
+  s.fields = is_asym(fmt) ? (kvarn ? 3 : 2) : block ? 1 : 0;
+  s.meta = is_asym(fmt) ? meta + static_cast<size_t>(h) * s.fields * bs : block ? meta + 2 * h : nullptr;
+  s.meta_page = block ? scale_pitch(hkv) : static_cast<uint32_t>(hkv) * s.fields * bs;
   return s;
 }
 
@@ -501,10 +506,10 @@ struct Producer {
     }
   }
   __device__ __forceinline__ void copy(const Source& s, const KeyTile& k, int slot, uint32_t dst) const {
-    if (s.fmt == BF16) copy_codes<BF16>(s, k, slot, dst);
-    else if (s.fmt == INT4A) copy_codes<INT4A>(s, k, slot, dst);
+    if (!C::BLOCK && s.fmt == BF16) copy_codes<BF16>(s, k, slot, dst);
+    else if (!C::BLOCK && s.fmt == INT4A) copy_codes<INT4A>(s, k, slot, dst);
     else copy_codes<INT8>(s, k, slot, dst);  // any 8-bit code
-    if (is_block(s.fmt)) {  // a token per thread: its page's scale
+    if (C::BLOCK) {  // a token per thread: its page's scale
       const int blk = __shfl_sync(0xffffffffu, k.block, tid >> a.block_shift);
       cp_async_or_zero<4>(smem + C::META + slot * 3 * kKeys * 2 + tid * 4,
                           reinterpret_cast<const float*>(s.meta) + static_cast<unsigned long long>(static_cast<uint32_t>(blk)) * s.meta_page,
@@ -601,17 +606,19 @@ struct Producer {
   }
   template <bool IS_V>
   __device__ __forceinline__ bool finish(const Source& s, const KeyTile& k, int slot, uint32_t dst) const {
-    switch (s.fmt) {
-      case INT8: return convert<INT8, false, IS_V>(k, slot, dst);
-      case E4M3: return convert<E4M3, false, IS_V>(k, slot, dst);
-      case E5M2: return convert<E5M2, false, IS_V>(k, slot, dst);
-      case INT8B: return convert<INT8B, false, IS_V>(k, slot, dst);
-      case E4M3B: return convert<E4M3B, false, IS_V>(k, slot, dst);
-      case INT4A:
-        return s.fields == 3 ? convert<INT4A, true, IS_V>(k, slot, dst) : convert<INT4A, false, IS_V>(k, slot, dst);
-      case UINT8A:
-        return s.fields == 3 ? convert<UINT8A, true, IS_V>(k, slot, dst) : convert<UINT8A, false, IS_V>(k, slot, dst);
-      default: return IS_V ? check_bf16(dst) : false;
+    if constexpr (C::BLOCK) {
+      return s.fmt == INT8B ? convert<INT8B, false, IS_V>(k, slot, dst) : convert<E4M3B, false, IS_V>(k, slot, dst);
+    } else {
+      switch (s.fmt) {
+        case INT8: return convert<INT8, false, IS_V>(k, slot, dst);
+        case E4M3: return convert<E4M3, false, IS_V>(k, slot, dst);
+        case E5M2: return convert<E5M2, false, IS_V>(k, slot, dst);
+        case INT4A:
+          return s.fields == 3 ? convert<INT4A, true, IS_V>(k, slot, dst) : convert<INT4A, false, IS_V>(k, slot, dst);
+        case UINT8A:
+          return s.fields == 3 ? convert<UINT8A, true, IS_V>(k, slot, dst) : convert<UINT8A, false, IS_V>(k, slot, dst);
+        default: return IS_V ? check_bf16(dst) : false;
+      }
     }
   }
 };
@@ -803,7 +810,7 @@ template <class C>
 __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& span, int seq, int h, int p, int i_lo,
                                              int i_hi, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   const int bs = 1 << a.block_shift;
-  const Source s = make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, C::D, a.num_kv_heads, h, bs);
+  const Source s = make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, C::D, a.num_kv_heads, h, bs, C::block(a.v_fmt));
   for (int i = i_lo; i <= i_hi; ++i) {
     const int t0 = tile_key(span, i);
     for (int t = t0; t < t0 + kKeys && t <= p; ++t) {
@@ -814,7 +821,7 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
       const uint8_t* row = s.codes + static_cast<size_t>(blk) * s.page_bytes + static_cast<size_t>(off) * s.token_bytes;
       __half sc{}, zp{}, sg{};
       float ps = 0.f;
-      if (is_block(s.fmt)) {
+      if (C::block(s.fmt)) {
         ps = reinterpret_cast<const float*>(s.meta)[static_cast<size_t>(blk) * s.meta_page];
       } else if (s.fields > 0) {
         const __half* m = s.meta + static_cast<size_t>(blk) * s.meta_page + off;
@@ -832,7 +839,7 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
           v = static_cast<uint32_t>(row[d]) << 8;
         } else if (s.fmt == E4M3) {
           v = e4m3x2_to_f16x2(row[d]) & 0xFFFFu;
-        } else if (is_block(s.fmt)) {  // as dequantize16
+        } else if (C::block(s.fmt)) {  // as dequantize16
           const float c = s.fmt == INT8B ? static_cast<float>(static_cast<int8_t>(row[d]))
                                          : __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_to_f16x2(row[d]))));
           v = __half_as_ushort(__float2half_rn(c * ps));
@@ -879,10 +886,10 @@ __device__ __forceinline__ void result_columns(uint32_t (&o)[32], uint32_t addr,
   }
 }
 
-template <int D, int ROWS, bool STAGED>
-__global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
+template <int D, int ROWS, bool STAGED, bool BLOCK>
+__global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap map_staged) {
-  using C = Cfg<D, ROWS, STAGED>;
+  using C = Cfg<D, ROWS, STAGED, BLOCK>;
   constexpr int NW = C::NW;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzled tiles: 1024-byte aligned
@@ -912,7 +919,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
   // warps with rows, of all and of each half (the others of a half only wait for the end)
   const int row_warps = (R1 - R0 + 31) / 32;
   auto half_warps = [&](int w) { return max(min(row_warps - 4 * w, 4), 1); };
-  const bool bf = a.k_fmt == BF16;
+  const bool bf = !C::BLOCK && a.k_fmt == BF16;
 
   if (tid == 0) {
     mbar_init(bar(&ctrl->q_full), row_warps);
@@ -1129,8 +1136,8 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED>::THREADS, 1)
     if (nk > 0) {
       const int bs = 1 << a.block_shift;
       const bool is_v = wg == NW + 1;
-      const Source src = is_v ? make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs)
-                              : make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
+      const Source src = is_v ? make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs, C::BLOCK)
+                              : make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs, C::BLOCK);
       const Producer<C> pr{a, span, base, tid & 127, seq};
       const uint32_t operand = base + (is_v ? C::V : C::K);
       unsigned long long* full = is_v ? ctrl->v_full : ctrl->k_full;
@@ -1410,8 +1417,8 @@ __global__ void __launch_bounds__(2 * kProducers) stage_kernel(const __grid_cons
   const size_t seq_head = static_cast<size_t>(seq) * a.num_kv_heads + h;
   const bool is_v = tid >= kProducers;
   const size_t row = (is_v ? static_cast<size_t>(a.num_seqs) * a.num_kv_heads * a.staged_len : 0) + seq_head * a.staged_len + t0;
-  const Source s = is_v ? make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs)
-                        : make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs);
+  const Source s = is_v ? make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs, is_block(a.v_fmt))
+                        : make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs, is_block(a.k_fmt));
   uint16_t* dst = a.staged + row * D;
   const bool bad = is_v ? stage_any<D, true>(a, s, span, pages, t0, dst, tid & 127)
                         : stage_any<D, false>(a, s, span, pages, t0, dst, tid & 127);
@@ -1470,16 +1477,16 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs a, 
   }
 }
 
-template <int D, int ROWS, bool STAGED>
+template <int D, int ROWS, bool STAGED, bool BLOCK>
 cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
-  using C = Cfg<D, ROWS, STAGED>;
+  using C = Cfg<D, ROWS, STAGED, BLOCK>;
   static std::atomic<unsigned long long> attr_done{0};  // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
-    e = cudaFuncSetAttribute(prefill_kernel<D, ROWS, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(prefill_kernel<D, ROWS, STAGED, BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
   }
@@ -1501,18 +1508,23 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   const dim3 grid(static_cast<unsigned>(a.tiles) * a.num_kv_heads, a.num_splits, 1);
-  prefill_kernel<D, ROWS, STAGED><<<grid, C::THREADS, C::SMEM, st>>>(a, map);
+  prefill_kernel<D, ROWS, STAGED, BLOCK><<<grid, C::THREADS, C::SMEM, st>>>(a, map);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.num_splits == 1) return e;
   prefill_join_kernel<D><<<grid.x, 256, 0, st>>>(a, C::ROWS);
   return cudaGetLastError();
 }
 
+template <int D, bool BLOCK>
+cudaError_t launch_rows(const PrefillArgs& a, cudaStream_t st) {
+  if (a.rows_per_tile == 64) return launch_t<D, 64, false, BLOCK>(a, st);
+  if (a.rows_per_tile == 128) return launch_t<D, 128, false, BLOCK>(a, st);
+  return launch_t<D, 256, false, BLOCK>(a, st);
+}
 template <int D>
 cudaError_t launch_d(const PrefillArgs& a, cudaStream_t st) {
-  if (a.rows_per_tile == 64) return launch_t<D, 64, false>(a, st);
-  if (a.rows_per_tile == 128) return launch_t<D, 128, false>(a, st);
-  return a.staged != nullptr ? launch_t<D, 256, true>(a, st) : launch_t<D, 256, false>(a, st);
+  if (a.staged != nullptr) return launch_t<D, 256, true, false>(a, st);
+  return is_block(a.v_fmt) ? launch_rows<D, true>(a, st) : launch_rows<D, false>(a, st);
 }
 
 }  // namespace
