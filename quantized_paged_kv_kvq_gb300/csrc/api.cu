@@ -250,8 +250,9 @@ struct PrefillShape {
 // Measured ahead / not, 32 / 8 heads of 128: int8, 8 x 4,096 keys: 4 row tiles 160 /
 // 138 us, 8 257 / 257, 1 x 8,192 keys and 32 tiles 193 / 217; KVarN, 16 x 4,096 keys:
 // 2 tiles 223 / 222, 8 x 4,096: 4 tiles 182 / 210, 8 289 / 389; int4 4 tiles 165 / 177;
-// bf16 as int8; e4m3 per page, 8 x 4,096: 2 tiles 111 / 97, 3 163 / 181, 8 264 / 340.
-constexpr int64_t stage_tiles(int fmt) { return has_meta(fmt) ? 3 : 8; }
+// bf16 as int8; e4m3 per page, 8 x 4,096: 3 tiles 164 / 160, 4 165 / 164, 6 215 / 232, 8
+// 264 / 287, 32 x 2,048: 3 283 / 248, 4 318 / 304, 6 431 / 425, 8 513 / 541.
+constexpr int64_t stage_tiles(int fmt) { return is_asym(fmt) ? 3 : is_block(fmt) ? 5 : 8; }
 constexpr int64_t kStageBytes = 16ll << 30;
 // What can be said of a batch's sizes without a device.
 kvq_status check_prefill(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
