@@ -21,10 +21,11 @@
 // where runs begin and end: no search over sequences, no atomics.  step grows with the
 // call from 1 (a decode step: every request's run starts at once) to a page.  A thread a
 // token, the CTA loads the places of the tokens around its own and marks, a bit each, which
-// are there and which begin a run: the warps then only read bits.
+// are there, begin a run or follow on the offset before: the warps then only read bits.
 // Bound by HBM: 4 D bytes read and 2 D written per token and head (16,384 tokens, 8 heads of
-// 128, int8, pages of 16: 22.6 us, 4.5 TB/s; of 64: 29 us).  A decode step's 64 rows take
-// 4.5 us: places, scales and rows are loaded one after the other.
+// 128, int8, pages of 16: 20.3 us, 5.0 TB/s; of 64: 28.5 us).  Runs at offsets one after the
+// other, marked as such, are stored without a look-up per row (else 22.6 us).  A decode
+// step's 64 rows take 4.6 us: places, scales and rows are loaded one after the other.
 #include <algorithm>
 
 #include "kvq_device.cuh"
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
   constexpr int kNear = (CH <= 2 ? 1 : 2) * kWarps * 32;  // tokens whose places the CTA keeps
   __shared__ uint32_t most[2][kWarps];
   __shared__ int front[2][kWarps];
-  __shared__ uint32_t is_there[kNear / 32], begins[kNear / 32];
+  __shared__ uint32_t is_there[kNear / 32], begins[kNear / 32], goes_on[kNear / 32];
   __shared__ int near_page[kNear];
   __shared__ uint8_t near_off[kNear];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -149,9 +150,12 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
     if (page >= 0 && !append && i >= kBack)
       for (int d = 1; d <= kBack && before < 0; ++d) before = near_page[i - d];
     const uint32_t there = __ballot_sync(kAll, page >= 0), first = __ballot_sync(kAll, page >= 0 && i >= kBack && page != before);
+    const uint32_t next = __ballot_sync(kAll, page >= 0 && i > 0 && near_page[max(i - 1, 0)] == page &&
+                                                  near_off[max(i - 1, 0)] + 1 == near_off[i]);
     if (lane == 0) {
       is_there[i / 32] = there;
       begins[i / 32] = first;
+      goes_on[i / 32] = next;  // the next offset of the page of the token before it
     }
   }
   __syncthreads();
@@ -161,14 +165,16 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
     return t >= 0 && t < n ? place(t, false) : make_int2(-1, 0);
   };
 
-  // The run of `len` tokens from near0 + i0 on in `page` (skipped ones among them).
-  auto store_run = [&](int page, int i0, int64_t len) {
+  // The run of `len` tokens from near0 + i0 on in `page` (skipped ones among them).  dense: at
+  // offsets one after the other, so that nothing has to be looked up row by row.
+  auto store_run = [&](int page, int i0, int64_t len, bool dense) {
     const int64_t t0 = near0 + i0;
     float* const scale_at = scales + static_cast<size_t>(page) * pitch + h;
     const float was = active ? *scale_at : 0.0f;  // means nothing where the page is begun
     uint4 v[NP];
     uint32_t m2 = 0;
-    int first = bs;  // the foremost offset
+    const int off0 = near_off[i0];
+    int first = dense ? off0 : bs;  // the foremost offset
     const uint16_t* const row0 = rows + t0 * stride;
     uint32_t off[(NP + 3) / 4];  // offsets of the rows, a byte each, 255: not this thread's, or skipped
     auto load = [&](int64_t r0) {  // rows r0 .. r0 + 15 of the run
@@ -177,6 +183,12 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
         const int64_t r = r0 + grp + i * RPI;
         const bool read = active && r < len;
         v[i] = read ? ldg_stream16(row0 + r * stride) : make_uint4(0, 0, 0, 0);
+      }
+      if (dense) return;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int64_t r = r0 + grp + i * RPI;
+        const bool read = active && r < len;
         uint32_t o = 255u;
         if (read) {
           if (i0 + r < kNear) {
@@ -220,7 +232,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
     load(16 * chunk);
     take_max();
     uint32_t m = __reduce_max_sync(kAll, max(m2 & 0xFFFFu, m2 >> 16));
-    first = __reduce_min_sync(kAll, first);
+    if (!dense) first = __reduce_min_sync(kAll, first);
     if constexpr (CH > 1) {
       if (lane == 0) {
         most[parity][warp] = m;
@@ -267,7 +279,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
       if (r0 != 16 * chunk) load(r0);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const uint32_t o = off[i / 4] >> (8 * (i % 4)) & 255u;
+        const int64_t r = r0 + grp + i * RPI;
+        const uint32_t o = !dense ? off[i / 4] >> (8 * (i % 4)) & 255u : r < len ? off0 + static_cast<uint32_t>(r) : 255u;
         uint2 w;
         if (int8) w = make_uint2(quantize4<INT8>(v[i].x, v[i].y, inv), quantize4<INT8>(v[i].z, v[i].w, inv));
         else w = make_uint2(quantize4<E4M3>(v[i].x, v[i].y, inv), quantize4<E4M3>(v[i].z, v[i].w, inv));
@@ -284,6 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
       starts &= starts - 1;
       const int page = near_page[i0];
       int64_t len = 1;
+      bool dense = true;
       if (!append) {
         // to the last token that is there before the next run begins
         int e = w;
@@ -306,8 +320,12 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
           }
           len = last - (near0 + i0) + 1;
         }
+        int g = w;
+        uint32_t gap = ~goes_on[w] & ~((2u << (i0 & 31)) - 1u);
+        while (gap == 0 && g + 1 < kNear / 32) gap = ~goes_on[++g];
+        dense = i0 + len <= (gap != 0 ? 32 * g + __ffs(gap) - 1 : kNear);
       }
-      store_run(page, i0, len);
+      store_run(page, i0, len, dense);
     }
   }
 }
