@@ -84,6 +84,25 @@ def test_skipped_tokens_between_those_of_a_page():
         p.same()
 
 
+@pytest.mark.parametrize("bs,front", [(16, 0), (32, 5), (64, 0), (128, 0), (128, 37)])
+def test_one_jump_among_offsets_in_a_row(bs, front):
+    """Two neighbours swapped, or one left out, anywhere in the page; the rest in order."""
+    p = Blocked("e4m3_int8", [bs] * (2 * bs), 1, 64, bs)
+    for s in range(2 * bs):  # where the pages begin within the call moves by `front`
+        at = np.arange(front, bs)
+        if s % 2:
+            at = np.delete(at, (s // 2) % len(at))
+        else:
+            i = (s // 2) % (len(at) - 1)
+            at[[i, i + 1]] = at[[i + 1, i]]
+        slots = np.concatenate([np.full(s % 3, -1), p.slots(s, at), p.slots((s + 1) % (2 * bs), [0])]) if s % 4 == 3 else p.slots(s, at)
+        if front:
+            p.store(*p.rows(front), p.slots(s, np.arange(front)))
+        p.store(*p.rows(len(slots)), slots)
+    p.same()
+    assert kvq.kvq_get_device_error() == 0
+
+
 def test_a_slot_named_twice_spoils_no_other_row():
     p = Blocked("int8", [16], 2, 64, 16)
     k, v = p.rows(40)
