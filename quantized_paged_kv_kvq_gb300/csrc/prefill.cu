@@ -62,7 +62,7 @@ namespace {
 
 constexpr int kKeys = 128;            // keys per tile
 constexpr int kProducers = 128;       // threads that load and dequantize K; as many for V
-constexpr int kDrain = 1 << 18;       // polls for what is in flight at a CTA's end (some seconds)
+constexpr int kDrain = 1 << 18;       // polls for what is in flight at a CTA's end (a second)
 constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is not raised: p <= 2^8
 // Probabilities are made 2^7 times as large, sums and accumulators with them, so that
 // as 16-bit operands they end at 2^15 and reach down to 2^-32 of the maximum's: fp16

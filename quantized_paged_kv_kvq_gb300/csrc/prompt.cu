@@ -48,7 +48,8 @@ KVQ_ERROR_ACCESSOR(take_error_bits_prompt)
 namespace {
 
 constexpr int kKeys = 128;       // keys per tile
-constexpr int kDrain = 1 << 18;  // polls for what is in flight at a CTA's end (some seconds)
+constexpr int kDrain = 1 << 18;  // polls for what is in flight at a CTA's end (a second)
+constexpr int kQuick = 1 << 9;   // the issuing warp's looks before it waits as the others do (some 10 us)
 constexpr int kStep = 64;        // keys whose probabilities are handed over together
 constexpr float kMost = 0x1p20f; // largest sum of a step before the maximum is raised
 
@@ -675,19 +676,27 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       int ns = 0, nv = 0;  // products of each kind issued
       // The tensor cores take some four products ahead, 256 cycles' worth, and stall the issuing
       // warp behind that: between the last of one group and the first of the next, everything
-      // has to be done in that time.  So barriers are looked at together, in one loop.
-      auto poll = [&](auto ready) {  // until all that ready() looks at is there
-        for (int n = 0; n < spin; ++n) {
-          if (__all_sync(0xffffffffu, ready())) return true;
+      // has to be done in that time.  So barriers are looked at together, in one loop.  A look
+      // takes no time of its own, so those are not counted: what takes longer is waited for,
+      // `spin` times, by waits that sleep, as everywhere else.
+      auto look = [](uint32_t b, uint32_t parity) { return mbar_test(b, parity); };
+      auto sleep = [](uint32_t b, uint32_t parity) { return mbar_try_wait(b, parity); };
+      auto poll = [&](auto ready) {  // until all that ready(look) looks at is there
+        for (int n = 0; n < kQuick; ++n) {
+          if (__all_sync(0xffffffffu, ready(look))) return true;
           if ((n & 15) == 15 && __any_sync(0xffffffffu, *abort)) break;
+        }
+        for (int n = 0; n < spin; ++n) {
+          if (__all_sync(0xffffffffu, ready(sleep))) return true;
+          if (__any_sync(0xffffffffu, *abort)) break;
         }
         give_up();
         return false;
       };
       bool s_ready = false;  // the next score product's operands are there
-      auto scores_ready = [&]() {
+      auto scores_ready = [&](auto test) {
         const int t = sc.t0 + sc.i;
-        return mbar_test(bar(&ctrl->q_full), sc.item & 1) & mbar_test(bar(&ctrl->k_full[t % C::ST]), (t / C::ST) & 1);
+        return test(bar(&ctrl->q_full), sc.item & 1) & test(bar(&ctrl->k_full[t % C::ST]), (t / C::ST) & 1);
       };
       auto scores = [&]() {  // the next score product
         const int t = sc.t0 + sc.i, st = t % C::ST, w = sc.w, buf = ns % C::NB;
@@ -718,7 +727,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         while (ok && more_s && ns < nv + C::NB) {
           // where there are no scores to go on with, the next ones' operands are waited for
           if (!s_ready && ns == nv) ok = poll(scores_ready);
-          else if (!s_ready && !__all_sync(0xffffffffu, scores_ready())) break;
+          else if (!s_ready && !__all_sync(0xffffffffu, scores_ready(look))) break;
           if (ok) scores();
         }
         if (!ok) break;
@@ -732,15 +741,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const uint32_t p_parity = (nv / C::NB) & 1, v_parity = (t / C::ST) & 1;
         const uint32_t p_half = bar(&ctrl->p_half[buf]), p_full = bar(&ctrl->p_full[buf]), v_full = bar(&ctrl->v_full[st]),
                        v_ok = bar(&ctrl->v_ok[st]);
-        ok = poll([&]() { return mbar_test(p_half, p_parity) & mbar_test(v_full, v_parity) & mbar_test(v_ok, v_parity); });
+        ok = poll([&](auto test) { return test(p_half, p_parity) & test(v_full, v_parity) & test(v_ok, v_parity); });
         if (!ok) break;
         tc_fence_after();
         values(0);
         tc_commit(leader, bar(&ctrl->half_done[w][turn]));
         const bool last = pv.i + 1 == (w ? pv.of1 : pv.of0);
-        ok = poll([&]() {
-          s_ready = more_s && scores_ready();
-          return mbar_test(p_full, p_parity);
+        ok = poll([&](auto test) {
+          s_ready = more_s && scores_ready(look);
+          return test(p_full, p_parity);
         });
         if (!ok) break;
         s_ready = __all_sync(0xffffffffu, s_ready);
