@@ -25,3 +25,66 @@ def test_ordinary_waits_need_few_polls(d):
         out = attend(q, k, v, cu)
         assert kvq.kvq_get_device_error() == 0
         assert torch.equal(bits(out), bits(ref))
+
+
+def batch_with_a_bad_sequence(d, window, sinks, where, n=9000):
+    """Two prompts whose items are more than the SMs: the first one's values at `where` are not
+    finite; and the same with zeros there."""
+    cu = offsets([n, n])
+    q, k, v = projection(2 * n, 16, 4, d)
+    clean, v = v.clone(), v.clone()
+    clean[where], v[where] = 0.0, float("nan")
+    run = lambda x: attend(q, k, x, cu, None, window, sinks)
+    return run, clean, v
+
+
+def event_ms(call):
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    call()
+    b.record()
+    b.synchronize()
+    return a.elapsed_time(b)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (8192, 4), (2000, 300)])
+def test_a_sequence_of_nan_costs_the_others_nothing(d, window, sinks):
+    n = 9000
+    run, clean, v = batch_with_a_bad_sequence(d, window, sinks, slice(0, n))
+    ref, out = run(clean), run(v)
+    assert kvq.kvq_get_device_error() == 0
+    assert torch.equal(bits(out[n:]), bits(ref[n:]))
+    assert torch.isnan(out[:n]).all()
+    good, bad = (min(event_ms(lambda: run(x)) for _ in range(3)) for x in (clean, v))
+    assert bad < 5 * good + 1, f"{bad:.2f} ms with NaN, {good:.2f} without"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_not_finite_at_both_ends_of_a_wide_window(d, value):
+    """A kept key, one at a window's edge and one near the diagonal: the rows that see one of them
+    get it in its element, everything else keeps its bits; and in reasonable time when all of a
+    sequence's values are infinities of one sign, of which each row has to look at all."""
+    n, window, sinks = 9000, 4096, 4
+    run, clean, v = batch_with_a_bad_sequence(d, window, sinks, slice(0, 0))
+    at = {1: 3, 2000: 17, 2050: d - 1, 6000: 40, 8999: 5}  # key: element
+    for t, e in at.items():
+        clean[t, 0, e], v[t, 0, e] = 0.0, value
+    ref, out = run(clean), run(v)
+    assert kvq.kvq_get_device_error() == 0
+    p = torch.arange(n, device=DEV)
+    want = ref.clone()
+    for t, e in at.items():
+        sees = (p >= t) & ((p < t + window) | (t < sinks))
+        want[:n][sees, :4, e] = value
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    keep = ~torch.isnan(want)
+    assert torch.equal(bits(out)[keep], bits(want)[keep])
+    good = min(event_ms(lambda: run(clean)) for _ in range(3))
+    v[:n] = value
+    out = run(v)
+    assert kvq.kvq_get_device_error() == 0
+    assert torch.equal(bits(out[n:]), bits(ref[n:])) and not torch.isfinite(out[:n]).any()
+    bad = min(event_ms(lambda: run(v)) for _ in range(3))
+    assert bad < 30 * good + 1, f"{bad:.2f} ms, {good:.2f} with finite values"
