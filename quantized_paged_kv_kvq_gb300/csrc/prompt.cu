@@ -385,6 +385,7 @@ __device__ __noinline__ void store_not_finite(const PromptArgs& a, const volatil
     scale_result(w, o, mul);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
+      add_not_finite(w[e], up[e], down[e]);  // with what came from the tiles left as they were
       const uint32_t met = ((up[e] | down[e]) >> 15 & 0x00010001u) * 0xFFFFu;
       w[e] = (w[e] & ~met) | ((0x7F807F80u | (down[e] & ~up[e]) | (up[e] & down[e]) >> 9) & met);
     }

@@ -88,3 +88,26 @@ def test_values_not_finite_at_both_ends_of_a_wide_window(d, value):
     assert torch.equal(bits(out[n:]), bits(ref[n:])) and not torch.isfinite(out[:n]).any()
     bad = min(event_ms(lambda: run(v)) for _ in range(3))
     assert bad < 30 * good + 1, f"{bad:.2f} ms, {good:.2f} with finite values"
+
+
+@pytest.mark.parametrize("d,g", [(64, 1), (128, 4)])
+@pytest.mark.parametrize("a,b,window,sinks", [(500, 1000, 700, 0), (1000, 500, 700, 0), (2, 900, 300, 4), (1200, 1210, 0, 0)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinities_of_both_signs_make_nan(d, g, a, b, window, sinks, sign):
+    """One in a tile that every row of an item sees, the other in one that only some see."""
+    n, inf = 2000, sign * float("inf")
+    q, k, v = projection(n, g, 1, d)
+    clean, v = v.clone(), v.clone()
+    clean[[a, b], 0, 3] = 0.0
+    v[a, 0, 3], v[b, 0, 3] = -inf, inf
+    cu = np.array([0, n])
+    ref, out = (attend(q, k, x, cu, None, window, sinks) for x in (clean, v))
+    p = torch.arange(n, device=DEV)
+    sees = [(p >= t) & ((window == 0) | (p < t + window) | (t < sinks)) for t in (a, b)]
+    want = ref.clone()
+    want[sees[0], :, 3] = -inf
+    want[sees[1], :, 3] = inf
+    want[sees[0] & sees[1], :, 3] = float("nan")
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    keep = ~torch.isnan(want)
+    assert torch.equal(bits(out)[keep], bits(want)[keep])
