@@ -593,6 +593,11 @@ __device__ __forceinline__ long long slot_index(const DecodeArgs& a, long long W
 // Block formats, whose values may lie anywhere in float32's range: the slot's pair is
 // (m + log2 l, f), f the power of two that the normalised output was divided by to
 // bring its largest element into [1, 2).
+// Their sums of probabilities are held kSumUnit times as large: with pages of zeros, or of values
+// near 2^-100, each key at the maximum counts 2^110, and 2^18 of those would pass float32's
+// range (the sum of a range was infinite then, and what it was merged into NaN).  Times 2^-12
+// that takes 2^30 keys, and the smallest, 2^-112 beside values of 2^121, are still normal.
+constexpr float kSumUnit = 0x1p-12f;
 __device__ __forceinline__ float slot_factor(float largest) {
   const int e = (__float_as_int(largest) >> 23) - 127;  // largest >= 0
   return __int_as_float((min(max(e, -126), 126) + 127) << 23);
@@ -1216,7 +1221,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   const uint32_t meta_k = m_off + warp * C::KMF * fstr;
   const uint32_t meta_v = vm_off + warp * C::VMF * fstr;
   // this warp's kv-head scales (per-kv-head scales, when given, replace the tensor's)
-  const float vsc = is_asym(VF) || C::BLOCK ? 1.0f : (a.v_head_scale != nullptr ? a.v_head_scale[h] : a.v_scale);
+  const float vsc = C::BLOCK ? kSumUnit : is_asym(VF) ? 1.0f : (a.v_head_scale != nullptr ? a.v_head_scale[h] : a.v_scale);
   const float qks = (!is_asym(KF) && a.k_head_scale != nullptr) ? a.qk_base * a.k_head_scale[h]
                                                                 : a.qk_scale;
 
@@ -1508,9 +1513,12 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
         raise(mx0 - lift, mx1 - lift);
         products();
       }
-      l0 += sum0;
-      l1 += sum1;
-      if constexpr (!C::BLOCK) {
+      if constexpr (C::BLOCK) {
+        l0 = fmaf(sum0, kSumUnit, l0);
+        l1 = fmaf(sum1, kSumUnit, l1);
+      } else {
+        l0 += sum0;
+        l1 += sum1;
         z0 += pr[0] * vz0 + pr[2] * vz1;
         z1 += pr[1] * vz0 + pr[3] * vz1;
       }
