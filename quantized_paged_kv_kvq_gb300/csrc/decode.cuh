@@ -655,8 +655,14 @@ __device__ __forceinline__ void merge_slots(const DecodeArgs& a, int s, const Se
 #pragma unroll
         for (int u = 1; u < PU; ++u) bm = fmaxf(bm, ml[u][0]);
         // no slot in this batch (empty ranges; more ranges than tiles): nothing to
-        // add, and 2^(m - M) would be 2^(-inf + inf) while M is still -inf
-        if (bm == -INFINITY) continue;
+        // add, and 2^(m - M) would be 2^(-inf + inf) while M is still -inf.  A slot whose
+        // (m, l) holds a NaN is one, although the largest m does not show it.
+        if (bm == -INFINITY) {
+          float met = 0.f;
+#pragma unroll
+          for (int u = 0; u < PU; ++u) met += ml[u][0] + ml[u][1];
+          if (met == -INFINITY) continue;
+        }
         if (bm > M) {  // raise the running maximum, rescaling what was summed so far
           const float sc = fast_exp2(M - bm);
           Lsum *= sc;
