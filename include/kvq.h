@@ -214,7 +214,8 @@ kvq_status kvq_decode_workspace_size(const kvq_cache_desc* cache, int32_t num_se
  *   16-bit cache keeps the bf16 query).  Probabilities enter them in 16 bits too, below
  *   2^-25 of the largest as 0 (symmetric formats: 4,096 such keys weigh 1.2e-4); of
  *   asymmetric and block formats times the row's or page's scale, by a power of two that keeps
- *   the product in range whatever the scale is (a page's: from 2^-100 on).
+ *   the product in range whatever the scale is (a page's: from 2^-100 to 2^100; keys that
+ *   weigh less than 2^-34 of the largest probability times scale do not count).
  */
 kvq_status kvq_paged_decode(const kvq_cache_desc* cache, const void* k_cache,
                             const void* v_cache, void* out, const void* query,
@@ -581,14 +582,13 @@ kvq_status kvq_decode_window(const kvq_cache_desc* cache, void* k_cache, void* v
  *   total_q allows some hundred rows a sequence or more, the contexts of that many
  *   sequences dequantized to 16 bits (4 bytes x sequences x max_context_len, rounded up
  *   to 128, x num_kv_heads x head_dim, up to 16 GiB: a tight max_context_len keeps it
- *   small).
+ *   small; block formats 1.5 bytes for a kv-head's 4 head_dim more).
  * One to three launches on the stream; may be captured into a CUDA graph.
  * Arithmetic: 16-bit operands in the tensor cores, float32 sums and softmax.
  *   int8 and FP8 codes are exact in fp16; asymmetric rows are rounded once to fp16
  *   when they are dequantized ((code * scale + zero_point) [* sigma] past 65504 is
- *   infinite; only the result counts, not the product on the way); so are those of the
- *   block formats (code * scale: what is past 65504 is infinite, below 2^-25 zero; the
- *   decode keeps the scale apart and takes any);
+ *   infinite; only the result counts, not the product on the way); codes of the block formats
+ *   are exact, their pages' scales multiply scores and probabilities as in the decode;
  *   the query is rounded to fp16 as in kvq_paged_decode (KVQ_DEVERR_QUERY_RANGE);
  *   probabilities are rounded to fp16.  The 16-bit cache uses bf16 throughout.
  *   A value (V) that is not finite makes the rows that see it not finite; rows

@@ -251,10 +251,12 @@ struct PrefillShape {
 // Measured ahead / not, 32 / 8 heads of 128: int8, 8 x 4,096 keys: 4 row tiles 160 /
 // 138 us, 8 257 / 257, 1 x 8,192 keys and 32 tiles 193 / 217; KVarN, 16 x 4,096 keys:
 // 2 tiles 223 / 222, 8 x 4,096: 4 tiles 182 / 210, 8 289 / 389; int4 4 tiles 165 / 177;
-// bf16 as int8; e4m3 per page, 8 x 4,096: 3 tiles 164 / 160, 4 165 / 164, 6 215 / 232, 8
-// 264 / 287, 32 x 2,048: 3 283 / 248, 4 318 / 304, 6 431 / 425, 8 513 / 541.
-constexpr int64_t stage_tiles(int fmt) { return is_asym(fmt) ? 3 : is_block(fmt) ? 5 : 8; }
+// bf16 as int8; int8 per page, 8 x 4,096: 4 tiles 168 / 142, 6 221 / 207, 8 272 / 269,
+// 32 x 2,048: 6 431 / 412, 8 521 / 519, 1 x 8,192 keys and 32 tiles 205 / 229.
+constexpr int64_t stage_tiles(int fmt) { return is_asym(fmt) ? 3 : 8; }
 constexpr int64_t kStageBytes = 16ll << 30;
+// Bytes of a tile of 128 keys' scales behind them: three float32 for every 8 (block formats).
+constexpr size_t stage_scale_bytes(int fmt) { return is_block(fmt) ? 3 * 128 / 8 * 4 : 0; }
 // What can be said of a batch's sizes without a device.
 kvq_status check_prefill(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
                          int64_t total_q, int32_t max_query_len, int32_t max_context_len) {
@@ -295,7 +297,7 @@ kvq_status prefill_shape(const kvq_cache_desc* c, int32_t num_seqs, int32_t num_
   if (sh->rows == 256 && total_q * g >= stage_tiles(c->k_fmt) * 256 * num_seqs && 2 * rows <= INT32_MAX &&
       num_seqs * (len / 128) <= INT32_MAX && hkv <= 65535 && 2 * rows * c->head_dim * 2 <= kStageBytes) {
     sh->staged_len = static_cast<int>(len);
-    sh->staged = (static_cast<size_t>(2 * rows) * c->head_dim * 2 + rows / 128 + 15) / 16 * 16;
+    sh->staged = (static_cast<size_t>(2 * rows) * c->head_dim * 2 + rows / 128 * (stage_scale_bytes(c->k_fmt) + 1) + 15) / 16 * 16;
     sh->workspace += sh->staged;
   }
   return KVQ_OK;
@@ -325,7 +327,7 @@ kvq_status prefill_workspace(const kvq_cache_desc* c, int32_t num_seqs, int32_t 
     const int64_t len = (max_context_len + 127ll) / 128 * 128;
     const int64_t seqs = std::min<int64_t>(num_seqs, total_q * g / (stage_tiles(c->k_fmt) * 256));
     const int64_t rows = std::min(std::min<int64_t>(seqs * hkv * len, INT32_MAX / 2), kStageBytes / (4 * d));
-    *bytes += (static_cast<size_t>(2 * rows) * d * 2 + rows / 128 + 15) / 16 * 16;
+    *bytes += (static_cast<size_t>(2 * rows) * d * 2 + rows / 128 * (stage_scale_bytes(c->k_fmt) + 1) + 15) / 16 * 16;
   }
   return KVQ_OK;
 }
@@ -935,7 +937,7 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
   a.k_head_scale = cache->k_head_scales;
   a.v_head_scale = cache->v_head_scales;
   a.k_scale = scaled(cache->k_fmt) ? cache->k_scale : 1.0f;
-  a.v_scale = scaled(cache->v_fmt) ? cache->v_scale : 1.0f;
+  a.v_scale = scaled(cache->v_fmt) ? cache->v_scale : is_block(cache->v_fmt) ? kSumUnit : 1.0f;  // over the row's sum
   a.sm_scale_log2 = sm_scale * kLog2e;
   a.cR = rotation_scale(cache->head_dim);
   a.num_seqs = num_seqs;
@@ -954,7 +956,10 @@ kvq_status kvq_paged_prefill(const kvq_cache_desc* cache, const void* k_cache, c
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.staged = sh.staged ? reinterpret_cast<uint16_t*>(ws) : nullptr;
   a.staged_len = sh.staged_len;
-  a.staged_bad = ws + static_cast<size_t>(2) * num_seqs * cache->num_kv_heads * sh.staged_len * cache->head_dim * 2;
+  const size_t staged_rows = static_cast<size_t>(num_seqs) * cache->num_kv_heads * sh.staged_len;
+  uint8_t* const behind = ws + 2 * staged_rows * cache->head_dim * 2;
+  a.staged_scales = reinterpret_cast<float*>(behind);
+  a.staged_bad = behind + staged_rows / 128 * stage_scale_bytes(cache->k_fmt);
   a.ws_out = reinterpret_cast<float*>(ws + sh.staged);
   a.ws_ml = a.ws_out + sh.partial_rows * cache->head_dim;
   bound_waits(&a, kPrefillSpinLimit);

@@ -593,11 +593,6 @@ __device__ __forceinline__ long long slot_index(const DecodeArgs& a, long long W
 // Block formats, whose values may lie anywhere in float32's range: the slot's pair is
 // (m + log2 l, f), f the power of two that the normalised output was divided by to
 // bring its largest element into [1, 2).
-// Their sums of probabilities are held kSumUnit times as large: with pages of zeros, or of values
-// near 2^-100, each key at the maximum counts 2^110, and 2^18 of those would pass float32's
-// range (the sum of a range was infinite then, and what it was merged into NaN).  Times 2^-12
-// that takes 2^30 keys, and the smallest, 2^-112 beside values of 2^121, are still normal.
-constexpr float kSumUnit = 0x1p-12f;
 __device__ __forceinline__ float slot_factor(float largest) {
   const int e = (__float_as_int(largest) >> 23) - 127;  // largest >= 0
   return __int_as_float((min(max(e, -126), 126) + 127) << 23);

@@ -18,6 +18,12 @@ __host__ __device__ constexpr bool is_asym(int f) { return f == INT4A || f == UI
 // A float32 scale per (page, kv-head), and what its codes are.
 __host__ __device__ constexpr bool is_block(int f) { return f == INT8B || f == E4M3B; }
 __host__ __device__ constexpr int code_fmt(int f) { return f == INT8B ? INT8 : f == E4M3B ? E4M3 : f; }
+// Attention over block formats holds sums of probabilities kSumUnit times as large: with pages
+// of zeros, or of values near 2^-100, each key at the maximum counts 2^110, and 2^18 of those
+// would pass float32's range (in the decode a range's sum was infinite then, and what it was
+// merged into NaN).  Times 2^-12 that takes 2^30 keys, and the smallest, 2^-112 beside values of
+// 2^121, are still normal.
+constexpr float kSumUnit = 0x1p-12f;
 // Scales of a page: one per kv-head, the row padded to 16 bytes.
 __host__ __device__ constexpr int scale_pitch(int num_kv_heads) { return (num_kv_heads + 3) / 4 * 4; }
 __host__ __device__ constexpr int row_bytes(int f, int d) {

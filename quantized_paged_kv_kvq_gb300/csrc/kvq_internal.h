@@ -218,6 +218,7 @@ struct PrefillArgs {
   // 128 keys): values that are not finite.
   uint16_t* staged;
   uint8_t* staged_bad;
+  float* staged_scales;  // block formats: per (sequence, kv-head, 128 keys) 16 of K, of V, and their log2
   int staged_len;  // a multiple of 128
   // Bounded waits, as in DecodeArgs: polls of an mbarrier, and the test hook: CTA
   // (withhold_cta, 0) waits for what nothing signals in place of K tile withhold_tile.

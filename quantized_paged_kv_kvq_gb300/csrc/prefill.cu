@@ -70,13 +70,23 @@ constexpr float kLazy = 8.0f;         // a maximum that grows by less (log2) is 
 // dominates (often a first token whose own value is next to nothing).
 constexpr float kLift = 7.0f;
 
-// head_dim, rows, keys dequantized ahead, block formats (in instances of their own: beside
-// the other formats' their conversion cost those 2 %)
+// Block formats: codes are exact operands, as those of the other 8-bit formats, and a page's
+// scales, which may lie anywhere in float32's range, stay out of them: K's multiplies the
+// score, V's the probability.  p times V's scale is the 16-bit operand, so the row's m is the
+// largest z + log2(scale) less kBlockLift, and raised when one passes 2^15; but never lower
+// than the largest z less kBlockMost, so that the sum stays in range where all values are zeros.
+// (Folded into the operands, rows past 65,504 were infinite and those below 2^-14 lost bits.)
+constexpr float kBlockLift = 9.0f, kBlockRaise = 15.0f;
+constexpr float kBlockMost = 100.0f;
+// Scales of a tile, one of each for 8 keys: of the scores (sm_scale and log2(e) with it), of the
+// values, and those' log2.  A ring of kScaleSlots tiles: slots are written up to four tiles
+// ahead of the products and read until a tile's softmax is done, up to two behind them.
+constexpr int kGroups = kKeys / 8, kScaleBytes = 3 * kGroups * 4, kScaleSlots = 8;
+
+// head_dim, rows, keys dequantized ahead, block formats
 template <int D_, int ROWS_, bool STAGED = false, bool BLOCK_ = false>
 struct Cfg {
   static constexpr bool BLOCK = BLOCK_;
-  // whether fmt is a block format (keys dequantized ahead: of any)
-  static __device__ __forceinline__ bool block(int fmt) { return BLOCK || (STAGED && is_block(fmt)); }
   static constexpr int D = D_, ROWS = ROWS_;
   static constexpr int NW = ROWS == 256 ? 2 : 1;  // softmax warpgroups
   static constexpr int THREADS = 128 * NW + (STAGED ? 0 : 2 * kProducers) + 128;
@@ -97,6 +107,7 @@ struct Cfg {
   static constexpr int RAWQ = V + 2 * TILE;
   static constexpr int META = RAWQ + (STAGED ? 0 : (AHEAD_K + AHEAD_V) * RAW);  // slots of K, then of V
   static constexpr int CTRL = META + (AHEAD_K + AHEAD_V) * 3 * kKeys * 2;
+  static_assert(kScaleSlots * kScaleBytes <= CTRL - META, "the ring of tiles' scales lies where other formats' metadata does");
   static constexpr int SIGNS = CTRL + 256;  // the rotation's diagonal as masks of pairs of sign bits
   static constexpr int SMEM = SIGNS + 2 * D + 1024;
   // tensor memory columns: two score buffers (one per warpgroup, or the two that one
@@ -113,7 +124,8 @@ struct Cfg {
 
 // Control words in shared memory.
 struct Ctrl {
-  unsigned long long q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], pv_done, o_full[2], drained;
+  unsigned long long q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], pv_done, o_full[2], drained,
+      scales[kScaleSlots];
   uint32_t tmem;
   int abort;
   int seq, tile, q0, q, n;  // this CTA's rows
@@ -230,14 +242,13 @@ __device__ __forceinline__ int tile_key(const Span& s, int i) { return kKeys * (
 
 // A row's fields, each an fp16 value twice, as dequantize16 takes them.  Rotated rows:
 // scale and zero point times the deviation, in float32 (products of 11 bits each: exact).
-// Block formats: the bits of the page's scale, a float32, in the first.
-template <int F, bool KVARN>
+template <bool KVARN>
 struct RowFields {
   uint32_t s, z;
   __device__ __forceinline__ RowFields(uint32_t scale, uint32_t zero, uint32_t) : s(scale), z(zero) {}
 };
-template <int F>
-struct RowFields<F, true> {
+template <>
+struct RowFields<true> {
   float s, z;
   __device__ __forceinline__ RowFields(uint32_t scale, uint32_t zero, uint32_t deviation) {
     const float g = __half2float(__ushort_as_half(static_cast<uint16_t>(deviation)));
@@ -249,10 +260,9 @@ struct RowFields<F, true> {
 // 16 bytes of codes as 16-bit operands: 16 (8-bit codes) or 32 (int4) fp16
 // values, in order.  Asymmetric rows are rounded once, to fp16: code * scale + zero
 // point by a fused fp16 operation, rotated rows (code * (scale * deviation) + zero point *
-// deviation) in float32, where code * scale may pass fp16's range on the way; rows of block
-// formats too, code * scale in float32.
+// deviation) in float32, where code * scale may pass fp16's range on the way.
 template <int F, bool KVARN>
-__device__ __forceinline__ void dequantize16(const uint4& raw, const RowFields<F, KVARN>& row,
+__device__ __forceinline__ void dequantize16(const uint4& raw, const RowFields<KVARN>& row,
                                              uint32_t (&o)[F == INT4A ? 16 : 8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   constexpr uint32_t K64 = 0x64646464u;
@@ -290,30 +300,6 @@ __device__ __forceinline__ void dequantize16(const uint4& raw, const RowFields<F
     } else if constexpr (F == E5M2) {
       o[2 * i] = prmt(w[i], 0u, 0x1404);
       o[2 * i + 1] = prmt(w[i], 0u, 0x3424);
-    } else if constexpr (is_block(F)) {
-      const float s = __uint_as_float(row.s);
-      float x[4];
-      if constexpr (F == INT8B) {  // 2^23 + (code + 128), less both
-        const uint32_t b = w[i] ^ 0x80808080u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(prmt(b, 0x4B000000u, 0x7440u + e));
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) add2(x[e], x[e + 1], x[e], x[e + 1], -8388736.f, -8388736.f);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t h = e4m3x2_to_f16x2((w[i] >> (16 * e)) & 0xFFFFu);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          x[2 * e] = f.x;
-          x[2 * e + 1] = f.y;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        float u, v;
-        mul2(u, v, x[e], x[e + 1], s, s);
-        o[2 * i + e / 2] = pack_half2(u, v);
-      }
     } else if constexpr (F == UINT8A) {
       affine2(w[i], o + 2 * i);
     } else {  // INT4A: element 2i in the low nibble of byte i
@@ -362,11 +348,6 @@ __device__ __forceinline__ uint4 ldsv4(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
   return r;
 }
-__device__ __forceinline__ uint32_t lds_word(uint32_t a) {
-  uint32_t r;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
-  return r;
-}
 __device__ __forceinline__ uint32_t lds_pair(uint32_t a) {  // a 16-bit value, twice
   uint16_t r;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
@@ -402,7 +383,7 @@ __device__ __forceinline__ Source make_source(const uint8_t* cache, const __half
   s.token_bytes = hkv * rb;
   s.page_bytes = static_cast<uint32_t>(bs) * s.token_bytes;  // below 2^31: checked on the host
   s.fmt = fmt;
-  s.fields = is_asym(fmt) ? (kvarn ? 3 : 2) : block ? 1 : 0;
+  s.fields = is_asym(fmt) ? (kvarn ? 3 : 2) : 0;
   s.meta = is_asym(fmt) ? meta + static_cast<size_t>(h) * s.fields * bs : block ? meta + 2 * h : nullptr;
   s.meta_page = block ? scale_pitch(hkv) : static_cast<uint32_t>(hkv) * s.fields * bs;
   return s;
@@ -439,6 +420,24 @@ struct Pieces {
     row0 = tid / CL % RL + RL * (tid / (8 * CH));
   }
 };
+
+// Whether some row sees one of the 8 keys from t on.
+__device__ __forceinline__ bool group_needed(const PrefillArgs& a, const Span& span, int t) {
+  return t <= span.p_hi && (t + 7 >= span.win || t < a.sinks);
+}
+// What the softmax takes of a group's scale of K: times sm_scale log2(e) (scale > 0), and never
+// 0, so that a masked score stays -inf.  Not a number: the rows that see the group get NaN at
+// the end (bad), the others' scores are not touched.
+__device__ __forceinline__ float key_scale(float scale, float of_page, bool& bad) {
+  const float f = scale * of_page;
+  bad = of_page != of_page;
+  return f >= 1.17549435e-38f ? f : 1.17549435e-38f;
+}
+// Of V: 0 where it is not finite, as such values are zeroed, too.
+__device__ __forceinline__ float value_scale(float of_page, bool& bad) {
+  bad = !isfinite(of_page);
+  return bad ? 0.f : of_page;
+}
 
 // The producer warpgroup's view of one key tile.
 struct KeyTile {
@@ -509,12 +508,7 @@ struct Producer {
     if (!C::BLOCK && s.fmt == BF16) copy_codes<BF16>(s, k, slot, dst);
     else if (!C::BLOCK && s.fmt == INT4A) copy_codes<INT4A>(s, k, slot, dst);
     else copy_codes<INT8>(s, k, slot, dst);  // any 8-bit code
-    if (C::BLOCK) {  // a token per thread: its page's scale
-      const int blk = __shfl_sync(0xffffffffu, k.block, tid >> a.block_shift);
-      cp_async_or_zero<4>(smem + C::META + slot * 3 * kKeys * 2 + tid * 4,
-                          reinterpret_cast<const float*>(s.meta) + static_cast<unsigned long long>(static_cast<uint32_t>(blk)) * s.meta_page,
-                          needed(k.t0 + tid));
-    } else if (s.fields > 0) {  // a pair of tokens per thread and field
+    if (s.fields > 0) {  // a pair of tokens per thread and field
       const int row = 2 * (tid & 63), t = k.t0 + row;
       const int blk = __shfl_sync(0xffffffffu, k.block, row >> a.block_shift);
       const __half* src = s.meta + static_cast<unsigned long long>(static_cast<uint32_t>(blk)) * s.meta_page +
@@ -524,6 +518,15 @@ struct Producer {
         cp_async_or_zero<4>(smem + C::META + (slot * 3 + f) * kKeys * 2 + row * 2, src + (f << a.block_shift), read);
     }
   }
+  // Block formats, by the first warp: start copying the scales of the tile's groups of 8 keys
+  // (lanes 0-15 K's, 16-31 V's; 0 for groups that no row sees) into their slot.
+  __device__ __forceinline__ void copy_scales(const Source& ks, const Source& vs, const KeyTile& k, uint32_t to) const {
+    const int g = tid % kGroups;
+    const int blk = __shfl_sync(0xffffffffu, k.block, (8 * g) >> a.block_shift);
+    const Source& s = tid < kGroups ? ks : vs;
+    cp_async_or_zero<4>(to + tid * 4, reinterpret_cast<const float*>(s.meta) + static_cast<unsigned long long>(static_cast<uint32_t>(blk)) * s.meta_page,
+                        group_needed(a, span, k.t0 + 8 * g));
+  }
   // The pieces in slot `slot` as operands; whether one may not be finite (of V,
   // and of formats that can hold such a value; large asymmetric rows count too).
   template <int F, bool KVARN, bool IS_V>
@@ -531,8 +534,7 @@ struct Producer {
     using P = Pieces<F, C::D>;
     const P p(tid);
     const uint32_t raw = smem + C::RAWQ + slot * C::RAW + tid * 16;
-    constexpr int MB = is_block(F) ? 4 : 2;  // bytes of a row's field
-    const uint32_t meta = smem + C::META + slot * 3 * kKeys * 2 + p.row0 * MB;
+    const uint32_t meta = smem + C::META + slot * 3 * kKeys * 2 + p.row0 * 2;
     const bool all = !is_asym(F) || all_needed(k.t0);
     uint32_t to[P::OUT];
 #pragma unroll
@@ -556,7 +558,6 @@ struct Producer {
             if (KVARN) sg[u] = lds_pair(meta + (2 * kKeys + i * P::STEP) * 2);
           }
         }
-        if constexpr (is_block(F)) sc[u] = lds_word(meta + i * P::STEP * MB);  // 0 for a row that no one sees
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -607,7 +608,7 @@ struct Producer {
   template <bool IS_V>
   __device__ __forceinline__ bool finish(const Source& s, const KeyTile& k, int slot, uint32_t dst) const {
     if constexpr (C::BLOCK) {
-      return s.fmt == INT8B ? convert<INT8B, false, IS_V>(k, slot, dst) : convert<E4M3B, false, IS_V>(k, slot, dst);
+      return s.fmt == INT8B ? convert<INT8, false, IS_V>(k, slot, dst) : convert<E4M3, false, IS_V>(k, slot, dst);
     } else {
       switch (s.fmt) {
         case INT8: return convert<INT8, false, IS_V>(k, slot, dst);
@@ -681,6 +682,75 @@ __device__ __forceinline__ float probabilities(uint32_t s_addr, float scale, flo
       y = fast_exp2(y);
       add2(sum[e & 2], sum[(e & 2) + 1], sum[e & 2], sum[(e & 2) + 1], x, y);
       p[e / 2] = BF ? pack_bf162(x, y) : pack_half2(x, y);
+    }
+    tmem_st32(s_addr + c0 / 2, p);  // over scores that have been read
+    if (c0 == 0 && half_bar != 0) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(half_bar);
+    }
+  }
+  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+__device__ __forceinline__ void lds_floats8(float (&x)[8], uint32_t a) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 w = ldsv4(a + 16 * i);
+    x[4 * i] = __uint_as_float(w.x);
+    x[4 * i + 1] = __uint_as_float(w.y);
+    x[4 * i + 2] = __uint_as_float(w.z);
+    x[4 * i + 3] = __uint_as_float(w.w);
+  }
+}
+// Block formats, with a tile's scales at `scales`: the largest logit, and the largest plus the
+// log2 of its value's scale.
+__device__ __forceinline__ void largest_logits(uint32_t s_addr, uint32_t scales, float& top, float& weighted) {
+  top = weighted = -INFINITY;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kKeys; c0 += 64) {
+    uint32_t s[64];
+    tmem_ld32(s, s_addr + c0);
+    tmem_ld32(s + 32, s_addr + c0 + 32);
+    float f[8], lv[8];
+    lds_floats8(f, scales + c0 / 8 * 4);
+    lds_floats8(lv, scales + (2 * kGroups + c0 / 8) * 4);
+    tmem_wait_ld32(s);
+    tmem_waited32(s + 32);
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const uint32_t* x = s + 8 * g;
+      float mx = max3f(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+      mx = max3f(mx, __uint_as_float(x[3]), __uint_as_float(x[4]));
+      mx = max3f(mx, __uint_as_float(x[5]), __uint_as_float(x[6]));
+      const float z = fmaxf(mx, __uint_as_float(x[7])) * f[g];
+      top = fmaxf(top, z);
+      weighted = fmaxf(weighted, z + lv[g]);
+    }
+  }
+}
+// probabilities of block formats: p = 2^(s * its scale + off), handed over times the value's.
+__device__ __forceinline__ float probabilities_scaled(uint32_t s_addr, uint32_t scales, float off, uint32_t half_bar, int lane) {
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int c0 = 0; c0 < kKeys; c0 += 64) {
+    uint32_t s[64], p[32];
+    tmem_ld32(s, s_addr + c0);
+    tmem_ld32(s + 32, s_addr + c0 + 32);
+    float f[8], v[8];
+    lds_floats8(f, scales + c0 / 8 * 4);
+    lds_floats8(v, scales + (kGroups + c0 / 8) * 4);
+    tmem_wait_ld32(s);
+    tmem_waited32(s + 32);
+#pragma unroll
+    for (int e = 0; e < 64; e += 2) {
+      float x, y;
+      fma2(x, y, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), f[e / 8], f[e / 8], off, off);
+      x = fast_exp2(x);
+      y = fast_exp2(y);
+      add2(sum[e & 2], sum[(e & 2) + 1], sum[e & 2], sum[(e & 2) + 1], x, y);
+      mul2(x, y, x, y, v[e / 8], v[e / 8]);
+      p[e / 2] = pack_half2(x, y);
     }
     tmem_st32(s_addr + c0 / 2, p);  // over scores that have been read
     if (c0 == 0 && half_bar != 0) {
@@ -810,7 +880,7 @@ template <class C>
 __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& span, int seq, int h, int p, int i_lo,
                                              int i_hi, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   const int bs = 1 << a.block_shift;
-  const Source s = make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, C::D, a.num_kv_heads, h, bs, C::block(a.v_fmt));
+  const Source s = make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, C::D, a.num_kv_heads, h, bs, C::BLOCK);
   for (int i = i_lo; i <= i_hi; ++i) {
     const int t0 = tile_key(span, i);
     for (int t = t0; t < t0 + kKeys && t <= p; ++t) {
@@ -821,8 +891,10 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
       const uint8_t* row = s.codes + static_cast<size_t>(blk) * s.page_bytes + static_cast<size_t>(off) * s.token_bytes;
       __half sc{}, zp{}, sg{};
       float ps = 0.f;
-      if (C::block(s.fmt)) {
-        ps = reinterpret_cast<const float*>(s.meta)[static_cast<size_t>(blk) * s.meta_page];
+      if (C::BLOCK) {
+        const size_t at = static_cast<size_t>(blk) * s.meta_page + h;
+        const float ks = reinterpret_cast<const float*>(a.k_meta)[at];
+        ps = ks != ks ? ks : reinterpret_cast<const float*>(a.v_meta)[at];
       } else if (s.fields > 0) {
         const __half* m = s.meta + static_cast<size_t>(blk) * s.meta_page + off;
         sc = m[0];
@@ -839,10 +911,12 @@ __device__ __noinline__ void find_not_finite(const PrefillArgs& a, const Span& s
           v = static_cast<uint32_t>(row[d]) << 8;
         } else if (s.fmt == E4M3) {
           v = e4m3x2_to_f16x2(row[d]) & 0xFFFFu;
-        } else if (C::block(s.fmt)) {  // as dequantize16
+        } else if (C::BLOCK) {
           const float c = s.fmt == INT8B ? static_cast<float>(static_cast<int8_t>(row[d]))
                                          : __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_to_f16x2(row[d]))));
-          v = __half_as_ushort(__float2half_rn(c * ps));
+          if (isfinite(ps) && isfinite(c)) continue;
+          const float x = c * ps;
+          v = x != x ? 0x7FFFu : x < 0.f ? 0xFC00u : 0x7C00u;
         } else if (s.fields > 0) {
           const int c = s.fmt == INT4A ? (row[d / 2] >> (4 * (d & 1))) & 15 : row[d];
           __half x = __hfma(__int2half_rn(c), sc, zp);  // as dequantize16
@@ -936,6 +1010,8 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
     }
     mbar_init(bar(&ctrl->pv_done), 1);
     mbar_init(bar(&ctrl->drained), 1);
+    if (C::BLOCK)
+      for (int i = 0; i < kScaleSlots; ++i) mbar_init(bar(&ctrl->scales[i]), 1);
     ctrl->abort = 0;
     ctrl->bad_lo = 0x7fffffff;
     ctrl->bad_hi = -1;
@@ -944,6 +1020,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
   if (a.kvarn && tid < D / 2)
     reinterpret_cast<uint32_t*>(smem + C::SIGNS)[tid] =
         a.signs == nullptr ? 0u : (a.signs[2 * tid] < 0 ? 0x8000u : 0u) | (a.signs[2 * tid + 1] < 0 ? 0x80000000u : 0u);
+  if (STAGED && BLOCK) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // find_tile's words, before copies over them
   __syncthreads();
   const size_t seq_head = static_cast<size_t>(seq) * a.num_kv_heads + h;
   if constexpr (STAGED) {  // tiles whose values were not all finite
@@ -961,6 +1038,8 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
     tc_fence_after();
   }
   const uint32_t tmem = ctrl->tmem;
+  auto scale_slot = [&](int i) { return base + C::META + (i % kScaleSlots) * kScaleBytes; };
+  const float abs_scale = a.sm_scale_log2 == 0.f ? 1.f : fabsf(a.sm_scale_log2);  // of block formats' scores
   auto give_up = [&]() {
     raise_error(16u);  // KVQ_DEVERR_TIMEOUT: the results of this launch are invalid
     *abort = 1;
@@ -995,6 +1074,10 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
         // each way for either: its warps may be a tile apart.
         const int buf = NW == 2 ? wg : i & 1;
         const uint32_t s_addr = NW == 2 ? s_first : s_first + buf * 128;
+        if (BLOCK && !__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->scales[i % kScaleSlots]), (i / kScaleSlots) & 1, spin, abort))) {
+          give_up();
+          break;
+        }
         if (!__all_sync(0xffffffffu, mbar_wait_or_abort(bar(&ctrl->s_full[buf]), (NW == 2 ? i : i >> 1) & 1, spin, abort))) {
           give_up();
           break;
@@ -1008,9 +1091,14 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
           const int last = pos - t0;
           mask_scores(s_addr, last, a.window > 0 ? last - a.window + 1 : -1, a.sinks - t0);
         }
-        const float top = largest_score(s_addr) * scale;
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          const float up = fmaxf(m, top);
+        float top, weighted = -INFINITY;
+        if constexpr (BLOCK) {
+          largest_logits(s_addr, scale_slot(i), top, weighted);
+        } else {
+          top = largest_score(s_addr) * scale;
+        }
+        if (__any_sync(0xffffffffu, BLOCK ? weighted > m + kBlockRaise || top > m + (kBlockMost + 8.f) : top > m + kLazy)) {
+          const float up = fmaxf(m, BLOCK ? fmaxf(weighted - kBlockLift, top - kBlockMost) : top);
           const float f = up == -INFINITY ? 1.f : fast_exp2(m - up);
           m = up;
           l *= f;
@@ -1029,10 +1117,11 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
             scale_columns(o_addr, D, f);
           }
         }
-        const float off = m == -INFINITY ? 0.f : kLift - m;  // a row that has seen nothing: every p is 0
+        const float off = m == -INFINITY ? 0.f : (BLOCK ? 0.f : kLift) - m;  // a row that has seen nothing: every p is 0
         const uint32_t half_bar = NW == 2 ? bar(&ctrl->p_half[wg]) : 0u;
-        l += bf ? probabilities<true>(s_addr, scale, off, half_bar, lane)
-                : probabilities<false>(s_addr, scale, off, half_bar, lane);
+        if constexpr (BLOCK) l = fmaf(probabilities_scaled(s_addr, scale_slot(i), off, half_bar, lane), kSumUnit, l);
+        else l += bf ? probabilities<true>(s_addr, scale, off, half_bar, lane)
+                     : probabilities<false>(s_addr, scale, off, half_bar, lane);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -1138,6 +1227,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
       const bool is_v = wg == NW + 1;
       const Source src = is_v ? make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs, C::BLOCK)
                               : make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs, C::BLOCK);
+      const Source v_src = BLOCK && !is_v ? make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs, true) : src;
       const Producer<C> pr{a, span, base, tid & 127, seq};
       const uint32_t operand = base + (is_v ? C::V : C::K);
       unsigned long long* full = is_v ? ctrl->v_full : ctrl->k_full;
@@ -1159,6 +1249,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
           pr.check(cur);
           if (i + 1 < nk) next = pr.look_up(i0 + i + 1);
           pr.copy(src, cur, slot0 + (ahead == 2 ? i & 1 : 0), operand + (i & 1) * C::TILE);
+          if (BLOCK && warp == 4 * NW) pr.copy_scales(src, v_src, cur, scale_slot(i));
         }
         cp_async_commit();
       };
@@ -1168,6 +1259,21 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
         bool ok = bf || wait_empty(i);
         if (src.fields > 0) ok = producers_all(is_v, ok);  // and the metadata that other threads copied is there
         if (!ok) break;
+        if (BLOCK && warp == 4 * NW) {  // the tile's scales, which this warp's lanes copied
+          const uint32_t at = scale_slot(i) + lane * 4;
+          bool bad;
+          uint32_t x;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+          const float f = lane < kGroups ? key_scale(abs_scale, __uint_as_float(x), bad) : value_scale(__uint_as_float(x), bad);
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(f) : "memory");
+          if (lane >= kGroups) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + kGroups * 4), "f"(__log2f(fabsf(f))) : "memory");
+          if (bad) {
+            atomicMin(&ctrl->bad_lo, i0 + i);
+            atomicMax(&ctrl->bad_hi, i0 + i);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&ctrl->scales[i % kScaleSlots]));
+        }
         const int slot = slot0 + (ahead == 2 ? i & 1 : 0);
         const uint32_t dst = operand + (i & 1) * C::TILE;
         const KeyTile ready{tile_key(span, i0 + i), 0};
@@ -1209,6 +1315,14 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
           const uint32_t full = bar(is_v ? &ctrl->v_full[st] : &ctrl->k_full[st]);
           const uint32_t dst = base + (is_v ? C::V : C::K) + st * C::TILE;
           const int y = row0 + tile_key(span, i0 + i) + (is_v ? rows : 0);
+          if (BLOCK && !is_v) {
+            const uint32_t there = bar(&ctrl->scales[i % kScaleSlots]);
+            mbar_arrive_expect(there, kScaleBytes);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(scale_slot(i)),
+                         "l"(a.staged_scales + (row0 + tile_key(span, i0 + i)) / kKeys * static_cast<size_t>(3 * kGroups)),
+                         "r"(kScaleBytes), "r"(there)
+                         : "memory");
+          }
           mbar_arrive_expect(full, C::TILE);
 #pragma unroll
           for (int g = 0; g < C::GROUPS; ++g)
@@ -1222,6 +1336,9 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
         // Leave with no copy in flight, whoever gave up: the last of each stage is there.
         for (int t = max(issued - 4, 0); t < issued; ++t)
           mbar_wait(bar((t & 1) ? &ctrl->v_full[t >> 1 & 1] : &ctrl->k_full[t >> 1 & 1]), (t >> 2) & 1, kDrain);
+        const int scaled = BLOCK ? (issued + 1) / 2 : 0;
+        for (int t = max(scaled - kScaleSlots, 0); t < scaled; ++t)
+          mbar_wait(bar(&ctrl->scales[t % kScaleSlots]), (t / kScaleSlots) & 1, kDrain);
       }
       __syncwarp();
     }
@@ -1322,7 +1439,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, STAGED, BLOCK>::THREADS, 1)
 
 // The contexts' rows that some row of the batch sees as 16-bit operands in memory,
 // [S, Hkv, staged_len, D] of K and then of V, by whole tiles of 128 keys (rows that
-// no one sees are 0).  A CTA per (sequence, tile) and kv-head: half its threads K, half V.
+// no one sees are 0; block formats: codes, and their scales apart).  A CTA per (sequence, tile) and kv-head: half its threads K, half V.
 // Worth its writes where many row tiles read the same keys.
 template <int D, int F, bool KVARN, bool IS_V>
 __device__ __forceinline__ bool stage_tile(const PrefillArgs& a, const Source& s, const Span& span, const int* pages,
@@ -1347,7 +1464,6 @@ __device__ __forceinline__ bool stage_tile(const PrefillArgs& a, const Source& s
       o[3] = w.w;
     } else {
       uint32_t f[3] = {0, 0, 0};
-      if (is_block(F) && need) f[0] = __float_as_uint(reinterpret_cast<const float*>(s.meta)[blk * s.meta_page]);
       if (is_asym(F) && need) {
         const __half* m = s.meta + blk * s.meta_page + (row & mask);
 #pragma unroll
@@ -1376,11 +1492,11 @@ template <int D, bool IS_V>
 __device__ __forceinline__ bool stage_any(const PrefillArgs& a, const Source& s, const Span& span, const int* pages,
                                           int t0, uint16_t* dst, int tid) {
   switch (s.fmt) {
-    case INT8: return stage_tile<D, INT8, false, IS_V>(a, s, span, pages, t0, dst, tid);
-    case E4M3: return stage_tile<D, E4M3, false, IS_V>(a, s, span, pages, t0, dst, tid);
+    case INT8:
+    case INT8B: return stage_tile<D, INT8, false, IS_V>(a, s, span, pages, t0, dst, tid);
+    case E4M3:
+    case E4M3B: return stage_tile<D, E4M3, false, IS_V>(a, s, span, pages, t0, dst, tid);
     case E5M2: return stage_tile<D, E5M2, false, IS_V>(a, s, span, pages, t0, dst, tid);
-    case INT8B: return stage_tile<D, INT8B, false, IS_V>(a, s, span, pages, t0, dst, tid);
-    case E4M3B: return stage_tile<D, E4M3B, false, IS_V>(a, s, span, pages, t0, dst, tid);
     case INT4A:
       return s.fields == 3 ? stage_tile<D, INT4A, true, IS_V>(a, s, span, pages, t0, dst, tid)
                            : stage_tile<D, INT4A, false, IS_V>(a, s, span, pages, t0, dst, tid);
@@ -1420,8 +1536,24 @@ __global__ void __launch_bounds__(2 * kProducers) stage_kernel(const __grid_cons
   const Source s = is_v ? make_source(a.v_cache, a.v_meta, a.v_fmt, a.kvarn, D, a.num_kv_heads, h, bs, is_block(a.v_fmt))
                         : make_source(a.k_cache, a.k_meta, a.k_fmt, a.kvarn, D, a.num_kv_heads, h, bs, is_block(a.k_fmt));
   uint16_t* dst = a.staged + row * D;
-  const bool bad = is_v ? stage_any<D, true>(a, s, span, pages, t0, dst, tid & 127)
-                        : stage_any<D, false>(a, s, span, pages, t0, dst, tid & 127);
+  bool bad = is_v ? stage_any<D, true>(a, s, span, pages, t0, dst, tid & 127)
+                  : stage_any<D, false>(a, s, span, pages, t0, dst, tid & 127);
+  if (is_block(s.fmt) && (tid & 127) < kGroups) {  // the tile's scales, as the softmax takes them
+    const int g = tid & 127;
+    const float x = group_needed(a, span, t0 + 8 * g)
+                        ? reinterpret_cast<const float*>(s.meta)[static_cast<size_t>(pages[(8 * g) >> a.block_shift]) * s.meta_page]
+                        : 0.f;
+    float* const to = a.staged_scales + (seq_head * tiles + tile) * (3 * kGroups) + g;
+    bool odd;
+    if (is_v) {
+      const float v = value_scale(x, odd);
+      to[kGroups] = v;
+      to[2 * kGroups] = __log2f(fabsf(v));
+    } else {
+      to[0] = key_scale(a.sm_scale_log2 == 0.f ? 1.f : fabsf(a.sm_scale_log2), x, odd);
+    }
+    bad |= odd;
+  }
   const int any = __syncthreads_or(bad);
   if (tid == 0) a.staged_bad[seq_head * tiles + tile] = any != 0;
 }
@@ -1523,8 +1655,9 @@ cudaError_t launch_rows(const PrefillArgs& a, cudaStream_t st) {
 }
 template <int D>
 cudaError_t launch_d(const PrefillArgs& a, cudaStream_t st) {
-  if (a.staged != nullptr) return launch_t<D, 256, true, false>(a, st);
-  return is_block(a.v_fmt) ? launch_rows<D, true>(a, st) : launch_rows<D, false>(a, st);
+  const bool block = is_block(a.v_fmt);
+  if (a.staged != nullptr) return block ? launch_t<D, 256, true, true>(a, st) : launch_t<D, 256, true, false>(a, st);
+  return block ? launch_rows<D, true>(a, st) : launch_rows<D, false>(a, st);
 }
 
 }  // namespace
