@@ -150,7 +150,8 @@ typedef struct {
  *          it >= need (old 0: need), and for k > 0 the codes in front become code * 2^-k,
  *          rounded to nearest even (e4m3: exact above its subnormals).  Codes are
  *          those of INT8 / E4M3 with inv = 1.0f / scale (0 for scale 0): an infinity
- *          becomes the largest code, a NaN 0 or E4M3's NaN.  Rows behind them keep
+ *          becomes the largest code (with scale 0 it counts as a NaN), a NaN 0 or E4M3's
+ *          NaN.  Rows behind them keep
  *          their codes, under the new scale.  Tokens of one page further apart in a
  *          call, or two that name one slot: which of them set a scale or land is
  *          unspecified, in that page.

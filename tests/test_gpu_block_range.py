@@ -202,3 +202,22 @@ def test_a_wait_of_the_chunks_that_runs_out(form, tile):
     assert found & kvq.DEVERR_TIMEOUT
     out, found = call()
     assert found == 0 and torch.equal(out, ref)
+
+
+# ---- store
+@pytest.mark.parametrize("pair", ["int8", "e4m3"])
+def test_an_infinity_among_zeros(pair):
+    """A page without a scale has no code for an infinity: 0, or e4m3's NaN, as for a NaN; behind rows
+    that gave the page a scale it is the largest code."""
+    p = Blocked(pair, [16, 16], 1, 64, 16)
+    x = torch.zeros((4, 1, 64), dtype=torch.bfloat16, device=DEV)
+    x[1, 0, :3] = torch.tensor([float("inf"), float("-inf"), float("nan")])
+    p.store(x, x, p.slots(0, np.arange(4)))
+    ones = torch.ones_like(x)
+    p.store(ones, ones, p.slots(1, np.arange(4)))
+    p.store(x, x, p.slots(1, np.arange(4, 8)))
+    p.same()
+    nan, most, least = (0, 127, 128) if pair == "int8" else (0x7F, 0x7E, 0xFE)
+    for codes, scales in ((p.cache.k_cache, p.cache.k_meta), (p.cache.v_cache, p.cache.v_meta)):
+        assert scales[p.table[0, 0], 0] == 0 and (codes[p.table[0, 0], 1, 0, :3].int() & 0x7F).tolist() == [nan] * 3
+        assert codes[p.table[1, 0], 5, 0, :2].tolist() == [most, least]
