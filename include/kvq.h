@@ -678,6 +678,9 @@ kvq_status kvq_read_cache(const kvq_cache_desc* cache, const void* k_cache, cons
 #define KVQ_DEVERR_TOKENS 256u      /* more new tokens than a call has room for, or query
                                        offsets that do not fit it */
 #define KVQ_DEVERR_POSITION 512u    /* a position outside the rotation table */
+#define KVQ_DEVERR_SHARED_WINDOW 1024u /* the decode of block formats found its shared memory
+                                       not 1,024-byte aligned, as it was declared to be: the
+                                       launch computed nothing */
 
 /*
  * kvq_debug_arm_wait_timeout -- test hook for the bounded pipeline waits of the

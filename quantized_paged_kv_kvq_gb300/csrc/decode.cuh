@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
   const uint32_t base_s = (raw_s + 1023u) & ~1023u;  // the window is padded by 1 KB
   uint8_t* smem = smem_raw + (base_s - raw_s);
   if (C::BLOCK && base_s != raw_s) {  // there is no room to align by: nothing is computed
-    if (threadIdx.x == 0) raise_error(16u);
+    if (threadIdx.x == 0) raise_error(1024u);  // KVQ_DEVERR_SHARED_WINDOW
     return;
   }
 

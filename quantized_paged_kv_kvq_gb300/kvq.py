@@ -35,6 +35,7 @@ DEVERR_QUERY_RANGE = 64
 DEVERR_FREE_BLOCKS = 128
 DEVERR_TOKENS = 256
 DEVERR_POSITION = 512
+DEVERR_SHARED_WINDOW = 1024
 ROPE_KIND = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 
