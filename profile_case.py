@@ -7,10 +7,10 @@ too large for a multi-pass capture):
 
 Arguments after the workload name override its generator settings (integers).
 
-  python profile_case.py operators prefill_long
+  python profile_case.py operators prefill_long repeats=5
 
 runs a case of perf/operators.py instead (`more_operators`: of perf/more_operators.py),
-through the library's calls.
+through the library's calls; repeats (3 if not given) is all it takes.
 Everything goes through the library's public calls; nothing is checked here.
 """
 from __future__ import annotations
@@ -79,14 +79,12 @@ def run_operator(module: str, name: str, repeats: int = 3) -> None:
 
 def main(argv=None) -> None:
     argv = sys.argv[1:] if argv is None else argv
-    if argv[0] in ("operators", "more_operators"):
-        run_operator(*argv)
-        return
+    words = 2 if argv[0] in ("operators", "more_operators") else 1
     kw = {}
-    for a in argv[1:]:
+    for a in argv[words:]:
         k, v = a.split("=", 1)
         kw[k] = int(v)
-    run(argv[0], **kw)
+    (run if words == 1 else run_operator)(*argv[:words], **kw)
 
 
 if __name__ == "__main__":
