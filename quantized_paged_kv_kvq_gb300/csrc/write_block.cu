@@ -19,7 +19,8 @@
 // share a CTA.  A CTA looks for the runs that begin among its `step` tokens by
 // comparing each token's page with that of the token before it, so the slots alone say
 // where runs begin and end: no search over sequences, no atomics.  step grows with the
-// call from 1 (a decode step: every request's run starts at once) to a page.  A thread a
+// call from 1 (a decode step: every request's run starts at once) to a page, at least 32
+// tokens (so of small pages a CTA stores several runs, one after the other).  A thread a
 // token, the CTA loads the places of the tokens around its own and marks, a bit each, which
 // are there, begin a run or follow on the offset before: the warps then only read bits.
 // Bound by HBM: 4 D bytes read and 2 D written per token and head (16,384 tokens, 8 heads of
@@ -42,6 +43,8 @@ constexpr int kWarps = 8;
 constexpr float kSmallest = 1.17549435e-38f;  // 2^-126: 1 / scale stays finite
 
 constexpr int kBack = 32;  // tokens before its own whose places a CTA keeps, too
+// Tokens of a CTA at most, pages having 16 CH (or 8) of them.
+constexpr int most_tokens(int ch) { return 16 * ch > 32 ? 16 * ch : 32; }
 
 __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
 
@@ -89,6 +92,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4) write_block_ker
   constexpr int LPR = RowGeom<D>::LPR, RPI = RowGeom<D>::RPI, NP = 16 / RPI;
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int kNear = (CH <= 2 ? 1 : 2) * kWarps * 32;  // tokens whose places the CTA keeps
+  static_assert(kBack + most_tokens(CH) <= kNear, "its own tokens' among them");
   __shared__ uint32_t most[2][kWarps];
   __shared__ int front[2][kWarps];
   __shared__ uint32_t is_there[kNear / 32], begins[kNear / 32], goes_on[kNear / 32];
@@ -334,7 +338,7 @@ template <int D, int CH>
 cudaError_t launch_t(const WriteArgs& a, const AppendSlots& s, int kf, int vf, cudaStream_t st, int num_sms) {
   const int y = (2 * a.num_kv_heads * CH + kWarps - 1) / kWarps;
   if (y > 65535) return cudaErrorNotSupported;
-  const int64_t step = std::min<int64_t>(std::max<int64_t>(a.num_tokens * y / (6 * num_sms), 1), std::max(a.block_size, 32));
+  const int64_t step = std::min<int64_t>(std::max<int64_t>(a.num_tokens * y / (6 * num_sms), 1), most_tokens(CH));
   const dim3 grid(static_cast<unsigned>((a.num_tokens + step - 1) / step), y, 1);
   write_block_kernel<D, CH><<<grid, kWarps * 32, 0, st>>>(a, s, kf, vf, static_cast<int>(step));
   return cudaGetLastError();
