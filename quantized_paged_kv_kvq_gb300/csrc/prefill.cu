@@ -79,8 +79,9 @@ constexpr float kLift = 7.0f;
 constexpr float kBlockLift = 9.0f, kBlockRaise = 15.0f;
 constexpr float kBlockMost = 100.0f;
 // Scales of a tile, one of each for 8 keys: of the scores (sm_scale and log2(e) with it), of the
-// values, and those' log2.  A ring of kScaleSlots tiles: slots are written up to four tiles
-// ahead of the products and read until a tile's softmax is done, up to two behind them.
+// values, and those' log2.  A ring of kScaleSlots tiles: a slot is written up to four tiles
+// ahead of the score products that are done and read until the tile's softmax is, at most two
+// behind them, so that six are in use.
 constexpr int kGroups = kKeys / 8, kScaleBytes = 3 * kGroups * 4, kScaleSlots = 8;
 
 // head_dim, rows, keys dequantized ahead, block formats

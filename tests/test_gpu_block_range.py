@@ -221,3 +221,13 @@ def test_an_infinity_among_zeros(pair):
     for codes, scales in ((p.cache.k_cache, p.cache.k_meta), (p.cache.v_cache, p.cache.v_meta)):
         assert scales[p.table[0, 0], 0] == 0 and (codes[p.table[0, 0], 1, 0, :3].int() & 0x7F).tolist() == [nan] * 3
         assert codes[p.table[1, 0], 5, 0, :2].tolist() == [most, least]
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("sm", [-0.125, 0.0, 1.0])
+def test_chunks_of_any_sm_scale(form, sm):
+    lens, counts, g = FORMS[form]
+    p = Blocked("int8_e4m3", lens, 2, 64, 32)
+    p.fill()
+    got, ref, tol = chunks(p, counts, g, sm)
+    assert np.isfinite(got).all() and (np.abs(got - ref) <= tol).all()
