@@ -436,7 +436,7 @@ kvq_status check_classes(const kvq_cache_desc* classes, int32_t num_classes,
   if (classes == nullptr || k_caches == nullptr || v_caches == nullptr || seq_class == nullptr)
     return KVQ_ERR_INVALID_ARGUMENT;
   if (num_classes < 1 || num_classes > kMaxPageClasses) return KVQ_ERR_UNSUPPORTED;
-  if (is_block(classes[0].k_fmt)) return KVQ_ERR_UNSUPPORTED;  // one pool: a scale belongs to a page
+  if (is_block(classes[0].k_fmt)) return KVQ_ERR_UNSUPPORTED;  // no such instances: page scales of class 0 only
   const kvq_cache_desc& c0 = classes[0];
   for (int c = 0; c < num_classes; ++c) {
     const kvq_cache_desc& x = classes[c];

@@ -125,7 +125,7 @@ cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
 
   auto kern_one = decode_partition_kernel<D, KF, VF, KVARN, kPagesOne>;
   auto kern_split = decode_partition_kernel<D, KF, VF, KVARN, kPages8>;
-  // block formats: one pool only (kern_mixed is not used)
+  // block formats: one pool only, no instance loads another class's scales (kern_mixed is not used)
   auto kern_mixed = decode_partition_kernel<D, KF, VF, KVARN, C::BLOCK ? kPagesOne : kPagesMixed>;
   if (C::BLOCK && a.seq_class != nullptr) return cudaErrorNotSupported;
   auto kern_window = decode_partition_kernel<D, KF, VF, KVARN, kPagesWindow>;

@@ -28,8 +28,9 @@
 // scores looks for maxima, only a step that has gone wrong is made again.
 //
 // Bound by the tensor cores for long prompts of 128-wide heads: 16,384 tokens, 64 / 8 heads
-// 2,730 us, 1,610 TFLOP/s, against 2,620 with the softmax left out; a pass for maxima
-// and two warps a row took 2,910.  Heads of 64 have half the products per exponential and
+// 2,730 to 2,970 us, 1,480 to 1,610 TFLOP/s, as the power limit allows (2,895 in most
+// runs), against 2,620 with the softmax left out (its best run); a pass for maxima and two
+// warps a row took 2,910 where this took 2,730.  Heads of 64 have half the products per exponential and
 // are bound by the softmax, whose two warps per scheduler do not hide all of their
 // latency: 0.63 us per half and 128 keys, where the products take 0.35.
 #include <algorithm>

@@ -18,6 +18,8 @@
 // and butterflies within a thread the rest: no value goes from lane to lane.  Codes
 // enter as 1024 + code, whose part 1024 D comes off element 0.  131,072 tokens, 8 heads of
 // 128, int4 K and uint8 V: 160 us, 4.7 TB/s; with a row over 16 lanes and shuffles 254.
+// Bound by loads in flight: a third of the warps that fit, and only a row's slot is loaded a
+// turn ahead, its codes and fields are waited for (5.5 stalls an issue).
 #include <algorithm>
 
 #include "kvq_device.cuh"
