@@ -593,6 +593,11 @@ __device__ __forceinline__ long long slot_index(const DecodeArgs& a, long long W
 // Block formats, whose values may lie anywhere in float32's range: the slot's pair is
 // (m + log2 l, f), f the power of two that the normalised output was divided by to
 // bring its largest element into [1, 2).
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float slot_factor(float largest) {
   const int e = (__float_as_int(largest) >> 23) - 127;  // largest >= 0
   return __int_as_float((min(max(e, -126), 126) + 127) << 23);
@@ -648,16 +653,11 @@ __device__ __forceinline__ void merge_slots(const DecodeArgs& a, int s, const Se
         }
         float bm = ml[0][0];
 #pragma unroll
-        for (int u = 1; u < PU; ++u) bm = fmaxf(bm, ml[u][0]);
+        for (int u = 1; u < PU; ++u) bm = max_or_nan(bm, ml[u][0]);
         // no slot in this batch (empty ranges; more ranges than tiles): nothing to
-        // add, and 2^(m - M) would be 2^(-inf + inf) while M is still -inf.  A slot whose
-        // (m, l) holds a NaN is one, although the largest m does not show it.
-        if (bm == -INFINITY) {
-          float met = 0.f;
-#pragma unroll
-          for (int u = 0; u < PU; ++u) met += ml[u][0] + ml[u][1];
-          if (met == -INFINITY) continue;
-        }
+        // add, and 2^(m - M) would be 2^(-inf + inf) while M is still -inf.  (A slot whose
+        // sum is NaN has such an m, too: it is one, and makes the result NaN.)
+        if (bm == -INFINITY) continue;
         if (bm > M) {  // raise the running maximum, rescaling what was summed so far
           const float sc = fast_exp2(M - bm);
           Lsum *= sc;
@@ -699,6 +699,8 @@ __device__ __forceinline__ void merge_slots(const DecodeArgs& a, int s, const Se
         for (int e = 0; e < DL; ++e) acc[e] *= by;
         M += __log2f(Lsum);
         Lsum = f;
+      } else {
+        M += Lsum - Lsum;  // NaN with a sum that is not finite
       }
       if (act) {
         const long long sl = dst * rows + warp * G + nn;
@@ -1630,6 +1632,9 @@ __global__ void __launch_bounds__(kHeadsPerCta * 32, (KF == BF16) ? 1 : 2)
       m1 += __log2f(L1);
       L0 = f0;
       L1 = f1;
+    } else {  // NaN with a sum that is not finite (keys that are not numbers alone leave m at -inf)
+      m0 += L0 - L0;
+      m1 += L1 - L1;
     }
     const size_t slot = ((static_cast<size_t>(k) * HG + hg) * 2 + j) * (hpc * G) + warp * G;
     if (2 * c < G) store_f16_run<E>(a.ws_acc + (slot + 2 * c) * D + g * E, Oa);
