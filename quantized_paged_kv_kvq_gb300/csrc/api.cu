@@ -251,8 +251,8 @@ struct PrefillShape {
 // Measured ahead / not, 32 / 8 heads of 128: int8, 8 x 4,096 keys: 4 row tiles 160 /
 // 138 us, 8 257 / 257, 1 x 8,192 keys and 32 tiles 193 / 217; KVarN, 16 x 4,096 keys:
 // 2 tiles 223 / 222, 8 x 4,096: 4 tiles 182 / 210, 8 289 / 389; int4 4 tiles 165 / 177;
-// bf16 as int8; int8 per page, 8 x 4,096: 4 tiles 168 / 142, 6 221 / 207, 8 272 / 269,
-// 32 x 2,048: 6 431 / 412, 8 521 / 519, 1 x 8,192 keys and 32 tiles 205 / 229.
+// bf16 as int8; int8 per page, 8 x 4,096: 4 tiles 168 / 142, 6 221 / 206, 8 270 / 266,
+// 32 x 2,048: 6 429 / 411, 8 518 / 518, 1 x 8,192 keys and 32 tiles 203 / 227.
 constexpr int64_t stage_tiles(int fmt) { return is_asym(fmt) ? 3 : 8; }
 constexpr int64_t kStageBytes = 16ll << 30;
 // Bytes of a tile of 128 keys' scales behind them: three float32 for every 8 (block formats).
