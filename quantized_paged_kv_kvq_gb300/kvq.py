@@ -315,7 +315,7 @@ def kvq_decode_append(cache: KVCache, new_key: torch.Tensor, new_value: torch.Te
                       context_lens: torch.Tensor, max_context_len: int, sm_scale: float,
                       workspace: Optional[torch.Tensor] = None, num_ctas: int = 0,
                       stream=None) -> torch.Tensor:
-    """One decode step in one launch: row s of new_key / new_value (bf16 [S, Hkv, D],
+    """One decode step in one launch (block formats: two): row s of new_key / new_value (bf16 [S, Hkv, D],
     sequence stride free) is quantized into the cache at position context_lens[s] - 1,
     then out = the paged decode over the context including it."""
     lib = load_library()
