@@ -216,7 +216,8 @@ kvq_status kvq_decode_workspace_size(const kvq_cache_desc* cache, int32_t num_se
  *   2^-25 of the largest as 0 (symmetric formats: 4,096 such keys weigh 1.2e-4); of
  *   asymmetric and block formats times the row's or page's scale, by a power of two that keeps
  *   the product in range whatever the scale is (a page's: from 2^-100 to 2^100; keys that
- *   weigh less than 2^-34 of the largest probability times scale do not count).
+ *   weigh less than 2^-34 of the largest probability times scale do not count).  A part of
+ *   a sequence's result is rounded to fp16 (block formats: 2^-25 of its largest element).
  */
 kvq_status kvq_paged_decode(const kvq_cache_desc* cache, const void* k_cache,
                             const void* v_cache, void* out, const void* query,
